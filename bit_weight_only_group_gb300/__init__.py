@@ -14,6 +14,10 @@ Entry points (same names as the C ABI):
 * ``qgemm_moe_grouped(x, topk_ids, experts)`` -> y [T, k, N]
 * ``qgemm_moe_grouped_multi(x, topk_ids, [experts_0, experts_1])`` -> [y_0, y_1]
   (products sharing one routing, e.g. an MoE layer's gate and up)
+* ``qkv_append(cache, batch, k, v, q=, rope=)`` -> q turned; k (turned) and v
+  written to the pages of a :class:`KVCache`
+* ``qattn_forward(q, cache, batch)`` -> attention over a shared prefix and each
+  sequence's own cached tokens (:class:`KVBatch`)
 """
 from __future__ import annotations
 
@@ -41,7 +45,8 @@ ABI_FUNCTIONS = ("qpack_query_sizes", "qpack_workspace_size", "qpack_quantize", 
                  "qgemm_device_status", "qgemm_selftest_bounded_wait", "qdiag_workspace_size", "qdiag_layer",
                  "qgemm_w8a8_workspace_size", "qgemm_forward_w8a8",
                  "qrepack_tiles_size", "qrepack_tiles", "qgemm_tiles_workspace_size", "qgemm_forward_tiles",
-                 "qgemm_set_dependent_launch", "qgemm_last_error")
+                 "qgemm_set_dependent_launch", "qkv_append", "qattn_workspace_size", "qattn_forward",
+                 "qgemm_last_error")
 
 
 class QgError(RuntimeError):
@@ -59,6 +64,28 @@ class QgQWeight(ctypes.Structure):
                 ("out_val", ctypes.c_void_p), ("scale8", ctypes.c_void_p), ("scale8_exp", ctypes.c_void_p),
                 ("fb_row_ptr", ctypes.c_void_p), ("fb_col", ctypes.c_void_p), ("fb_val", ctypes.c_void_p),
                 ("fb_cap", ctypes.c_int32)]
+
+
+class QgKvCache(ctypes.Structure):
+    """Mirror of ``qg_kv_cache`` in include/qgemm.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("heads_kv", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class QgKvBatch(ctypes.Structure):
+    """Mirror of ``qg_kv_batch`` in include/qgemm.h."""
+    _fields_ = [("sequences", ctypes.c_int32), ("tokens", ctypes.c_int32), ("max_q", ctypes.c_int32),
+                ("max_kv", ctypes.c_int32), ("table_ld", ctypes.c_int32), ("prefix_len", ctypes.c_int32),
+                ("table", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("cu_q", ctypes.c_void_p),
+                ("prefix_table", ctypes.c_void_p)]
+
+
+class QgRope(ctypes.Structure):
+    """Mirror of ``qg_rope`` in include/qgemm.h."""
+    _fields_ = [("table", ctypes.c_void_p), ("at", ctypes.c_void_p), ("positions", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
 _lib = None
@@ -96,6 +123,11 @@ def lib() -> ctypes.CDLL:
         L.qgemm_forward_w8a8.argtypes = [vp, i32, i32, pq, vp, i32, ctypes.c_int, vp, sz, vp]
         L.qdiag_layer.argtypes = [vp, pq, f32, vp, vp, vp, sz, vp]
         L.qgemm_forward_multi.argtypes = [vp, i32, i32, pq, i32, ctypes.POINTER(vp), pi32, ctypes.c_int, vp, sz, vp]
+        i64, pc, pb = ctypes.c_int64, ctypes.POINTER(QgKvCache), ctypes.POINTER(QgKvBatch)
+        L.qkv_append.argtypes = [pc, pb, ctypes.POINTER(QgRope), vp, i64, i32, vp, i64, vp, i64, ctypes.c_int, vp, i64,
+                                 vp]
+        L.qattn_workspace_size.argtypes = [pc, pb, i32, psz]
+        L.qattn_forward.argtypes = [pc, pb, vp, i64, i32, f32, vp, i64, ctypes.c_int, vp, vp, sz, vp]
         for name in ABI_FUNCTIONS[:-1]:
             getattr(L, name).restype = ctypes.c_int
         L.qgemm_last_error.argtypes = []
@@ -473,4 +505,160 @@ def qgemm_forward_tiles(x: torch.Tensor, qw: QWeight, tiles: torch.Tensor, out: 
     _check(lib().qgemm_forward_tiles(_ptr(x), M, x.stride(0), ctypes.byref(d), _ptr(tiles), _ptr(out), out.stride(0),
                                      yt, _ptr(workspace) if b.value else None, workspace.numel() if b.value else 0,
                                      _stream(stream)), "qgemm_forward_tiles")
+    return out
+
+
+# --------------------------------------------------------------------- paged cache
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}   # qg_dtype
+
+
+class KVCache:
+    """Pages of cached keys and values: k and v [num_pages, page_size, heads_kv,
+    head_dim] (bf16 or fp16, CUDA) with one set of strides, in any order with
+    the head's values contiguous."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+            raise ValueError("k and v must be 4-D with the same shape, strides and dtype")
+        if k.dtype not in (torch.bfloat16, torch.float16) or not k.is_cuda or not v.is_cuda or k.stride(3) != 1:
+            raise ValueError("k and v must be bfloat16 or float16 CUDA tensors with unit inner stride")
+        self.k, self.v, self.dtype = k, v, k.dtype
+        self.num_pages, self.page_size, self.heads_kv, self.head_dim = k.shape
+        self._desc = QgKvCache(k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype], *k.shape, *k.stride()[:3])
+        self._ref = ctypes.byref(self._desc)
+
+    @staticmethod
+    def empty(num_pages: int, page_size: int, heads_kv: int, head_dim: int, dtype: torch.dtype = torch.bfloat16,
+              device="cuda") -> "KVCache":
+        """Pages with heads first: a head's rows of a page are one contiguous run."""
+        k, v = (torch.empty((num_pages, heads_kv, page_size, head_dim), dtype=dtype, device=device).transpose(1, 2)
+                for _ in range(2))
+        return KVCache(k, v)
+
+
+class KVBatch:
+    """Sequences over one cache (``qg_kv_batch``): own pages table [B, width]
+    and own lengths kv_len [B] (new tokens counted), new tokens per sequence
+    cu_q [B + 1] (None: one each), all int32 on the device and read when the
+    kernels run; pages and length of the prefix they share; and host bounds
+    max_kv (own tokens), max_q (new tokens) and tokens (rows of q/k/v;
+    default B, one each)."""
+
+    def __init__(self, table: torch.Tensor | None, kv_len: torch.Tensor, max_kv: int, cu_q: torch.Tensor | None = None,
+                 max_q: int = 1, tokens: int | None = None, prefix_table: torch.Tensor | None = None,
+                 prefix_len: int = 0):
+        B = kv_len.numel()
+        for name, t, n in (("kv_len", kv_len, B), ("cu_q", cu_q, B + 1), ("prefix_table", prefix_table, None)):
+            if t is None:
+                continue
+            if t.dtype != torch.int32 or not t.is_cuda or t.dim() != 1 or (t.numel() > 1 and t.stride(0) != 1):
+                raise ValueError(f"{name} must be a contiguous 1-D int32 CUDA tensor")
+            if n is not None and t.numel() != n:
+                raise ValueError(f"{name} must have {n} entries")
+        if table is not None:
+            if table.dtype != torch.int32 or not table.is_cuda or table.dim() != 2 or table.shape[0] != B or \
+                    (table.shape[1] > 1 and table.stride(1) != 1):
+                raise ValueError("table must be an int32 CUDA tensor [B, width] with unit inner stride")
+        if cu_q is None and tokens not in (None, B):
+            raise ValueError("without cu_q every sequence has one new token")
+        if cu_q is not None and tokens is None:
+            raise ValueError("tokens (rows of q, k and v) is needed with cu_q")
+        self.table, self.kv_len, self.cu_q, self.prefix_table = table, kv_len, cu_q, prefix_table
+        self.sequences, self.tokens, self.max_q, self.max_kv = B, B if tokens is None else tokens, max_q, max_kv
+        self.prefix_len = prefix_len
+        self._width = 0 if table is None else table.shape[1]
+        self._shared = 0 if prefix_table is None else prefix_table.numel()
+        ld = 0 if table is None else (table.stride(0) if B > 1 else table.shape[1])
+        if ld < self._width:
+            raise ValueError("rows of table must not overlap")
+        self._desc = QgKvBatch(B, self.tokens, max_q, max_kv, ld, prefix_len, _ptr(table), _ptr(kv_len), _ptr(cu_q),
+                               _ptr(prefix_table))
+        self._ref = ctypes.byref(self._desc)
+
+    def check(self, cache: KVCache):
+        """The tables hold an entry for every page the bounds reach."""
+        if self._width * cache.page_size < self.max_kv:
+            raise ValueError(f"table width {self._width} holds fewer than max_kv={self.max_kv} tokens")
+        if self._shared * cache.page_size < self.prefix_len:
+            raise ValueError(f"prefix_table of {self._shared} pages holds fewer than prefix_len={self.prefix_len} tokens")
+
+
+def _rows(t: torch.Tensor, name: str, T: int, heads: int | None, dim: int):
+    """A CUDA array [T, heads, dim] whose heads are contiguous: its token stride."""
+    if not t.is_cuda or t.dim() != 3 or t.shape[0] != T or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be a CUDA tensor [{T}, {'heads' if heads is None else heads}, {dim}]")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != dim):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return t.stride(0) if T > 1 else t.shape[1] * dim
+
+
+def qkv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, q: torch.Tensor | None = None,
+               rope: torch.Tensor | None = None, positions: torch.Tensor | None = None, interleaved: bool = False,
+               q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """Write the batch's new tokens k and v [T, heads_kv, head_dim] (fp32,
+    bf16 or fp16) to their pages, k turned by its position; returns q [T,
+    heads_q, head_dim] turned, in the cache's type.  rope: fp32 [positions,
+    R], row p the R/2 cosines and then the R/2 sines of position p (None: no
+    rotation); positions: int32 [T] in place of the batch's own."""
+    T, D = batch.tokens, cache.head_dim
+    batch.check(cache)
+    ldk, ldv = _rows(k, "k", T, cache.heads_kv, D), _rows(v, "v", T, cache.heads_kv, D)
+    if k.dtype not in _DTYPES or v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+        raise ValueError("q, k and v must share one dtype (float32, bfloat16 or float16)")
+    heads_q = ldq = ldq_out = 0
+    if q is not None:
+        heads_q = q.shape[1]
+        ldq = _rows(q, "q", T, None, D)
+        if q_out is None:
+            q_out = torch.empty((T, heads_q, D), dtype=cache.dtype, device=q.device)
+        ldq_out = _rows(q_out, "q_out", T, heads_q, D)
+        if q_out.dtype != cache.dtype:
+            raise ValueError("q_out must have the cache's dtype")
+    turn = None
+    if rope is not None:
+        if rope.dtype != torch.float32 or not rope.is_cuda or rope.dim() != 2 or not rope.is_contiguous():
+            raise ValueError("rope must be a contiguous float32 CUDA tensor [positions, R]")
+        if positions is not None and (positions.dtype != torch.int32 or not positions.is_cuda or
+                                      positions.shape != (T,) or not positions.is_contiguous()):
+            raise ValueError(f"positions must be a contiguous int32 CUDA tensor [{T}]")
+        turn = ctypes.byref(QgRope(rope.data_ptr(), _ptr(positions), rope.shape[0], rope.shape[1], int(interleaved)))
+    _check(lib().qkv_append(cache._ref, batch._ref, turn, None if q is None else q.data_ptr(), ldq, heads_q,
+                            k.data_ptr(), ldk, v.data_ptr(), ldv, _DTYPES[k.dtype],
+                            None if q is None else q_out.data_ptr(), ldq_out, _stream(stream)), "qkv_append")
+    return q_out
+
+
+def qattn_workspace_size(cache: KVCache, batch: KVBatch, heads_q: int) -> int:
+    b = ctypes.c_size_t()
+    _check(lib().qattn_workspace_size(cache._ref, batch._ref, heads_q, ctypes.byref(b)), "qattn_workspace_size")
+    return b.value
+
+
+def qattn_forward(q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: float | None = None,
+                  out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                  lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """out [T, heads_q, head_dim] (default: of q's type): attention of the new
+    tokens q (of the cache's type) over the shared prefix and their own cached
+    tokens.  scale: 1 / sqrt(head_dim) by default; lse: fp32 [T, heads_q] to
+    receive the log of each row's sum of exponentials."""
+    T, D = batch.tokens, cache.head_dim
+    batch.check(cache)
+    if q.dtype != cache.dtype:
+        raise ValueError("q must have the cache's dtype")
+    ldq = _rows(q, "q", T, None, D)
+    heads_q = q.shape[1]
+    if out is None:
+        out = torch.empty((T, heads_q, D), dtype=out_dtype or q.dtype, device=q.device)
+    ldo = _rows(out, "out", T, heads_q, D)
+    if out.dtype not in _DTYPES:
+        raise ValueError("out must be float32, bfloat16 or float16")
+    if lse is not None and (lse.dtype != torch.float32 or not lse.is_cuda or lse.shape != (T, heads_q) or
+                            not lse.is_contiguous()):
+        raise ValueError(f"lse must be a contiguous float32 CUDA tensor [{T}, {heads_q}]")
+    if workspace is None:
+        need = qattn_workspace_size(cache, batch, heads_q)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    _check(lib().qattn_forward(cache._ref, batch._ref, q.data_ptr(), ldq, heads_q, D ** -0.5 if scale is None else scale,
+                               out.data_ptr(), ldo, _DTYPES[out.dtype], _ptr(lse), _ptr(workspace),
+                               0 if workspace is None else workspace.numel(), _stream(stream)), "qattn_forward")
     return out

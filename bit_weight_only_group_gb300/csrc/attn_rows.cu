@@ -1,0 +1,431 @@
+// Attention for few query rows per key/value head: a decoding step's own
+// tokens, 1 to 64 rows (tokens x query heads of one key/value head) a CTA.
+//
+// The keys are the bound: at R rows a key/value pair of 4 dim bytes takes
+// 4 R dim operations, below the tensor cores' rate for R up to a few hundred.
+// So K and V stream through shared memory once, by TMA (64 keys a stage, the
+// page's place looked up by one lane per box), and warp-level matrix
+// instructions (m16n8k16) do the products from there:
+//     S = Q K^T      Q in registers as the A operand, 16 rows a warp
+//     P = 2^(S scale_log2 - m), with the running maximum m and sum l
+//     O = O 2^(m_old - m) + P V
+// P goes from S's accumulator layout to the A operand's without leaving the
+// thread.  Four warps split a stage's keys among them and the rows in blocks
+// of 16 (RW row blocks x 4 / RW key ranges); each keeps m, l and O of its own
+// keys, and the CTA joins them at the end.
+#include <algorithm>
+
+#include "attn.cuh"
+
+namespace qg {
+namespace attn {
+namespace {
+
+constexpr int KT = 64;                       // keys of a stage
+constexpr int kWarps = 4;                    // consumer warps; warp 4 issues the loads
+constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kStages = 3;
+
+template <int D> struct Cfg {
+    static constexpr int TILE = KT * D * 2;              // bytes of a K or V tile: [dim / 64][key][64 values], swizzled
+    static constexpr int STAGE = 2 * TILE;
+    static constexpr int OFF_BAR = kStages * STAGE;
+    static constexpr int OFF_ML = OFF_BAR + 128;         // (m, l) of the joining warps' rows
+    static constexpr int SMEM = OFF_ML + kWarps * 16 * 8 + 1024;
+    // the joining buffers (2 slots of 16 x D fp32) lie over the stages
+    static_assert(2 * 16 * D * 4 <= kStages * STAGE, "joining buffers fit the stages");
+};
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (std::is_same<T, __half>::value)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+static_assert(kWarps * 32 == 128, "consumer_sync counts 128 threads");
+
+// What one CTA works on.
+struct Item {
+    int t0;             // the unit's first token; its row i is query head i % group of token t0 + i / group
+    int row0, rows;     // this CTA's rows of it
+    int b;              // sequence (own keys only)
+    int own0;           // own places token t sees: own0 + t - t0 (own keys only)
+    int own;            // own places any row sees
+    int prefix, np;     // prefix tokens and their tiles (0 without prefix keys)
+    int tile0, tile1;   // this part's tiles
+};
+
+template <int KEYS>
+__device__ __forceinline__ Item find_item(const Args& a, int unit, int row_block, int part, int tiles_per_part,
+                                          int rows_cap, bool tell)
+{
+    Item it;
+    it.b = unit;
+    int t0, t1;
+    bool ok = true;
+    if (KEYS & kOwn) {
+        kv::token_range(a.bt, unit, t0, t1);
+        ok = t1 - t0 <= a.bt.max_q;
+    } else {
+        t0 = 0;
+        t1 = kv::used_tokens(a.bt);
+    }
+    it.t0 = t0;
+    it.row0 = row_block * rows_cap;
+    it.rows = max(0, min(rows_cap, (t1 - t0) * a.group - it.row0));
+    it.own = it.own0 = 0;
+    if ((KEYS & kOwn) && it.rows > 0) {
+        int len;
+        ok = kv::own_length(a.bt, unit, len) && ok;
+        it.own0 = len - (t1 - t0) + 1;
+        it.own = max(0, it.own0 + (it.row0 + it.rows - 1) / a.group);
+    }
+    if (!ok && tell) kv::report(a.status);
+    it.prefix = (KEYS & kPrefix) ? a.bt.prefix_len : 0;
+    it.np = (it.prefix + KT - 1) / KT;
+    const int tiles = it.rows > 0 ? it.np + (it.own + KT - 1) / KT : 0;
+    it.tile0 = min(part * tiles_per_part, tiles);
+    it.tile1 = min(it.tile0 + tiles_per_part, tiles);
+    return it;
+}
+
+template <typename T, int D, int RW, int KEYS>
+__global__ void __launch_bounds__(kThreads)
+    k_attn_rows(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                const __grid_constant__ Args a, int part0, int parts, int tiles_per_part, int row_blocks)
+{
+    using C = Cfg<D>;
+    constexpr int KW = kWarps / RW, NK = KT / KW, HALVES = D / 64;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sbase = ptx::smem_u32(smem), bars = sbase + C::OFF_BAR;
+    auto full = [&](int s) { return bars + 8 * s; };
+    auto empty = [&](int s) { return bars + 8 * (kStages + s); };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    // neighbouring CTAs take the heads of one unit (their rows of a page lie together when tokens come first)
+    int x = blockIdx.x;
+    const int head = x % a.c.heads;
+    x /= a.c.heads;
+    const int part = x % parts;
+    x /= parts;
+    const int row_block = x % row_blocks, unit = x / row_blocks;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; s++) { ptx::mbar_init(full(s), 1); ptx::mbar_init(empty(s), kWarps); }
+        ptx::fence_mbar_init();
+    }
+    if (warp == kWarps && lane == 0) { ptx::prefetch_tensormap(&kmap); ptx::prefetch_tensormap(&vmap); }
+    __syncthreads();
+    kv::pdl_wait();
+    kv::pdl_release();
+    const Item it = find_item<KEYS>(a, unit, row_block, part, tiles_per_part, 16 * RW, threadIdx.x == 0);
+    if (it.rows == 0) return;
+    bool ok = true;
+    // keys of tile j that any row sees
+    auto tile_keys = [&](int j) { return j < it.np ? min(KT, it.prefix - j * KT) : min(KT, it.own - (j - it.np) * KT); };
+
+    if (warp == kWarps) {
+        // ------------------------------------------------ loads: one lane per box
+        const int boxes = KT / a.box_rows;                       // key ranges of a tile, each a page's rows
+        const int mine = lane % boxes, what = lane / boxes;      // what: 64-value half and K or V
+        const bool busy = what < 2 * HALVES;
+        const int half = what % HALVES, is_v = what / HALVES;
+        const int* own_table = (KEYS & kOwn) ? a.bt.table + (long long)it.b * a.bt.table_ld : nullptr;
+        const int n_prefix = (it.prefix + (1 << a.c.page_shift) - 1) >> a.c.page_shift;
+        auto page_at = [&](int j) -> int {   // page of this lane's box of tile j
+            if (!busy || j >= it.tile1 || mine * a.box_rows >= tile_keys(j)) return 0;
+            const int key = (j < it.np ? j : j - it.np) * KT + mine * a.box_rows;
+            return j < it.np ? page_of(a, a.bt.prefix_table, n_prefix, key >> a.c.page_shift)
+                             : page_of(a, own_table, a.bt.table_ld, key >> a.c.page_shift);
+        };
+        int s = 0;
+        uint32_t ph = 0;
+        int page = page_at(it.tile0);
+        for (int j = it.tile0; j < it.tile1; j++) {
+            const int next = page_at(j + 1);
+            ok = __all_sync(0xffffffffu, ptx::mbar_wait(empty(s), ph ^ 1u));
+            if (!ok) break;
+            const int used = (tile_keys(j) + a.box_rows - 1) / a.box_rows;
+            if (lane == 0) ptx::mbar_expect_tx(full(s), (uint32_t)(used * 2 * HALVES * a.box_rows * 128));
+            __syncwarp();
+            if (busy && mine < used) {
+                const int key = (j < it.np ? j : j - it.np) * KT + mine * a.box_rows;
+                const uint32_t dst = sbase + s * C::STAGE + is_v * C::TILE + half * (KT * 128) + mine * a.box_rows * 128;
+                tma_load_4d(dst, is_v ? &vmap : &kmap, half * 64, key & ((1 << a.c.page_shift) - 1), head, page, full(s));
+            }
+            page = next;
+            if (++s == kStages) { s = 0; ph ^= 1u; }
+        }
+    } else {
+        // ------------------------------------------------ products
+        const int rw = warp % RW, kw = warp / RW, k0 = kw * NK;
+        const int r0 = 16 * rw + lane / 4, r1 = r0 + 8;   // this thread's two rows
+        const int tok0 = it.t0 + (it.row0 + r0) / a.group, tok1 = it.t0 + (it.row0 + r1) / a.group;
+        const int hq0 = head * a.group + (it.row0 + r0) % a.group, hq1 = head * a.group + (it.row0 + r1) % a.group;
+        const bool in0 = r0 < it.rows, in1 = r1 < it.rows;
+        uint32_t qf[D / 16][4];
+        {
+            const uint32_t* q0 = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.q) + tok0 * a.ldq + (long long)hq0 * D) + lane % 4;
+            const uint32_t* q1 = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.q) + tok1 * a.ldq + (long long)hq1 * D) + lane % 4;
+#pragma unroll
+            for (int i = 0; i < D / 16; i++) {
+                qf[i][0] = in0 ? __ldg(q0 + 8 * i) : 0u;
+                qf[i][1] = in1 ? __ldg(q1 + 8 * i) : 0u;
+                qf[i][2] = in0 ? __ldg(q0 + 8 * i + 4) : 0u;
+                qf[i][3] = in1 ? __ldg(q1 + 8 * i + 4) : 0u;
+            }
+        }
+        float o[D / 8][4];
+#pragma unroll
+        for (int i = 0; i < D / 8; i++) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+        // shared-memory rows of the ldmatrix lanes
+        const int krow = (lane / 16) * 8 + lane % 8, kchunk = (lane / 8) % 2;
+        const int vrow = ((lane / 8) % 2) * 8 + lane % 8, vchunk = lane / 16;
+
+        int s = 0;
+        uint32_t ph = 0;
+        for (int j = it.tile0; j < it.tile1 && ok; j++) {
+            ok = __all_sync(0xffffffffu, ptx::mbar_wait(full(s), ph));
+            if (!ok) break;
+            const uint32_t kt = sbase + s * C::STAGE, vt = kt + C::TILE;
+            // keys k0 .. k0 + vis - 1 of the tile are seen by the row
+            int vis0 = tile_keys(j) - k0, vis1 = vis0;
+            const int any = vis0;   // ... by any row
+            if (j >= it.np) {
+                const int base = (j - it.np) * KT + k0;
+                vis0 = it.own0 + (tok0 - it.t0) - base;
+                vis1 = it.own0 + (tok1 - it.t0) - base;
+            }
+            if (any > 0) {
+                if (any < NK) {
+                    // V rows past the last key: whatever the page or an older tile left there times a
+                    // probability of 0 must be 0
+                    for (int i = lane; i < (NK - max(any, 0)) * HALVES * 8; i += 32) {
+                        const int row = k0 + any + i / (HALVES * 8), c = i % (HALVES * 8);
+                        *reinterpret_cast<uint4*>(smem + s * C::STAGE + C::TILE + (c / 8) * (KT * 128) + row * 128 + (c % 8) * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    ptx::fence_proxy_async();   // the slot's next TMA write comes after these
+                    __syncwarp();
+                }
+                float sc[NK / 8][4];
+#pragma unroll
+                for (int n = 0; n < NK / 8; n++) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < D / 16; i++) {
+#pragma unroll
+                    for (int n = 0; n < NK / 16; n++) {
+                        const int row = k0 + 16 * n + krow, ch = (2 * i + kchunk) % 8;
+                        uint32_t kf[4];
+                        ldsm4(kf, kt + (i / 4) * (KT * 128) + row * 128 + ((ch ^ (row & 7)) << 4));
+                        mma16816<T>(sc[2 * n], qf[i], kf[0], kf[1]);
+                        mma16816<T>(sc[2 * n + 1], qf[i], kf[2], kf[3]);
+                    }
+                }
+                if (!__all_sync(0xffffffffu, vis0 >= NK && vis1 >= NK)) {
+#pragma unroll
+                    for (int n = 0; n < NK / 8; n++) {
+                        const int c = 8 * n + 2 * (lane % 4);
+                        if (c >= vis0) sc[n][0] = -INFINITY;
+                        if (c + 1 >= vis0) sc[n][1] = -INFINITY;
+                        if (c >= vis1) sc[n][2] = -INFINITY;
+                        if (c + 1 >= vis1) sc[n][3] = -INFINITY;
+                    }
+                }
+                float t0 = sc[0][0], t1 = sc[0][2];
+#pragma unroll
+                for (int n = 0; n < NK / 8; n++) {
+                    t0 = fmaxf(t0, fmaxf(sc[n][0], sc[n][1]));
+                    t1 = fmaxf(t1, fmaxf(sc[n][2], sc[n][3]));
+                }
+                t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
+                t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
+                t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
+                t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
+                const float n0 = fmaxf(m0, t0 * a.scale_log2), n1 = fmaxf(m1, t1 * a.scale_log2);
+                // a row that has seen nothing yet has m = -inf: subtract 0 instead (all its terms are 2^-inf)
+                const float u0 = n0 == -INFINITY ? 0.0f : n0, u1 = n1 == -INFINITY ? 0.0f : n1;
+                if (!__all_sync(0xffffffffu, n0 == m0 && n1 == m1)) {
+                    const float f0 = exp2_approx(m0 - u0), f1 = exp2_approx(m1 - u1);
+                    l0 *= f0;
+                    l1 *= f1;
+#pragma unroll
+                    for (int i = 0; i < D / 8; i++) {
+                        o[i][0] *= f0; o[i][1] *= f0;
+                        o[i][2] *= f1; o[i][3] *= f1;
+                    }
+                    m0 = n0;
+                    m1 = n1;
+                }
+                uint32_t pf[NK / 16][4];
+#pragma unroll
+                for (int n = 0; n < NK / 8; n++) {
+                    const float p0 = exp2_approx(fmaf(sc[n][0], a.scale_log2, -u0));
+                    const float p1 = exp2_approx(fmaf(sc[n][1], a.scale_log2, -u0));
+                    const float p2 = exp2_approx(fmaf(sc[n][2], a.scale_log2, -u1));
+                    const float p3 = exp2_approx(fmaf(sc[n][3], a.scale_log2, -u1));
+                    l0 += p0 + p1;
+                    l1 += p2 + p3;
+                    pf[n / 2][2 * (n % 2)] = kv::pack2<T>(p0, p1);
+                    pf[n / 2][2 * (n % 2) + 1] = kv::pack2<T>(p2, p3);
+                }
+#pragma unroll
+                for (int n = 0; n < NK / 16; n++) {
+#pragma unroll
+                    for (int i = 0; i < D / 16; i++) {
+                        const int row = k0 + 16 * n + vrow, ch = (2 * i + vchunk) % 8;
+                        uint32_t vf[4];
+                        ldsm4t(vf, vt + (i / 4) * (KT * 128) + row * 128 + ((ch ^ (row & 7)) << 4));
+                        mma16816<T>(o[2 * i], pf[n], vf[0], vf[1]);
+                        mma16816<T>(o[2 * i + 1], pf[n], vf[2], vf[3]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(empty(s));
+            if (++s == kStages) { s = 0; ph ^= 1u; }
+        }
+        l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+        l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+
+        // ------------------------------------------------ join the key ranges: the upper half of the warps into the lower
+        float4* slots = reinterpret_cast<float4*>(smem);
+        float2* mls = reinterpret_cast<float2*>(smem + C::OFF_ML);
+#pragma unroll
+        for (int step = KW / 2; step > 0; step /= 2) {
+            consumer_sync();   // the stages, or the last step's slots, are no longer read
+            if (kw >= step && kw < 2 * step) {
+                const int slot = (kw - step) * RW + rw;
+#pragma unroll
+                for (int i = 0; i < D / 8; i++)
+                    slots[(slot * (D / 8) + i) * 32 + lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+                if (lane % 4 == 0) {
+                    mls[slot * 16 + lane / 4] = make_float2(m0, l0);
+                    mls[slot * 16 + lane / 4 + 8] = make_float2(m1, l1);
+                }
+            }
+            consumer_sync();
+            if (kw < step) {
+                const int slot = kw * RW + rw;
+                const float2 p0 = mls[slot * 16 + lane / 4], p1 = mls[slot * 16 + lane / 4 + 8];
+                const float n0 = fmaxf(m0, p0.x), n1 = fmaxf(m1, p1.x);
+                const float u0 = n0 == -INFINITY ? 0.0f : n0, u1 = n1 == -INFINITY ? 0.0f : n1;
+                const float f0 = exp2_approx(m0 - u0), f1 = exp2_approx(m1 - u1);
+                const float g0 = exp2_approx(p0.x - u0), g1 = exp2_approx(p1.x - u1);
+                l0 = l0 * f0 + p0.y * g0;
+                l1 = l1 * f1 + p1.y * g1;
+                m0 = n0;
+                m1 = n1;
+#pragma unroll
+                for (int i = 0; i < D / 8; i++) {
+                    const float4 v = slots[(slot * (D / 8) + i) * 32 + lane];
+                    o[i][0] = o[i][0] * f0 + v.x * g0;
+                    o[i][1] = o[i][1] * f0 + v.y * g0;
+                    o[i][2] = o[i][2] * f1 + v.z * g1;
+                    o[i][3] = o[i][3] * f1 + v.w * g1;
+                }
+            }
+        }
+        if (kw == 0) {
+            const bool final = a.part_o == nullptr;
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                if (!(e ? in1 : in0)) continue;
+                const int tok = e ? tok1 : tok0, hq = e ? hq1 : hq0;
+                const float m = e ? m1 : m0, l = e ? l1 : l0;
+                const long long row = (long long)tok * a.heads_q + hq;
+                if (final) {
+                    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll
+                    for (int i = 0; i < D / 8; i++)
+                        store_out2(a, tok * a.ldo + (long long)hq * D + 8 * i + 2 * (lane % 4), o[i][2 * e] * inv,
+                                   o[i][2 * e + 1] * inv);
+                    if (lane % 4 == 0) store_lse(a, row, m, l);
+                } else {
+                    const long long at = (long long)(part0 + part) * a.rows + row;
+                    if (lane % 4 == 0) a.part_ml[at] = make_float2(m, l);
+                    if (l > 0.0f)
+#pragma unroll
+                        for (int i = 0; i < D / 8; i++)
+                            *reinterpret_cast<float2*>(a.part_o + at * D + 8 * i + 2 * (lane % 4)) =
+                                make_float2(o[i][2 * e], o[i][2 * e + 1]);
+                }
+            }
+        }
+    }
+    if (!ok && a.status) atomicExch(a.status, (int)QG_ERR_TIMEOUT);
+}
+
+template <typename T, int D, int RW, int KEYS>
+cudaError_t launch_one(const Args& a, const CUtensorMap& kmap, const CUtensorMap& vmap, int part0, int parts,
+                       int tiles_per_part, cudaStream_t s)
+{
+    auto kernel = k_attn_rows<T, D, RW, KEYS>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    const int64_t units = (KEYS & kOwn) ? a.bt.B : 1;
+    const int64_t blocks = ceil_div((int64_t)a.group * ((KEYS & kOwn) ? a.bt.max_q : a.bt.T), 16 * RW);
+    const int64_t grid = units * blocks * parts * a.c.heads;
+    if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    return kv::launch_dependent(kernel, dim3((unsigned)grid), kThreads, Cfg<D>::SMEM, s, kmap, vmap, a, part0, parts,
+                                tiles_per_part, (int)blocks);
+}
+
+template <typename T, int D, int RW>
+cudaError_t by_keys(const Args& a, const CUtensorMap& kmap, const CUtensorMap& vmap, int keys, int part0, int parts,
+                    int tiles_per_part, cudaStream_t s)
+{
+    switch (keys) {
+        case kPrefix: return launch_one<T, D, RW, kPrefix>(a, kmap, vmap, part0, parts, tiles_per_part, s);
+        case kOwn: return launch_one<T, D, RW, kOwn>(a, kmap, vmap, part0, parts, tiles_per_part, s);
+        default: return launch_one<T, D, RW, kPrefix | kOwn>(a, kmap, vmap, part0, parts, tiles_per_part, s);
+    }
+}
+
+template <typename T, int D>
+cudaError_t by_rows(const Args& a, const CUtensorMap& kmap, const CUtensorMap& vmap, int keys, int part0, int parts,
+                    int tiles_per_part, cudaStream_t s)
+{
+    const int64_t rows = (int64_t)a.group * (keys == kPrefix ? a.bt.T : a.bt.max_q);
+    if (rows <= 16) return by_keys<T, D, 1>(a, kmap, vmap, keys, part0, parts, tiles_per_part, s);
+    if (rows <= 32) return by_keys<T, D, 2>(a, kmap, vmap, keys, part0, parts, tiles_per_part, s);
+    return by_keys<T, D, 4>(a, kmap, vmap, keys, part0, parts, tiles_per_part, s);
+}
+
+}  // namespace
+
+cudaError_t launch_rows(const Args& a, int dtype, const CUtensorMap& kmap, const CUtensorMap& vmap, int keys,
+                        int part0, int parts, int tiles_per_part, cudaStream_t s)
+{
+    if (dtype == QG_T_BF16)
+        return a.c.dim == 128 ? by_rows<__nv_bfloat16, 128>(a, kmap, vmap, keys, part0, parts, tiles_per_part, s)
+                              : by_rows<__nv_bfloat16, 64>(a, kmap, vmap, keys, part0, parts, tiles_per_part, s);
+    return a.c.dim == 128 ? by_rows<__half, 128>(a, kmap, vmap, keys, part0, parts, tiles_per_part, s)
+                          : by_rows<__half, 64>(a, kmap, vmap, keys, part0, parts, tiles_per_part, s);
+}
+
+}  // namespace attn
+}  // namespace qg

@@ -139,4 +139,12 @@ size_t diag_workspace_bytes(int N, int K, int group);
 qg_status launch_diag(const uint16_t* W, const qg_qweight& w, float threshold, float* ratio, qg_diag* out, void* ws,
                       cudaStream_t s);
 
+// ---------------------------------------------------------------- paged cache and attention
+qg_status launch_kv_append(const qg_kv_cache& cache, const qg_kv_batch& batch, const qg_rope* rope, const void* q,
+                           int64_t ldq, int heads_q, const void* k, int64_t ldk, const void* v, int64_t ldv, int xt,
+                           void* q_out, int64_t ldq_out, cudaStream_t s);
+size_t attn_workspace_bytes(const qg_kv_cache& cache, const qg_kv_batch& batch, int heads_q);
+qg_status launch_attn(const qg_kv_cache& cache, const qg_kv_batch& batch, const void* q, int64_t ldq, int heads_q,
+                      float scale, void* out, int64_t ldo, int ot, float* lse, void* ws, cudaStream_t s);
+
 }  // namespace qg

@@ -63,7 +63,7 @@ typedef enum {
     QG_ERR_WORKSPACE = -4,     /* workspace missing or smaller than the size query */
     QG_ERR_CUDA = -5,          /* a CUDA runtime call or launch failed */
     QG_ERR_TIMEOUT = -6,       /* reserved: a bounded device-side wait gave up */
-    QG_ERR_DEVICE_STATUS = -7  /* reserved: a device-side check reported an error */
+    QG_ERR_DEVICE_STATUS = -7  /* a device-side check of lengths, pages or positions failed (status word) */
 } qg_status;
 
 typedef enum { QG_Y_F32 = 0, QG_Y_BF16 = 1 } qg_ydtype;
@@ -459,6 +459,137 @@ QG_API qg_status qdiag_workspace_size(int32_t N, int32_t K, int32_t group, size_
  */
 QG_API qg_status qdiag_layer(const uint16_t* W, const qg_qweight* w, float threshold, float* group_ratio,
                              qg_diag* out, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Paged key/value cache: appending with the position rotation, and attention
+ * over a batch that shares a prefix.  These two calls lead from the fused
+ * q/k/v product to the o product's input.
+ *
+ * Cache.  K and V of token place s of page p, head h are head_dim values at
+ *     k + p * page_stride + s * token_stride + h * head_stride   (elements)
+ * and the same for v, so pages may hold heads first ([page, head, place,
+ * dim]), tokens first ([page, place, head, dim]), or both tensors interleaved.
+ *  dtype        QG_T_BF16 or QG_T_F16.
+ *  num_pages    pages the two tensors hold (1 .. 2^30).
+ *  page_size    tokens of a page: a power of two, 16 .. 1024.
+ *  heads_kv     key/value heads; head_dim 64 or 128.
+ *  k, v         16-byte aligned; the strides are multiples of 8 elements,
+ *               at least head_dim, and below 2^38.
+ */
+typedef enum { QG_T_F32 = 0, QG_T_BF16 = 1, QG_T_F16 = 2 } qg_dtype;
+
+typedef struct {
+    void* k;
+    void* v;
+    int32_t dtype, num_pages, page_size, heads_kv, head_dim;
+    int64_t page_stride, token_stride, head_stride;
+} qg_kv_cache;
+
+/*
+ * A batch of sequences over one cache.  Sequence b has n_b new tokens, the
+ * rows cu_q[b] .. cu_q[b+1]-1 of the token arrays, and L_b = kv_len[b] cached
+ * tokens of its own (the new ones, already counted, are its last n_b).  Its
+ * own token at place j lies in page table[b * table_ld + j / page_size]; all
+ * sequences share the prefix_len tokens in the pages of prefix_table, which
+ * come before their own.  New token i stands at own place L_b - n_b + i, at
+ * position prefix_len + L_b - n_b + i, and sees the whole prefix and the own
+ * places up to its own.
+ *
+ * The lengths and tables are DEVICE arrays, read when the kernels run, so a
+ * captured graph may be replayed with new ones; the host gives bounds:
+ *  sequences    B >= 0.
+ *  tokens       T, rows of the token arrays.  Rows from cu_q[B] on belong to
+ *               no sequence: nothing is read or written for them.
+ *  max_q        bound of n_b.       max_kv      bound of L_b (<= table_ld * page_size).
+ *  table        int32 [B, table_ld] (NULL when max_kv = 0).
+ *  kv_len       int32 [B].
+ *  cu_q         int32 [B + 1], not descending, starting at 0; NULL: one new
+ *               token a sequence (T = B, max_q = 1).
+ *  prefix_table int32 [ceil(prefix_len / page_size)] (NULL when prefix_len = 0).
+ *  prefix_len   tokens of the shared prefix (a host value; 0: none).
+ * A length outside its bound is cut to it, and a page number outside
+ * [0, num_pages) is not followed; both set the device status word to
+ * QG_ERR_DEVICE_STATUS (see qgemm_device_status), and the outputs of the
+ * sequences concerned are then not valid.
+ */
+typedef struct {
+    int32_t sequences, tokens, max_q, max_kv, table_ld, prefix_len;
+    const int32_t* table;
+    const int32_t* kv_len;
+    const int32_t* cu_q;
+    const int32_t* prefix_table;
+} qg_kv_batch;
+
+/*
+ * Position rotation.  Row p of `table` (fp32, DEVICE, 16-byte aligned) holds
+ * the dim/2 cosines and then the dim/2 sines of position p, for
+ * p < positions.  The first `dim` values of a head are turned in pairs (a, c):
+ * a' = a cos - c sin, c' = c cos + a sin, with a and c dim/2 apart, or
+ * adjacent when `interleaved`; the others are copied.
+ *  dim          a multiple of 16, at most head_dim.
+ *  positions    rows of the table.
+ *  at           int32 [T] (DEVICE) position of each token, or NULL: the
+ *               batch's own, prefix_len + L_b - n_b + i.
+ */
+typedef struct {
+    const float* table;
+    const int32_t* at;
+    int32_t positions, dim, interleaved;
+} qg_rope;
+
+/*
+ * Append the batch's new tokens to the cache, and turn its queries.
+ *   k, v     [T, heads_kv, head_dim] of type xt (a token's heads contiguous,
+ *            tokens ldk / ldv elements apart, e.g. column ranges of the fused
+ *            q/k/v product's output); DEVICE.
+ *   q        [T, heads_q, head_dim], ldq apart, or NULL (heads_q = 0).
+ *   q_out    [T, heads_q, head_dim] of the cache's type, ldq_out apart.
+ *   xt       QG_T_F32, QG_T_BF16 or QG_T_F16.
+ *   rope     NULL: nothing is rotated.
+ * k (rotated) and v are written to their pages, q (rotated) to q_out, each
+ * value computed in fp32 and rounded once to the cache's type.  A token whose
+ * own place is negative or whose page number is invalid is not cached, and
+ * one whose position is outside the rotation table is not written at all;
+ * both set the status word.  Two tokens must not share a place.
+ * Pointers 16-byte aligned, leading dimensions multiples of 16 bytes.
+ * Bounds-checked on the device as the batch's text says.
+ * Errors: QG_ERR_INVALID_ARG, QG_ERR_UNSUPPORTED, QG_ERR_ALIGNMENT,
+ * QG_ERR_CUDA.
+ */
+QG_API qg_status qkv_append(const qg_kv_cache* cache, const qg_kv_batch* batch, const qg_rope* rope, const void* q,
+                            int64_t ldq, int32_t heads_q, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                            qg_dtype xt, void* q_out, int64_t ldq_out, void* stream);
+
+/*
+ * Attention of the batch's new tokens over the shared prefix and their own
+ * cached tokens:
+ *     out[t, h] = sum_j p_j v_j,  p = softmax_j(scale * q[t, h] . k_j)
+ * over the places token t sees, with the key/value head h / (heads_q / heads_kv).
+ * The prefix is read once for all sequences where that pays.
+ *   q        [T, heads_q, head_dim] of the cache's type, tokens ldq elements
+ *            apart; DEVICE, 16-byte aligned, ldq a multiple of 8.
+ *   heads_q  a multiple of heads_kv.
+ *   scale    > 0, finite (1 / sqrt(head_dim) as a rule).
+ *   out      [T, heads_q, head_dim] of type ot, tokens ldo elements apart;
+ *            16-byte aligned, ldo a multiple of 16 bytes.
+ *   lse      fp32 [T, heads_q] or NULL: ln sum_j exp(scale * q . k_j).
+ *   ws       qattn_workspace_size bytes, 256-byte aligned; contents need not
+ *            be kept or cleared between calls.
+ * A token that sees nothing (kv_len below n_b, no prefix) gets out = 0 and
+ * lse = -inf.  What lies past kv_len or prefix_len in a page is never used,
+ * whatever it holds; cached values in reach must be finite.  Logits, the
+ * softmax's maximum and sum, and the sums over v are held in fp32; p is
+ * rounded to the cache's type for the product with v.  The result does not
+ * depend on the order in which blocks run (repeatable bit for bit).
+ * Errors: QG_ERR_INVALID_ARG, QG_ERR_UNSUPPORTED, QG_ERR_ALIGNMENT,
+ * QG_ERR_WORKSPACE, QG_ERR_CUDA.
+ */
+QG_API qg_status qattn_workspace_size(const qg_kv_cache* cache, const qg_kv_batch* batch, int32_t heads_q,
+                                      size_t* bytes);
+QG_API qg_status qattn_forward(const qg_kv_cache* cache, const qg_kv_batch* batch, const void* q, int64_t ldq,
+                               int32_t heads_q, float scale, void* out, int64_t ldo, qg_dtype ot, float* lse, void* ws,
+                               size_t ws_bytes, void* stream);
 
 /* Self-check of the failure path of the bounded waits: launches one small
  * kernel on `stream` whose single mbarrier wait (at most poll_limit polls,
