@@ -11,12 +11,16 @@ namespace qg {
 namespace attn {
 namespace {
 
-constexpr int kTile = 64;   // keys of a tile of the row kernel
+constexpr int kTile = 64;     // keys of a tile of the row kernel
+constexpr int kBlock = 128;   // keys of a block of the tile kernel
+
+enum Path { kRows, kTiles };
 
 // How a call is split.  Parts are numbered prefix first.
 struct Plan {
     bool shared;                      // the prefix once for all rows, apart from the own tokens
-    int prefix_parts, prefix_tiles;   // parts and tiles of one (shared)
+    Path prefix_path, own_path;       // kernel of each (own_path: of prefix and own together when not shared)
+    int prefix_parts, prefix_tiles;   // parts and tiles or blocks of one (shared)
     int own_parts, own_tiles;         // the same of the own tokens, or of prefix and own together
     int parts;                        // in all; 1: no joining, results are written at once
 };
@@ -32,18 +36,55 @@ void split(int64_t units, int64_t tiles, int* parts, int* per)
     *parts = (int)std::max<int64_t>(1, ceil_div(tiles, *per));
 }
 
+// Parts of `blocks` blocks for `units` pairs of tiles on one CTA an SM: the
+// count whose rounds of the whole card end soonest, an item costing its
+// blocks and about three more to start and finish, and a part's results about
+// a quarter block to write and to join.
+void split_tiles(int64_t units, int64_t blocks, int* parts, int* per)
+{
+    const int64_t sms = num_sms();
+    double best = 0;
+    *parts = 1;
+    *per = (int)std::max<int64_t>(1, blocks);
+    for (int64_t n = 1; n <= 64 && n <= std::max<int64_t>(1, blocks / 2); n++) {
+        const int64_t k = ceil_div(blocks, n);
+        if (n > 1 && ceil_div(blocks, k) != n) continue;
+        const int64_t rounds = ceil_div(units * n, sms);
+        const double cost = (double)rounds * (k + 3) + (n > 1 ? 0.25 * n * ceil_div(units, sms) : 0.0);
+        if (n == 1 || cost < best) {
+            best = cost;
+            *parts = (int)n;
+            *per = (int)std::max<int64_t>(1, k);
+        }
+    }
+}
+
 Plan make_plan(const qg_kv_cache& c, const qg_kv_batch& b, int heads_q)
 {
     Plan p{};
     const int64_t group = heads_q / c.heads_kv;
-    const int64_t np = ceil_div(b.prefix_len, kTile), no = ceil_div(b.max_kv, kTile);
+    const bool tiles = group <= 128;   // a tile holds whole tokens
+    const int64_t per2 = 2 * std::max(1, tile_tokens(group));
     const int64_t own_units = (int64_t)b.sequences * c.heads_kv * ceil_div(group * b.max_q, 64);
-    p.shared = b.sequences > 1 && b.prefix_len >= 256;
-    if (p.shared) {
-        split(c.heads_kv * ceil_div(group * b.tokens, 64), np, &p.prefix_parts, &p.prefix_tiles);
-        split(own_units, no, &p.own_parts, &p.own_tiles);
+    if (tiles && group * b.max_q > 64) {
+        // rows enough for tiles within a sequence: prefix and own tokens in one pass, nothing to join
+        p.own_path = kTiles;
+        const int64_t pairs = std::min<int64_t>(b.tokens / per2 + b.sequences, b.sequences * ceil_div(b.max_q, per2));
+        split_tiles(pairs * c.heads_kv, ceil_div(b.prefix_len, kBlock) + ceil_div(b.max_kv, kBlock), &p.own_parts, &p.own_tiles);
+    } else if (b.sequences > 1 && b.prefix_len >= 256) {
+        p.shared = true;
+        p.own_path = kRows;
+        if (tiles) {
+            p.prefix_path = kTiles;
+            split_tiles(ceil_div(b.tokens, per2) * c.heads_kv, ceil_div(b.prefix_len, kBlock), &p.prefix_parts, &p.prefix_tiles);
+        } else {
+            p.prefix_path = kRows;
+            split(c.heads_kv * ceil_div(group * b.tokens, 64), ceil_div(b.prefix_len, kTile), &p.prefix_parts, &p.prefix_tiles);
+        }
+        split(own_units, ceil_div(b.max_kv, kTile), &p.own_parts, &p.own_tiles);
     } else {
-        split(own_units, np + no, &p.own_parts, &p.own_tiles);
+        p.own_path = kRows;
+        split(own_units, ceil_div(b.prefix_len, kTile) + ceil_div(b.max_kv, kTile), &p.own_parts, &p.own_tiles);
     }
     p.parts = p.prefix_parts + p.own_parts;
     return p;
@@ -117,7 +158,8 @@ cudaError_t launch_join(const Args& a, int parts, cudaStream_t s)
                           : kv::launch_dependent(k_attn_join<64>, grid, 256, 0, s, a, parts);
 }
 
-qg_status encode_pages(CUtensorMap* map, const qg_kv_cache& c, const void* base, int box_rows)
+namespace {
+PFN_cuTensorMapEncodeTiled_v12000 encoder()
 {
     static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> encode{nullptr};
     PFN_cuTensorMapEncodeTiled_v12000 fn = encode.load(std::memory_order_acquire);
@@ -125,11 +167,30 @@ qg_status encode_pages(CUtensorMap* map, const qg_kv_cache& c, const void* base,
         void* f = nullptr;
         cudaDriverEntryPointQueryResult q;
         const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q);
-        if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !f)
-            return fail(QG_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+        if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !f) return nullptr;
         fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
         encode.store(fn, std::memory_order_release);
     }
+    return fn;
+}
+
+qg_status encode(CUtensorMap* map, int dtype, int rank, const void* base, const cuuint64_t* dims,
+                 const cuuint64_t* strides, const cuuint32_t* box)
+{
+    const PFN_cuTensorMapEncodeTiled_v12000 fn = encoder();
+    if (!fn) return fail(QG_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    const CUresult r = fn(map, dtype == QG_T_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                          (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(QG_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return QG_OK;
+}
+}  // namespace
+
+qg_status encode_pages(CUtensorMap* map, const qg_kv_cache& c, const void* base, int box_rows)
+{
     // the stride of a dimension of one entry is never used: any valid one
     const cuuint64_t any = 16;
     const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.heads_kv,
@@ -137,13 +198,16 @@ qg_status encode_pages(CUtensorMap* map, const qg_kv_cache& c, const void* base,
     const cuuint64_t strides[3] = {(cuuint64_t)c.token_stride * 2, c.heads_kv > 1 ? (cuuint64_t)c.head_stride * 2 : any,
                                    c.num_pages > 1 ? (cuuint64_t)c.page_stride * 2 : any};
     const cuuint32_t box[4] = {64u, (cuuint32_t)box_rows, 1u, 1u};
-    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
-    const CUresult r = fn(map, c.dtype == QG_T_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                          4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return fail(QG_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
-    return QG_OK;
+    return encode(map, c.dtype, 4, base, dims, strides, box);
+}
+
+qg_status encode_rows(CUtensorMap* map, int dtype, const void* q, int dim, int heads_q, int64_t ldq, int64_t tokens,
+                      int group)
+{
+    const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads_q, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)dim * 2, (cuuint64_t)ldq * 2};
+    const cuuint32_t box[3] = {64u, (cuuint32_t)group, (cuuint32_t)tile_tokens(group)};
+    return encode(map, dtype, 3, q, dims, strides, box);
 }
 
 }  // namespace attn
@@ -173,16 +237,25 @@ qg_status launch_attn(const qg_kv_cache& cache, const qg_kv_batch& batch, const 
                             : nullptr;
     a.box_rows = std::min(cache.page_size, attn::kTile);
     a.status = device_status_ptr();
-    CUtensorMap kmap, vmap;
+    CUtensorMap qmap, kmap, vmap;
     qg_status st = attn::encode_pages(&kmap, cache, cache.k, a.box_rows);
     if (st != QG_OK) return st;
     st = attn::encode_pages(&vmap, cache, cache.v, a.box_rows);
     if (st != QG_OK) return st;
+    if (p.own_path == attn::kTiles || (p.shared && p.prefix_path == attn::kTiles)) {
+        st = attn::encode_rows(&qmap, cache.dtype, q, cache.head_dim, heads_q, ldq, batch.tokens, a.group);
+        if (st != QG_OK) return st;
+    }
     cudaError_t e = cudaSuccess;
-    if (p.shared) e = attn::launch_rows(a, cache.dtype, kmap, vmap, attn::kPrefix, 0, p.prefix_parts, p.prefix_tiles, s);
+    if (p.shared)
+        e = p.prefix_path == attn::kTiles
+                ? attn::launch_tiles(a, cache.dtype, qmap, kmap, vmap, attn::kPrefix, 0, p.prefix_parts, p.prefix_tiles, s)
+                : attn::launch_rows(a, cache.dtype, kmap, vmap, attn::kPrefix, 0, p.prefix_parts, p.prefix_tiles, s);
+    const int keys = p.shared ? attn::kOwn : attn::kPrefix | attn::kOwn;
     if (e == cudaSuccess)
-        e = attn::launch_rows(a, cache.dtype, kmap, vmap, p.shared ? attn::kOwn : attn::kPrefix | attn::kOwn,
-                              p.prefix_parts, p.own_parts, p.own_tiles, s);
+        e = p.own_path == attn::kTiles
+                ? attn::launch_tiles(a, cache.dtype, qmap, kmap, vmap, keys, p.prefix_parts, p.own_parts, p.own_tiles, s)
+                : attn::launch_rows(a, cache.dtype, kmap, vmap, keys, p.prefix_parts, p.own_parts, p.own_tiles, s);
     if (e == cudaSuccess && p.parts > 1) e = attn::launch_join(a, p.parts, s);
     if (e != cudaSuccess) return cuda_fail(e, "qattn_forward launch");
     return QG_OK;

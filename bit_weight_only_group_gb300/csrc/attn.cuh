@@ -95,12 +95,19 @@ __device__ __forceinline__ int page_of(const Args& a, const int* table, int n, i
 // Host side.
 // Map of K or V pages: dimensions (dim, place, head, page), boxes of 64 values x box_rows places.
 qg_status encode_pages(CUtensorMap* map, const qg_kv_cache& c, const void* base, int box_rows);
+// Map of the query rows: dimensions (dim, head, token), boxes of 64 values x a group x a tile's tokens.
+qg_status encode_rows(CUtensorMap* map, int dtype, const void* q, int dim, int heads_q, int64_t ldq, int64_t tokens,
+                      int group);
 
 // The kernels' launches.  A keys flag says what a row sees: the shared
 // prefix, its own sequence's tokens, or both in that order.
 enum Keys { kPrefix = 1, kOwn = 2 };
 cudaError_t launch_rows(const Args& a, int dtype, const CUtensorMap& kmap, const CUtensorMap& vmap, int keys,
                         int part0, int parts, int tiles_per_part, cudaStream_t s);
+// Tokens of a tile of the tile kernel (its rows: that times the group, at most 128).
+inline int tile_tokens(int64_t group) { return (int)(128 / group); }
+cudaError_t launch_tiles(const Args& a, int dtype, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                         const CUtensorMap& vmap, int keys, int part0, int parts, int blocks_per_part, cudaStream_t s);
 cudaError_t launch_join(const Args& a, int parts, cudaStream_t s);
 
 }  // namespace attn

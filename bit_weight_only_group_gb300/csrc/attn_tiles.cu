@@ -1,0 +1,650 @@
+// Attention for many query rows per key/value head on the 5th-generation
+// tensor cores: the prefix shared by a batch (all its tokens' rows against one
+// run of keys), and prompts of many tokens a sequence.
+//
+// A tile is up to 128 rows: 128 / group tokens times the query heads of one
+// key/value head.  Keys come in blocks of 128.  For a tile and a block
+//     S = Q K^T     tcgen05, Q and K from shared memory, S in tensor memory
+//     P = 2^(S scale_log2 - m)   one thread a row: S read from tensor memory,
+//                   P written back over it in the cache's type
+//     O += P V      tcgen05, P from tensor memory, V from shared memory
+//                   (its head dimension contiguous), O in tensor memory
+// The tensor core waits for the softmax of a block and the softmax for its S,
+// so a CTA runs two such chains ("streams") side by side, 256 columns of
+// tensor memory each (S and P 128, O 128): while one is in its softmax the
+// tensor core works for the other.  With two tiles of rows the streams are the
+// tiles, over the same blocks, so each K and V block loaded feeds 256 rows;
+// with one tile left they take alternate blocks of it and are joined at the
+// end.
+//
+// The running maximum is only raised when a row's new maximum is above it by
+// more than 8 (in powers of two): P then stays below 2^8, exact in range for
+// both types, sums are fp32, and O is rescaled in few blocks instead of all.
+//
+// Warps: 0-3 softmax of stream 0, 4-7 of stream 1 (a warp may reach only the
+// 32 lanes of tensor memory its index modulo 4 names), 8 loads (one lane per
+// TMA box), 9 the matrix products.  One persistent CTA an SM (all 512 columns
+// of tensor memory); items of work are dealt in turn.
+#include <algorithm>
+
+#include "attn.cuh"
+
+namespace qg {
+namespace attn {
+namespace {
+
+constexpr int KB = 128;                      // keys of a block
+constexpr int kWarpLoad = 8, kWarpMma = 9;
+constexpr int kThreads = 384;                // warps 10 and 11 only fill the third warpgroup
+// Registers of a thread: 168 at launch (65536 over 384), then shared out by
+// warpgroup, 208 for the softmax's (a row of S, 128 values, in registers) and
+// 120 for the other: 2 * 192 + 120 = 3 * 168.
+constexpr int kRegsSoftmax = 192, kRegsOther = 120;
+static_assert(2 * kRegsSoftmax + kRegsOther == 3 * 168, "registers shared out are those of the launch");
+constexpr int kMarks = 128;                  // sequences whose place in the list of tile pairs is kept in shared memory
+constexpr float kRaise = 8.0f;               // see above
+
+template <int D> struct Cfg {
+    static constexpr int HALVES = D / 64;
+    static constexpr int HALF = 128 * 128;                 // bytes of 128 rows of 64 values
+    static constexpr int TILE = HALVES * HALF;             // a Q tile, a K or a V block
+    static constexpr int SLOTS = D == 128 ? 5 : 8;         // ring of K and V blocks
+    static constexpr int OFF_KV = 2 * TILE;
+    static constexpr int OFF_BAR = OFF_KV + SLOTS * TILE;
+    static constexpr int OFF_ML = OFF_BAR + 256;           // (m, l) of stream 1's rows (joining)
+    static constexpr int OFF_UNITS = OFF_ML + 128 * 8;
+    static constexpr int SMEM = OFF_UNITS + (kMarks + 1) * 4 + 1024 /* alignment */;
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+constexpr int kTmemCols = 512, kColO = 256;  // S and P of stream s at 128 s, O at 256 + 128 s
+
+// kind::f16 instruction descriptor: M = 128, fp32 accumulator; B's head dimension contiguous when `mn`.
+template <typename T>
+__device__ constexpr uint32_t idesc(int N, bool mn)
+{
+    const uint32_t fmt = std::is_same<T, __half>::value ? 0u : 1u;
+    return (1u << 4) | (fmt << 7) | (fmt << 10) | ((mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+}
+// Descriptor of an operand whose M or N dimension is contiguous, 128-byte
+// swizzle: 8 k rows of 64 values are 1024 bytes, the next 8 follow (stride),
+// the next 64 values are `next64` bytes away (leading).
+__device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t next64)
+{
+    return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(next64 >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// D += A B^T with A in tensor memory, issued by one lane of the whole warp.
+__device__ __forceinline__ void mma_ts_elect(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t id, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(id), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+        "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+        "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(
+            r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+
+struct Shape {
+    int parts, blocks_per_part;   // of an item's keys
+    int part0;                    // number of the first part
+    int per;                      // tokens of a tile
+};
+
+// One item: a pair of tiles (or one) of a unit's rows, a key/value head, a part of the keys.
+struct Item {
+    int head, part;
+    int t0, t1;         // first token of the pair, end of the unit's tokens
+    bool two;           // the second tile has rows
+    int own0;           // own places token t sees: own0 + t - t0
+    int own;            // own places any row sees
+    int prefix, np;     // prefix tokens, their blocks
+    int blk0, blk1;     // this part's blocks
+    int b;
+};
+
+// Pairs of tiles of sequence b.
+__device__ __forceinline__ int pairs_of(const Args& a, int b, int per2, int& t0, int& t1)
+{
+    kv::token_range(a.bt, b, t0, t1);
+    return (t1 - t0 + per2 - 1) / per2;
+}
+
+// Item i of the CTA's list, or false past the end.  marks (own keys, in
+// shared memory): pairs of tiles before every `stride`-th sequence, and in
+// all at kMarks.
+template <int KEYS>
+__device__ __forceinline__ bool get_item(const Args& a, const Shape& sh, const int* marks, int i, bool tell, Item& it)
+{
+    const int per2 = 2 * sh.per;
+    int pair, t0, t1;
+    it.own0 = it.own = 0;
+    it.b = 0;
+    it.prefix = (KEYS & kPrefix) ? a.bt.prefix_len : 0;
+    it.np = (it.prefix + KB - 1) / KB;
+    if (KEYS & kOwn) {
+        // heads fastest, then parts, then pairs of tiles
+        it.head = i % a.c.heads;
+        i /= a.c.heads;
+        it.part = i % sh.parts;
+        pair = i / sh.parts;
+        if (pair >= marks[kMarks]) return false;
+        const int stride = (a.bt.B + kMarks - 1) / kMarks;
+        int lo = 0, hi = (a.bt.B + stride - 1) / stride;   // the last mark at or before the pair
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (marks[mid] <= pair) lo = mid;
+            else hi = mid;
+        }
+        pair -= marks[lo];
+        it.b = lo * stride;
+        for (int n; (n = pairs_of(a, it.b, per2, t0, t1)) <= pair && it.b + 1 < a.bt.B; it.b++) pair -= n;
+    } else {
+        // pairs of tiles fastest: CTAs that run together read the same blocks
+        t0 = 0;
+        t1 = kv::used_tokens(a.bt);
+        const int pairs = (t1 + per2 - 1) / per2;
+        if (pairs == 0 || i >= pairs * sh.parts * a.c.heads) return false;
+        pair = i % pairs;
+        i /= pairs;
+        it.part = i % sh.parts;
+        it.head = i / sh.parts;
+    }
+    it.t0 = t0 + pair * per2;
+    it.t1 = t1;
+    it.two = t1 - it.t0 > sh.per;
+    if (KEYS & kOwn) {
+        int len;
+        const bool ok = kv::own_length(a.bt, it.b, len) && t1 - t0 <= a.bt.max_q;
+        if (!ok && tell) kv::report(a.status);
+        it.own0 = len - (t1 - it.t0) + 1;
+        it.own = max(0, it.own0 + min(per2, t1 - it.t0) - 1);
+    }
+    const int blocks = it.np + (it.own + KB - 1) / KB;
+    it.blk0 = min(it.part * sh.blocks_per_part, blocks);
+    it.blk1 = min(it.blk0 + sh.blocks_per_part, blocks);
+    return true;
+}
+
+// Ring positions of an item's loads, in the order K0, K1 V0, K2 V1, ...:
+// the order the products want them in.
+__device__ __forceinline__ int pos_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ int pos_v(int j, int n) { return j + 1 < n ? 2 * j + 2 : 2 * j + 1; }
+
+template <typename T, int D, int KEYS>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_attn_tiles(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                 const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Args a,
+                 const __grid_constant__ Shape sh)
+{
+    using C = Cfg<D>;
+    constexpr int NS = C::SLOTS, HALVES = C::HALVES;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sbase = ptx::smem_u32(smem), bars = sbase + C::OFF_BAR;
+    const uint32_t q_full = bars, q_empty = bars + 8;
+    auto s_full = [&](int s) { return bars + 16 + 8 * s; };     // S of stream s is in tensor memory
+    auto p_full = [&](int s) { return bars + 32 + 8 * s; };     // P is, and O may be added to
+    auto o_full = [&](int s) { return bars + 48 + 8 * s; };     // O is complete
+    const uint32_t join_full = bars + 64, join_empty = bars + 72;   // stream 1's results for stream 0 to join: ready, read
+    auto kv_full = [&](int x) { return bars + 80 + 8 * x; };
+    auto kv_empty = [&](int x) { return bars + 80 + 8 * (NS + x); };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 80 + 16 * NS);
+    static_assert(80 + 16 * NS + 4 <= 256, "barriers");
+    int* marks = reinterpret_cast<int*>(smem + C::OFF_UNITS);
+    float2* ml1 = reinterpret_cast<float2*>(smem + C::OFF_ML);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(q_full, 1);
+        ptx::mbar_init(q_empty, 1);
+        for (int s = 0; s < 2; s++) {
+            ptx::mbar_init(s_full(s), 1);
+            ptx::mbar_init(p_full(s), 4);
+            ptx::mbar_init(o_full(s), 1);
+        }
+        ptx::mbar_init(join_full, 4);
+        ptx::mbar_init(join_empty, 4);
+        for (int x = 0; x < NS; x++) { ptx::mbar_init(kv_full(x), 1); ptx::mbar_init(kv_empty(x), 1); }
+        ptx::fence_mbar_init();
+    }
+    if (warp == kWarpMma) {
+        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    if (warp == kWarpLoad && lane == 0) {
+        ptx::prefetch_tensormap(&qmap);
+        ptx::prefetch_tensormap(&kmap);
+        ptx::prefetch_tensormap(&vmap);
+    }
+    kv::pdl_wait();
+    kv::pdl_release();
+    if ((KEYS & kOwn) && warp == 0) {
+        const int stride = (a.bt.B + kMarks - 1) / kMarks;
+        int sum = 0;
+        for (int b0 = 0; b0 < a.bt.B; b0 += 32) {
+            const int b = b0 + lane;
+            int t0, t1;
+            const int n = b < a.bt.B ? pairs_of(a, b, 2 * sh.per, t0, t1) : 0;
+            int upto = n;
+#pragma unroll
+            for (int i = 1; i < 32; i *= 2) {
+                const int v = __shfl_up_sync(0xffffffffu, upto, i);
+                if (lane >= i) upto += v;
+            }
+            if (b < a.bt.B && b % stride == 0) marks[b / stride] = sum + upto - n;
+            sum += __shfl_sync(0xffffffffu, upto, 31);
+        }
+        if (lane == 0) marks[kMarks] = sum;
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    bool ok = true;
+    Item it;
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        if (warp == kWarpLoad) {
+            // ------------------------------------------------ loads
+            const int boxes = KB / a.box_rows;                 // of a block, each rows of one page
+            const int mine = lane % boxes, half = lane / boxes;
+            const bool busy = half < HALVES;
+            const int in_page_mask = (1 << a.c.page_shift) - 1;
+            int pos = 0;                                       // loads so far
+            uint32_t item_phase = 0;
+            for (int i = blockIdx.x; ok && get_item<KEYS>(a, sh, marks, i, false, it); i += gridDim.x, item_phase ^= 1u) {
+                const int n = it.blk1 - it.blk0;
+                const int n_prefix = (it.prefix + in_page_mask) >> a.c.page_shift;
+                const int* own_table = (KEYS & kOwn) ? a.bt.table + (long long)it.b * a.bt.table_ld : nullptr;
+                auto keys_of = [&](int blk) { return blk < it.np ? min(KB, it.prefix - blk * KB) : min(KB, it.own - (blk - it.np) * KB); };
+                auto page_at = [&](int blk) -> int {
+                    if (!busy || blk >= it.blk1 || mine * a.box_rows >= keys_of(blk)) return 0;
+                    const int key = (blk < it.np ? blk : blk - it.np) * KB + mine * a.box_rows;
+                    return blk < it.np ? page_of(a, a.bt.prefix_table, n_prefix, key >> a.c.page_shift)
+                                       : page_of(a, own_table, a.bt.table_ld, key >> a.c.page_shift);
+                };
+                auto load = [&](const CUtensorMap* map, int blk, int page) -> bool {
+                    const int x = pos % NS;
+                    if (!__all_sync(0xffffffffu, ptx::mbar_wait(kv_empty(x), ((pos / NS) & 1) ^ 1u))) return false;
+                    pos++;
+                    const int used = (keys_of(blk) + a.box_rows - 1) / a.box_rows;
+                    if (lane == 0) ptx::mbar_expect_tx(kv_full(x), (uint32_t)(used * HALVES * a.box_rows * 128));
+                    __syncwarp();
+                    if (busy && mine < used) {
+                        const int key = (blk < it.np ? blk : blk - it.np) * KB + mine * a.box_rows;
+                        tma_load_4d(sbase + C::OFF_KV + x * C::TILE + half * C::HALF + mine * a.box_rows * 128, map, half * 64,
+                                    key & in_page_mask, it.head, page, kv_full(x));
+                    }
+                    return true;
+                };
+                int page = page_at(it.blk0);
+                if (n > 0) ok = load(&kmap, it.blk0, page);
+                if (!ok) break;
+                // the last item's Q is no longer read
+                ok = __all_sync(0xffffffffu, ptx::mbar_wait(q_empty, item_phase ^ 1u));
+                if (!ok) break;
+                if (lane == 0) {
+                    const uint32_t bytes = (uint32_t)(sh.per * a.group) * 128u * HALVES;
+                    ptx::mbar_expect_tx(q_full, it.two ? 2 * bytes : bytes);
+                    for (int s = 0; s < (it.two ? 2 : 1); s++)
+                        for (int h = 0; h < HALVES; h++)
+                            tma_load_3d(sbase + s * C::TILE + h * C::HALF, &qmap, 64 * h, it.head * a.group,
+                                        it.t0 + s * sh.per, q_full);
+                }
+                __syncwarp();
+                for (int j = 1; ok && j <= n; j++) {
+                    const int next = j < n ? page_at(it.blk0 + j) : 0;
+                    if (j < n) ok = load(&kmap, it.blk0 + j, next);
+                    if (ok) ok = load(&vmap, it.blk0 + j - 1, page);
+                    page = next;
+                }
+            }
+        } else if (warp == kWarpMma) {
+            // ------------------------------------------------ matrix products
+            constexpr uint32_t id_qk = idesc<T>(KB, false), id_pv = idesc<T>(D, true);
+            uint32_t item_phase = 0, p_phase[2] = {0, 0};
+            int base = 0;   // ring position of the item's first load
+            auto wait_kv = [&](int pos) {
+                const bool r = __all_sync(0xffffffffu, ptx::mbar_wait(kv_full(pos % NS), (pos / NS) & 1));
+                ptx::tc_fence_after();
+                return r;
+            };
+            auto qk = [&](int tile, int s, int pos) {
+                const uint64_t ad = ptx::sw128_desc(sbase + tile * C::TILE);
+                const uint64_t bd = ptx::sw128_desc(sbase + C::OFF_KV + (pos % NS) * C::TILE);
+    #pragma unroll
+                for (int k = 0; k < D / 16; k++) {
+                    const uint64_t off = (uint64_t)(((k / 4) * C::HALF + (k % 4) * 32) >> 4);
+                    ptx::mma_f16_elect(tmem + 128 * s, ad + off, bd + off, id_qk, k != 0);
+                }
+                ptx::tc_commit_elect(s_full(s));
+            };
+            auto pv = [&](int s, int pos, bool first) {
+                const uint64_t bd = mn_desc(sbase + C::OFF_KV + (pos % NS) * C::TILE, C::HALF);
+    #pragma unroll
+                for (int k = 0; k < KB / 16; k++)
+                    mma_ts_elect(tmem + kColO + 128 * s, tmem + 128 * s + 8 * k, bd + (uint64_t)((k * 2048) >> 4), id_pv,
+                                 !first || k != 0);
+            };
+            auto wait_p = [&](int s) {
+                const bool r = __all_sync(0xffffffffu, ptx::mbar_wait(p_full(s), p_phase[s]));
+                p_phase[s] ^= 1u;
+                ptx::tc_fence_after();
+                return r;
+            };
+            for (int i = blockIdx.x; ok && get_item<KEYS>(a, sh, marks, i, false, it); i += gridDim.x, item_phase ^= 1u) {
+                const int n = it.blk1 - it.blk0;
+                const int step = it.two ? 1 : 2;       // a stream's next block
+                auto release = [&](int pos) { ptx::tc_commit_elect(kv_empty(pos % NS)); };
+                ok = __all_sync(0xffffffffu, ptx::mbar_wait(q_full, item_phase));
+                if (!ok) break;
+                if (n > 0) {
+                    ok = wait_kv(base + pos_k(0));
+                    if (!ok) break;
+                    qk(0, 0, base + pos_k(0));
+                    if (it.two) qk(1, 1, base + pos_k(0));
+                    release(base + pos_k(0));
+                    if (!it.two && n > 1) {
+                        ok = wait_kv(base + pos_k(1));
+                        if (!ok) break;
+                        qk(0, 1, base + pos_k(1));
+                        release(base + pos_k(1));
+                    }
+                }
+                if (n <= step) ptx::tc_commit_elect(q_empty);   // (n = 0: at once)
+                for (int j = 0; ok && j < n; j++) {
+                    const int pv_pos = base + pos_v(j, n);
+                    ok = wait_kv(pv_pos);
+                    if (!ok) break;
+                    const int blk = it.blk0 + j;
+                    const int keys = blk < it.np ? it.prefix - blk * KB : it.own - (blk - it.np) * KB;
+                    if (keys < KB) {
+                        // V rows past the last key: what the page or an older block left there times 0 must be 0
+                        unsigned char* v = smem + C::OFF_KV + (pv_pos % NS) * C::TILE;
+                        for (int e = lane; e < (KB - keys) * 8 * HALVES; e += 32) {
+                            const int row = keys + e / (8 * HALVES), c = e % (8 * HALVES);
+                            *reinterpret_cast<uint4*>(v + (c / 8) * C::HALF + row * 128 + (c % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        ptx::fence_proxy_async();
+                        __syncwarp();
+                    }
+                    const bool more = j + step < n;
+                    const int k_pos = base + pos_k(j + step);
+    #pragma unroll
+                    for (int s = 0; s < 2; s++) {
+                        if (!it.two && s != (j & 1)) continue;
+                        ok = ok && wait_p(s);
+                        if (!ok) break;
+                        pv(s, pv_pos, j < step);
+                        if (!it.two || s == 1) release(pv_pos);
+                        if (more) {
+                            if (!it.two || s == 0) ok = wait_kv(k_pos);
+                            if (!ok) break;
+                            qk(it.two ? s : 0, s, k_pos);
+                            if (!it.two || s == 1) {
+                                release(k_pos);
+                                if (j + step == n - 1) ptx::tc_commit_elect(q_empty);
+                            }
+                        } else {
+                            ptx::tc_commit_elect(o_full(s));
+                        }
+                    }
+                }
+                base += 2 * n;
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        // ------------------------------------------------ softmax, a row a thread
+        const int s = warp / 4;
+        const uint32_t lanes = (uint32_t)(32 * (warp % 4)) << 16;
+        const uint32_t t_s = tmem + lanes + 128 * s, t_o = tmem + lanes + kColO + 128 * s;
+        const int r = 32 * (warp % 4) + lane;
+        const int tok_in_tile = r / a.group;
+        uint32_t s_phase = 0, o_phase = 0, join_phase = 0;
+        for (int i = blockIdx.x; ok && get_item<KEYS>(a, sh, marks, i, threadIdx.x == 0, it); i += gridDim.x) {
+            const int n = it.blk1 - it.blk0, step = it.two ? 1 : 2;
+            const int tok = it.t0 + (it.two ? s * sh.per : 0) + tok_in_tile;
+            const bool in = tok_in_tile < sh.per && tok < it.t1;
+            float m = -INFINITY, l = 0.0f;
+            const int first = it.two ? 0 : s;
+            for (int j = first; j < n; j += step) {
+                const int blk = it.blk0 + j;
+                const int vis = blk < it.np ? it.prefix - blk * KB : it.own0 + (tok - it.t0) - (blk - it.np) * KB;
+                ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full(s), s_phase));
+                s_phase ^= 1u;
+                if (!ok) break;
+                ptx::tc_fence_after();
+                uint32_t x[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; c++) tmem_ld32(t_s + 32 * c, x[c]);
+                ptx::tmem_ld_wait();
+                if (__any_sync(0xffffffffu, vis < KB)) {
+#pragma unroll
+                    for (int c = 0; c < 4; c++)
+#pragma unroll
+                        for (int e = 0; e < 32; e++)
+                            if (32 * c + e >= vis) x[c][e] = 0xFF800000u;   // -inf
+                }
+                float t = __uint_as_float(x[0][0]);
+#pragma unroll
+                for (int c = 0; c < 4; c++)
+#pragma unroll
+                    for (int e = 0; e < 32; e++) t = fmaxf(t, __uint_as_float(x[c][e]));
+                t *= a.scale_log2;
+                const bool raise = t > m + kRaise || (m == -INFINITY && t > -INFINITY);
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float to = raise ? t : m;
+                    const float f = to == m ? 1.0f : exp2_approx(m - to);
+                    m = to;
+                    l *= f;
+                    if (j != first) {
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; c++) {
+                            uint32_t o[32];
+                            tmem_ld32(t_o + 32 * c, o);
+                            ptx::tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st32(t_o + 32 * c, o);
+                        }
+                    }
+                }
+                const float u = m == -INFINITY ? 0.0f : m;   // a row that has seen nothing: all terms 2^-inf
+                float sum = 0.0f;
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int e = 0; e < 16; e++) {
+                        const float p0 = exp2_approx(fmaf(__uint_as_float(x[c][2 * e]), a.scale_log2, -u));
+                        const float p1 = exp2_approx(fmaf(__uint_as_float(x[c][2 * e + 1]), a.scale_log2, -u));
+                        sum += p0 + p1;
+                        p[e] = kv::pack2<T>(p0, p1);
+                    }
+                    tmem_st16(t_s + 16 * c, p);
+                }
+                l += sum;
+                tmem_st_wait();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(p_full(s));
+            }
+            if (!ok) break;
+            // ------------------------------------------------ the item's rows
+            const bool ran = n > first;
+            if (ran) {
+                ok = __all_sync(0xffffffffu, ptx::mbar_wait(o_full(s), o_phase));
+                o_phase ^= 1u;
+                if (!ok) break;
+                ptx::tc_fence_after();
+            }
+            float w0 = 1.0f, w1 = 0.0f;       // weights of the two streams' O
+            const bool both = !it.two && n > 1;
+            if (!it.two) {
+                if (s == 1) {
+                    ml1[r] = make_float2(m, l);
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(join_full);
+                } else {
+                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(join_full, join_phase));
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const float2 v = ml1[r];
+                    const float to = fmaxf(m, v.x), u = to == -INFINITY ? 0.0f : to;
+                    w0 = exp2_approx(m - u);
+                    w1 = exp2_approx(v.x - u);
+                    l = l * w0 + v.y * w1;
+                    m = to;
+                }
+            }
+            if (it.two || s == 0) {
+                const int hq = it.head * a.group + (r - tok_in_tile * a.group);
+                const long long row = (long long)tok * a.heads_q + hq;
+                const bool final = a.part_o == nullptr;
+                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                if (final) { w0 *= inv; w1 *= inv; }
+                const long long at = (long long)(sh.part0 + it.part) * a.rows + row;
+                if (in) {
+                    if (final) store_lse(a, row, m, l);
+                    else a.part_ml[at] = make_float2(m, l);
+                }
+#pragma unroll 1
+                for (int c = 0; c < D / 32; c++) {
+                    uint32_t o[32];
+                    if (ran) {
+                        tmem_ld32(t_o + 32 * c, o);
+                        ptx::tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * w0);
+                        if (both) {
+                            uint32_t o1[32];
+                            tmem_ld32(t_o + 128 + 32 * c, o1);
+                            ptx::tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; e++)
+                                o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), w1, __uint_as_float(o[e])));
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e++) o[e] = 0u;
+                    }
+                    if (!in) continue;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 v = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                                                     __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+                        if (final) store_out4(a, tok * a.ldo + (long long)hq * D + 32 * c + e, v);
+                        else if (l > 0.0f) __stcg(reinterpret_cast<float4*>(a.part_o + at * D + 32 * c + e), v);
+                    }
+                }
+            }
+            if (!it.two) {
+                if (s == 0) {
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(join_empty);
+                } else {
+                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(join_empty, join_phase));
+                    ptx::tc_fence_after();
+                }
+                join_phase ^= 1u;
+            }
+        }
+    }
+    if (!ok && a.status) atomicExch(a.status, (int)QG_ERR_TIMEOUT);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == kWarpMma) ptx::tmem_dealloc(tmem, kTmemCols);
+}
+
+template <typename T, int D, int KEYS>
+cudaError_t launch_one(const Args& a, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                       const Shape& sh, int64_t items, cudaStream_t s)
+{
+    auto kernel = k_attn_tiles<T, D, KEYS>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = (unsigned)std::min<int64_t>(num_sms(), items);
+    return kv::launch_dependent(kernel, dim3(grid), kThreads, Cfg<D>::SMEM, s, qmap, kmap, vmap, a, sh);
+}
+
+template <typename T>
+cudaError_t by_shape(const Args& a, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                     const Shape& sh, int keys, int64_t items, cudaStream_t s)
+{
+    if (keys == kPrefix)
+        return a.c.dim == 128 ? launch_one<T, 128, kPrefix>(a, qmap, kmap, vmap, sh, items, s)
+                              : launch_one<T, 64, kPrefix>(a, qmap, kmap, vmap, sh, items, s);
+    return a.c.dim == 128 ? launch_one<T, 128, kPrefix | kOwn>(a, qmap, kmap, vmap, sh, items, s)
+                          : launch_one<T, 64, kPrefix | kOwn>(a, qmap, kmap, vmap, sh, items, s);
+}
+
+}  // namespace
+
+cudaError_t launch_tiles(const Args& a, int dtype, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                         const CUtensorMap& vmap, int keys, int part0, int parts, int blocks_per_part, cudaStream_t s)
+{
+    Shape sh;
+    sh.parts = parts;
+    sh.blocks_per_part = blocks_per_part;
+    sh.part0 = part0;
+    sh.per = tile_tokens(a.group);
+    // pairs of tiles: a whole batch's tokens, or at most so many over the sequences
+    const int64_t pairs = keys == kPrefix ? ceil_div(a.bt.T, 2 * sh.per)
+                                          : std::min<int64_t>(a.bt.T / (2 * sh.per) + a.bt.B,
+                                                              (int64_t)a.bt.B * ceil_div(a.bt.max_q, 2 * sh.per));
+    const int64_t items = pairs * parts * a.c.heads;
+    if (items > 0x3FFFFFFF) return cudaErrorInvalidConfiguration;
+    return dtype == QG_T_BF16 ? by_shape<__nv_bfloat16>(a, qmap, kmap, vmap, sh, keys, items, s)
+                              : by_shape<__half>(a, qmap, kmap, vmap, sh, keys, items, s);
+}
+
+}  // namespace attn
+}  // namespace qg
