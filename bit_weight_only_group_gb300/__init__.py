@@ -522,7 +522,7 @@ class KVCache:
             raise ValueError("k and v must be 4-D with the same shape, strides and dtype")
         if k.dtype not in (torch.bfloat16, torch.float16) or not k.is_cuda or not v.is_cuda or k.stride(3) != 1:
             raise ValueError("k and v must be bfloat16 or float16 CUDA tensors with unit inner stride")
-        self.k, self.v, self.dtype = k, v, k.dtype
+        self.k, self.v, self.dtype, self.device = k, v, k.dtype, k.device
         self.num_pages, self.page_size, self.heads_kv, self.head_dim = k.shape
         self._desc = QgKvCache(k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype], *k.shape, *k.stride()[:3])
         self._ref = ctypes.byref(self._desc)
@@ -583,13 +583,24 @@ class KVBatch:
             raise ValueError(f"prefix_table of {self._shared} pages holds fewer than prefix_len={self.prefix_len} tokens")
 
 
-def _rows(t: torch.Tensor, name: str, T: int, heads: int | None, dim: int):
-    """A CUDA array [T, heads, dim] whose heads are contiguous: its token stride."""
-    if not t.is_cuda or t.dim() != 3 or t.shape[0] != T or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be a CUDA tensor [{T}, {'heads' if heads is None else heads}, {dim}]")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != dim):
-        raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return t.stride(0) if T > 1 else t.shape[1] * dim
+def _rows(t: torch.Tensor, name: str, T: int, heads: int, dim: int) -> int:
+    """Token stride of a CUDA array [T, heads, dim] whose heads are contiguous (heads 0: any number)."""
+    shape = t.shape
+    if len(shape) == 3 and t.is_cuda:
+        n, h, d = shape
+        if n == T and d == dim and (h == heads or not heads):
+            st, sh, sd = t.stride()
+            if sd == 1 and (sh == dim or h == 1):
+                return st if T > 1 else h * dim
+            raise ValueError(f"the heads of a token of {name} must be contiguous")
+    raise ValueError(f"{name} must be a CUDA tensor [{T}, {heads or 'heads'}, {dim}]")
+
+
+def _raw_stream(stream, index: int) -> int:
+    """cudaStream_t of a stream argument; None: the device's current stream."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def qkv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, q: torch.Tensor | None = None,
@@ -600,20 +611,24 @@ def qkv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor,
     heads_q, head_dim] turned, in the cache's type.  rope: fp32 [positions,
     R], row p the R/2 cosines and then the R/2 sines of position p (None: no
     rotation); positions: int32 [T] in place of the batch's own."""
-    T, D = batch.tokens, cache.head_dim
+    T, D, xt = batch.tokens, cache.head_dim, k.dtype
     batch.check(cache)
     ldk, ldv = _rows(k, "k", T, cache.heads_kv, D), _rows(v, "v", T, cache.heads_kv, D)
-    if k.dtype not in _DTYPES or v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+    if v.dtype != xt or (q is not None and q.dtype != xt) or xt not in _DTYPES:
         raise ValueError("q, k and v must share one dtype (float32, bfloat16 or float16)")
     heads_q = ldq = ldq_out = 0
+    q_at = out_at = None
     if q is not None:
+        ldq = _rows(q, "q", T, 0, D)
         heads_q = q.shape[1]
-        ldq = _rows(q, "q", T, None, D)
         if q_out is None:
-            q_out = torch.empty((T, heads_q, D), dtype=cache.dtype, device=q.device)
-        ldq_out = _rows(q_out, "q_out", T, heads_q, D)
-        if q_out.dtype != cache.dtype:
-            raise ValueError("q_out must have the cache's dtype")
+            q_out = torch.empty((T, heads_q, D), dtype=cache.dtype, device=cache.device)
+            ldq_out = heads_q * D
+        else:
+            ldq_out = _rows(q_out, "q_out", T, heads_q, D)
+            if q_out.dtype != cache.dtype:
+                raise ValueError("q_out must have the cache's dtype")
+        q_at, out_at = q.data_ptr(), q_out.data_ptr()
     turn = None
     if rope is not None:
         if rope.dtype != torch.float32 or not rope.is_cuda or rope.dim() != 2 or not rope.is_contiguous():
@@ -621,10 +636,11 @@ def qkv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor,
         if positions is not None and (positions.dtype != torch.int32 or not positions.is_cuda or
                                       positions.shape != (T,) or not positions.is_contiguous()):
             raise ValueError(f"positions must be a contiguous int32 CUDA tensor [{T}]")
-        turn = ctypes.byref(QgRope(rope.data_ptr(), _ptr(positions), rope.shape[0], rope.shape[1], int(interleaved)))
-    _check(lib().qkv_append(cache._ref, batch._ref, turn, None if q is None else q.data_ptr(), ldq, heads_q,
-                            k.data_ptr(), ldk, v.data_ptr(), ldv, _DTYPES[k.dtype],
-                            None if q is None else q_out.data_ptr(), ldq_out, _stream(stream)), "qkv_append")
+        turn = QgRope(rope.data_ptr(), _ptr(positions), *rope.shape, interleaved)
+    st = lib().qkv_append(cache._ref, batch._ref, turn, q_at, ldq, heads_q, k.data_ptr(), ldk, v.data_ptr(), ldv,
+                          _DTYPES[xt], out_at, ldq_out, _raw_stream(stream, cache.device.index))
+    if st != QG_OK:
+        _check(st, "qkv_append")
     return q_out
 
 
@@ -645,20 +661,24 @@ def qattn_forward(q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: float 
     batch.check(cache)
     if q.dtype != cache.dtype:
         raise ValueError("q must have the cache's dtype")
-    ldq = _rows(q, "q", T, None, D)
+    ldq = _rows(q, "q", T, 0, D)
     heads_q = q.shape[1]
     if out is None:
-        out = torch.empty((T, heads_q, D), dtype=out_dtype or q.dtype, device=q.device)
-    ldo = _rows(out, "out", T, heads_q, D)
+        out = torch.empty((T, heads_q, D), dtype=out_dtype or cache.dtype, device=cache.device)
+        ldo = heads_q * D
+    else:
+        ldo = _rows(out, "out", T, heads_q, D)
     if out.dtype not in _DTYPES:
         raise ValueError("out must be float32, bfloat16 or float16")
     if lse is not None and (lse.dtype != torch.float32 or not lse.is_cuda or lse.shape != (T, heads_q) or
                             not lse.is_contiguous()):
         raise ValueError(f"lse must be a contiguous float32 CUDA tensor [{T}, {heads_q}]")
     if workspace is None:
-        need = qattn_workspace_size(cache, batch, heads_q)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    _check(lib().qattn_forward(cache._ref, batch._ref, q.data_ptr(), ldq, heads_q, D ** -0.5 if scale is None else scale,
-                               out.data_ptr(), ldo, _DTYPES[out.dtype], _ptr(lse), _ptr(workspace),
-                               0 if workspace is None else workspace.numel(), _stream(stream)), "qattn_forward")
+        workspace = torch.empty(qattn_workspace_size(cache, batch, heads_q), dtype=torch.uint8, device=cache.device)
+    st = lib().qattn_forward(cache._ref, batch._ref, q.data_ptr(), ldq, heads_q, D ** -0.5 if scale is None else scale,
+                             out.data_ptr(), ldo, _DTYPES[out.dtype], None if lse is None else lse.data_ptr(),
+                             workspace.data_ptr() or None, workspace.numel() * workspace.element_size(),
+                             _raw_stream(stream, cache.device.index))
+    if st != QG_OK:
+        _check(st, "qattn_forward")
     return out

@@ -5,6 +5,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <type_traits>
 #include <atomic>
 
 namespace qg {
@@ -20,16 +21,18 @@ enum Path { kRows, kTiles };
 struct Plan {
     bool shared;                      // the prefix once for all rows, apart from the own tokens
     Path prefix_path, own_path;       // kernel of each (own_path: of prefix and own together when not shared)
-    int prefix_parts, prefix_tiles;   // parts and tiles or blocks of one (shared)
+    Deal deal;                        // shared, by tiles: the prefix's work, on so many CTAs
+    int ctas;
+    int prefix_parts, prefix_tiles;   // parts, and tiles of one (by rows)
     int own_parts, own_tiles;         // the same of the own tokens, or of prefix and own together
     int parts;                        // in all; 1: no joining, results are written at once
 };
 
 // Parts of `tiles` tiles for `units` independent units of work: enough for
-// two CTAs on each SM, none below four tiles.
+// three CTAs on each SM, none below four tiles.
 void split(int64_t units, int64_t tiles, int* parts, int* per)
 {
-    const int64_t want = std::max<int64_t>(1, ceil_div(2 * num_sms(), std::max<int64_t>(1, units)));
+    const int64_t want = std::max<int64_t>(1, ceil_div(3 * num_sms(), std::max<int64_t>(1, units)));
     const int64_t most = std::max<int64_t>(1, tiles / 4);
     const int64_t n = std::min(want, most);
     *per = (int)std::max<int64_t>(1, ceil_div(tiles, n));
@@ -59,6 +62,56 @@ void split_tiles(int64_t units, int64_t blocks, int* parts, int* per)
     }
 }
 
+// The shared prefix dealt to `ctas` CTAs, none with less than two blocks.
+Deal make_deal(const qg_kv_cache& c, const qg_kv_batch& b, int64_t group, int ctas)
+{
+    Deal d{};
+    d.per = tile_tokens(group);
+    d.heads = c.heads_kv;
+    d.blocks = (int)ceil_div(b.prefix_len, kBlock);
+    const int64_t line = (int64_t)d.heads * d.blocks, tiles = ceil_div(b.tokens, d.per);
+    const int64_t most = std::max<int64_t>(1, std::min(line / 2, ((int64_t)1 << 31) / line - 1));
+    d.pairs = (int)(tiles / 2);
+    d.single = (int)(tiles % 2);
+    // CTAs in proportion to the work: a pair of tiles 2, a single one 1
+    if (d.pairs) d.groups = (int)std::min<int64_t>(most, std::max<int64_t>(1, 2 * (int64_t)ctas / tiles));
+    if (d.single) d.sgroups = (int)std::min<int64_t>(most, std::max<int64_t>(1, ctas - (int64_t)d.pairs * d.groups));
+    return d;
+}
+
+// CTAs (one an SM) for the shared prefix, so that the own tokens' kernel, which
+// runs beside on the other SMs and takes over the rest when they end, ends
+// with them.  In microseconds: a CTA of the tile kernel takes about 10 and
+// then 1.45 for a block and a pair of tiles, 1.2 for a single tile (bound by
+// its loads), two thirds of that with 64-wide heads, slowed by up to 0.7
+// where the other kernel has the memory; the row kernel streams 6.4 TB/s of
+// own tokens (which fill half of max_kv, say) and takes 0.006 a CTA.  Measured
+// over 32 to 152 CTAs: 256 sequences over 8192 + 1024 keys best at 64 (134 us,
+// 158 on all SMs), 64 over 32768 + 2048 at 96 to 112 (103, 120), 128 over 131072 +
+// 2048 at 136 (429, 446), 32 over 2011 + 700 with a key/value head per query
+// head at 32 (48, 56).
+int choose_ctas(const qg_kv_cache& c, const qg_kv_batch& b, int64_t group, int64_t own_ctas)
+{
+    const double sms = num_sms(), dim = c.head_dim == 128 ? 1.0 : 0.67;
+    const double own = 5.0 + 0.5 * b.sequences * b.max_kv * c.heads_kv * c.head_dim * 4 / 6.4e6 + 0.006 * own_ctas;
+    int best = num_sms();
+    double least = 1e30;
+    for (int x = num_sms(); x >= 8; x -= 4) {
+        const Deal d = make_deal(c, b, group, x);
+        const double line = (double)d.heads * d.blocks, rounds = (double)ceil_div(d.slots(), x);
+        const double each = dim * rounds * std::max(d.pairs ? 1.45 * line / d.groups : 0.0, d.single ? 1.2 * line / d.sgroups : 0.0);
+        const double busy = std::min(x, d.slots());
+        const double tile_end = (10.0 + each) * (1.0 + 0.7 * (sms - busy) / sms);
+        const double all_end = own + (10.0 + each) * busy / sms;
+        const double end = std::max(tile_end, all_end);
+        if (end < least) {
+            least = end;
+            best = x;
+        }
+    }
+    return best;
+}
+
 Plan make_plan(const qg_kv_cache& c, const qg_kv_batch& b, int heads_q)
 {
     Plan p{};
@@ -76,12 +129,15 @@ Plan make_plan(const qg_kv_cache& c, const qg_kv_batch& b, int heads_q)
         p.own_path = kRows;
         if (tiles) {
             p.prefix_path = kTiles;
-            split_tiles(ceil_div(b.tokens, per2) * c.heads_kv, ceil_div(b.prefix_len, kBlock), &p.prefix_parts, &p.prefix_tiles);
+            split(own_units, ceil_div(b.max_kv, kTile), &p.own_parts, &p.own_tiles);
+            p.ctas = choose_ctas(c, b, group, own_units * p.own_parts);
+            p.deal = make_deal(c, b, group, p.ctas);
+            p.prefix_parts = p.deal.most_pieces();
         } else {
             p.prefix_path = kRows;
             split(c.heads_kv * ceil_div(group * b.tokens, 64), ceil_div(b.prefix_len, kTile), &p.prefix_parts, &p.prefix_tiles);
+            split(own_units, ceil_div(b.max_kv, kTile), &p.own_parts, &p.own_tiles);
         }
-        split(own_units, ceil_div(b.max_kv, kTile), &p.own_parts, &p.own_tiles);
     } else {
         p.own_path = kRows;
         split(own_units, ceil_div(b.prefix_len, kTile) + ceil_div(b.max_kv, kTile), &p.own_parts, &p.own_tiles);
@@ -97,65 +153,80 @@ size_t part_o_bytes(const Plan& p, int64_t rows, int dim)
 
 // out[r] = sum_p w_p o_p / sum_p w_p l_p with w_p = 2^(m_p - max m), in the
 // order of the parts: one warp a row, a lane 4 (or 2) of the row's values.
-// Reads every part once: bound by L2, where the parts were just written.
+// Bound by latency (the parts were just written and are in L2): the (m, l)
+// and the values of the first four parts are loaded at once, before anything
+// that decides whether they are wanted.
 template <int D>
-__global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ Args a, int parts)
+__global__ void __launch_bounds__(256, 6) k_attn_join(const __grid_constant__ Args a, const __grid_constant__ Deal d,
+                                                      int part0, int parts)
 {
+    using Vec = typename std::conditional<D == 128, float4, float2>::type;
+    constexpr int AT_ONCE = 4;
     kv::pdl_wait();
     kv::pdl_release();
     const int lane = threadIdx.x & 31;
     const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int t = (int)(row / a.heads_q), hq = (int)(row % a.heads_q);
-    if (row >= a.rows || t >= kv::used_tokens(a.bt)) return;
-    float m = -INFINITY, l = 0.0f;
-    for (int p = lane; p < parts; p += 32) {
-        const float2 v = __ldcg(a.part_ml + p * a.rows + row);
-        if (v.y > 0.0f) m = fmaxf(m, v.x);
+    if (row >= a.rows) return;
+    const int t = (int)((uint32_t)row / (uint32_t)a.heads_q), hq = (int)row - t * a.heads_q;
+    // pieces of the prefix first, then the other parts
+    int pieces = 0;
+    if (d.blocks) pieces = d.pieces(hq / a.group, t < d.pairs * 2 * d.per ? d.groups : d.sgroups);
+    const int n = pieces + parts;
+    auto slot = [&](int p) { return (long long)(p < pieces ? p : part0 + p - pieces) * a.rows + row; };
+    auto load_ml = [&](int p) { return p < n ? __ldcg(a.part_ml + slot(p)) : make_float2(-INFINITY, 0.0f); };
+    auto load_o = [&](int p0, Vec (&v)[AT_ONCE]) {   // where a part saw nothing its values are unset, and are not used
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; i++)
+            if (p0 + i < n) v[i] = __ldcg(reinterpret_cast<const Vec*>(a.part_o + slot(p0 + i) * D) + lane);
+    };
+    float2 ml = load_ml(lane);
+    Vec v[AT_ONCE];
+    load_o(0, v);
+    const int used = kv::used_tokens(a.bt);
+    float m = ml.y > 0.0f ? ml.x : -INFINITY, l = 0.0f;
+    for (int p = 32 + lane; p < n; p += 32) {
+        const float2 w = load_ml(p);
+        if (w.y > 0.0f) m = fmaxf(m, w.x);
     }
 #pragma unroll
     for (int i = 16; i > 0; i /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int base = 0; base < parts; base += 32) {
-        float w = 0.0f, part_l = 0.0f;
-        if (base + lane < parts) {
-            const float2 v = __ldcg(a.part_ml + (base + lane) * a.rows + row);
-            if (v.y > 0.0f) {
-                w = exp2_approx(v.x - m);
-                part_l = v.y * w;
-            }
+    float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float w = ml.y > 0.0f ? exp2_approx(ml.x - m) : 0.0f;
+    for (int p0 = 0; p0 < n; p0 += AT_ONCE) {
+        if (p0 && p0 % 32 == 0) {
+            ml = load_ml(p0 + lane);
+            w = ml.y > 0.0f ? exp2_approx(ml.x - m) : 0.0f;
         }
-        const int n = min(32, parts - base);
-#pragma unroll 4
-        for (int p = 0; p < n; p++) {
-            const float wp = __shfl_sync(0xffffffffu, w, p);
-            l += __shfl_sync(0xffffffffu, part_l, p);
-            if (wp > 0.0f) {   // a part that saw nothing has no o
-                const float* src = a.part_o + ((base + p) * a.rows + row) * D;
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; i++) {
+            const float wp = __shfl_sync(0xffffffffu, w, (p0 + i) % 32), lp = __shfl_sync(0xffffffffu, ml.y, (p0 + i) % 32);
+            if (p0 + i < n && wp > 0.0f) {
+                l = fmaf(wp, lp, l);
+                o[0] = fmaf(wp, v[i].x, o[0]);
+                o[1] = fmaf(wp, v[i].y, o[1]);
                 if constexpr (D == 128) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4*>(src) + lane);
-                    o.x = fmaf(wp, v.x, o.x); o.y = fmaf(wp, v.y, o.y);
-                    o.z = fmaf(wp, v.z, o.z); o.w = fmaf(wp, v.w, o.w);
-                } else {
-                    const float2 v = __ldcg(reinterpret_cast<const float2*>(src) + lane);
-                    o.x = fmaf(wp, v.x, o.x); o.y = fmaf(wp, v.y, o.y);
+                    o[2] = fmaf(wp, v[i].z, o[2]);
+                    o[3] = fmaf(wp, v[i].w, o[3]);
                 }
             }
         }
+        load_o(p0 + AT_ONCE, v);
     }
+    if (t >= used) return;
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
     const long long at = t * a.ldo + (long long)hq * D;
-    if constexpr (D == 128) store_out4(a, at + 4 * lane, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-    else store_out2(a, at + 2 * lane, o.x * inv, o.y * inv);
+    if constexpr (D == 128) store_out4(a, at + 4 * lane, make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv));
+    else store_out2(a, at + 2 * lane, o[0] * inv, o[1] * inv);
     if (lane == 0) store_lse(a, row, m, l);
 }
 
 }  // namespace
 
-cudaError_t launch_join(const Args& a, int parts, cudaStream_t s)
+cudaError_t launch_join(const Args& a, const Deal& d, int part0, int parts, cudaStream_t s)
 {
     const dim3 grid((unsigned)ceil_div(a.rows, 8));
-    return a.c.dim == 128 ? kv::launch_dependent(k_attn_join<128>, grid, 256, 0, s, a, parts)
-                          : kv::launch_dependent(k_attn_join<64>, grid, 256, 0, s, a, parts);
+    return a.c.dim == 128 ? kv::launch_dependent(k_attn_join<128>, grid, 256, 0, s, a, d, part0, parts)
+                          : kv::launch_dependent(k_attn_join<64>, grid, 256, 0, s, a, d, part0, parts);
 }
 
 namespace {
@@ -179,7 +250,7 @@ qg_status encode(CUtensorMap* map, int dtype, int rank, const void* base, const 
 {
     const PFN_cuTensorMapEncodeTiled_v12000 fn = encoder();
     if (!fn) return fail(QG_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    const cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
     const CUresult r = fn(map, dtype == QG_T_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                           (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, estr,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -189,14 +260,19 @@ qg_status encode(CUtensorMap* map, int dtype, int rank, const void* base, const 
 }
 }  // namespace
 
-qg_status encode_pages(CUtensorMap* map, const qg_kv_cache& c, const void* base, int box_rows)
+qg_status encode_pages(CUtensorMap* map, const qg_kv_cache& c, const void* base, int box_rows, bool whole)
 {
     // the stride of a dimension of one entry is never used: any valid one
-    const cuuint64_t any = 16;
-    const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.heads_kv,
-                                (cuuint64_t)c.num_pages};
-    const cuuint64_t strides[3] = {(cuuint64_t)c.token_stride * 2, c.heads_kv > 1 ? (cuuint64_t)c.head_stride * 2 : any,
-                                   c.num_pages > 1 ? (cuuint64_t)c.page_stride * 2 : any};
+    const cuuint64_t any = 16, token = (cuuint64_t)c.token_stride * 2;
+    const cuuint64_t head = c.heads_kv > 1 ? (cuuint64_t)c.head_stride * 2 : any;
+    const cuuint64_t page = c.num_pages > 1 ? (cuuint64_t)c.page_stride * 2 : any;
+    const cuuint64_t places = c.page_size, heads = c.heads_kv, pages = c.num_pages, halves = c.head_dim / 64;
+    if (whole) {
+        const cuuint64_t dims[5] = {64, places, halves, heads, pages}, strides[4] = {token, 128, head, page};
+        const cuuint32_t box[5] = {64u, (cuuint32_t)box_rows, (cuuint32_t)halves, 1u, 1u};
+        return encode(map, c.dtype, 5, base, dims, strides, box);
+    }
+    const cuuint64_t dims[4] = {64 * halves, places, heads, pages}, strides[3] = {token, head, page};
     const cuuint32_t box[4] = {64u, (cuuint32_t)box_rows, 1u, 1u};
     return encode(map, c.dtype, 4, base, dims, strides, box);
 }
@@ -235,28 +311,37 @@ qg_status launch_attn(const qg_kv_cache& cache, const qg_kv_batch& batch, const 
     a.part_o = p.parts > 1 ? static_cast<float*>(ws) : nullptr;
     a.part_ml = p.parts > 1 ? reinterpret_cast<float2*>(static_cast<char*>(ws) + attn::part_o_bytes(p, a.rows, cache.head_dim))
                             : nullptr;
-    a.box_rows = std::min(cache.page_size, attn::kTile);
     a.status = device_status_ptr();
+    const bool tiles = p.shared ? p.prefix_path == attn::kTiles : p.own_path == attn::kTiles;
+    const bool rows = !(tiles && !p.shared);
+    qg_status st = QG_OK;
     CUtensorMap qmap, kmap, vmap;
-    qg_status st = attn::encode_pages(&kmap, cache, cache.k, a.box_rows);
-    if (st != QG_OK) return st;
-    st = attn::encode_pages(&vmap, cache, cache.v, a.box_rows);
-    if (st != QG_OK) return st;
-    if (p.own_path == attn::kTiles || (p.shared && p.prefix_path == attn::kTiles)) {
-        st = attn::encode_rows(&qmap, cache.dtype, q, cache.head_dim, heads_q, ldq, batch.tokens, a.group);
-        if (st != QG_OK) return st;
-    }
     cudaError_t e = cudaSuccess;
-    if (p.shared)
-        e = p.prefix_path == attn::kTiles
-                ? attn::launch_tiles(a, cache.dtype, qmap, kmap, vmap, attn::kPrefix, 0, p.prefix_parts, p.prefix_tiles, s)
-                : attn::launch_rows(a, cache.dtype, kmap, vmap, attn::kPrefix, 0, p.prefix_parts, p.prefix_tiles, s);
-    const int keys = p.shared ? attn::kOwn : attn::kPrefix | attn::kOwn;
-    if (e == cudaSuccess)
-        e = p.own_path == attn::kTiles
-                ? attn::launch_tiles(a, cache.dtype, qmap, kmap, vmap, keys, p.prefix_parts, p.own_parts, p.own_tiles, s)
-                : attn::launch_rows(a, cache.dtype, kmap, vmap, keys, p.prefix_parts, p.own_parts, p.own_tiles, s);
-    if (e == cudaSuccess && p.parts > 1) e = attn::launch_join(a, p.parts, s);
+    if (tiles) {
+        a.box_rows = std::min(cache.page_size, attn::kBlock / 2);
+        st = attn::encode_rows(&qmap, cache.dtype, q, cache.head_dim, heads_q, ldq, batch.tokens, a.group);
+        if (st == QG_OK) st = attn::encode_pages(&kmap, cache, cache.k, a.box_rows, false);
+        if (st == QG_OK) st = attn::encode_pages(&vmap, cache, cache.v, a.box_rows, false);
+        if (st != QG_OK) return st;
+        e = p.shared ? attn::launch_tiles_shared(a, cache.dtype, qmap, kmap, vmap, p.deal, p.ctas, s)
+                     : attn::launch_tiles(a, cache.dtype, qmap, kmap, vmap, p.own_parts, p.own_tiles, s);
+    }
+    if (rows) {
+        a.box_rows = std::min(cache.page_size, attn::kTile);
+        st = attn::encode_pages(&kmap, cache, cache.k, a.box_rows, true);
+        if (st == QG_OK) st = attn::encode_pages(&vmap, cache, cache.v, a.box_rows, true);
+        if (st != QG_OK) return st;
+        if (e == cudaSuccess && p.shared && !tiles)
+            e = attn::launch_rows(a, cache.dtype, kmap, vmap, attn::kPrefix, 0, p.prefix_parts, p.prefix_tiles, false, s);
+        if (e == cudaSuccess)
+            e = attn::launch_rows(a, cache.dtype, kmap, vmap, p.shared ? attn::kOwn : attn::kPrefix | attn::kOwn,
+                                  p.prefix_parts, p.own_parts, p.own_tiles, tiles, s);
+    }
+    if (e == cudaSuccess && p.parts > 1) {
+        // parts of the row kernel follow one another from 0 on when the prefix was not dealt to tiles
+        const bool dealt = p.shared && tiles;
+        e = attn::launch_join(a, p.deal, dealt ? p.prefix_parts : 0, dealt ? p.own_parts : p.parts, s);
+    }
     if (e != cudaSuccess) return cuda_fail(e, "qattn_forward launch");
     return QG_OK;
 }

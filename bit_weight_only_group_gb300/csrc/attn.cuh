@@ -34,7 +34,7 @@ struct Args {
     float* part_o;
     float2* part_ml;
     long long rows;              // T * heads_q
-    int box_rows;                // key rows of one TMA box
+    int box_rows;                // key rows of one TMA box of the kernel launched
     int* status;
 };
 
@@ -60,6 +60,25 @@ __device__ __forceinline__ void store_out4(const Args& a, long long at, float4 v
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
             make_uint2(kv::pack2<__half>(v.x, v.y), kv::pack2<__half>(v.z, v.w));
 }
+// Eight fp32 values (as bits).
+__device__ __forceinline__ void store_out8(const Args& a, long long at, const uint32_t* v)
+{
+    const float* f = reinterpret_cast<const float*>(v);
+    if (a.out_type == QG_T_F32) {
+        float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
+        p[0] = make_float4(f[0], f[1], f[2], f[3]);
+        p[1] = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+        uint4 w;
+        if (a.out_type == QG_T_BF16)
+            w = make_uint4(kv::pack2<__nv_bfloat16>(f[0], f[1]), kv::pack2<__nv_bfloat16>(f[2], f[3]),
+                           kv::pack2<__nv_bfloat16>(f[4], f[5]), kv::pack2<__nv_bfloat16>(f[6], f[7]));
+        else
+            w = make_uint4(kv::pack2<__half>(f[0], f[1]), kv::pack2<__half>(f[2], f[3]), kv::pack2<__half>(f[4], f[5]),
+                           kv::pack2<__half>(f[6], f[7]));
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at) = w;
+    }
+}
 __device__ __forceinline__ void store_lse(const Args& a, long long row, float m, float l)
 {
     if (a.lse) a.lse[row] = l > 0.0f ? kLn2 * (m + log2f(l)) : -INFINITY;
@@ -82,6 +101,16 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, int c4,
+                                            uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, "
+        "%6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
+        : "memory");
+}
+
 // Page number of entry e of a table of n entries; num_pages (a box past the
 // tensor, which TMA fills with zeros) where there is none to follow.
 __device__ __forceinline__ int page_of(const Args& a, const int* table, int n, int e)
@@ -93,22 +122,61 @@ __device__ __forceinline__ int page_of(const Args& a, const int* table, int n, i
 }
 
 // Host side.
-// Map of K or V pages: dimensions (dim, place, head, page), boxes of 64 values x box_rows places.
-qg_status encode_pages(CUtensorMap* map, const qg_kv_cache& c, const void* base, int box_rows);
+// Maps of K or V pages.  whole: dimensions (64 values, place, half of the
+// head, head, page), boxes of box_rows places of a whole head; else (dim,
+// place, head, page), boxes of 64 values x box_rows places.
+qg_status encode_pages(CUtensorMap* map, const qg_kv_cache& c, const void* base, int box_rows, bool whole);
 // Map of the query rows: dimensions (dim, head, token), boxes of 64 values x a group x a tile's tokens.
 qg_status encode_rows(CUtensorMap* map, int dtype, const void* q, int dim, int heads_q, int64_t ldq, int64_t tokens,
                       int group);
 
+// How the tile kernel's work on a shared prefix is dealt: a pair of tiles
+// (256 rows) is worked on by `groups` CTAs, each taking an equal run of the
+// blocks of all heads laid end to end, so a head's blocks fall into pieces, one
+// part each.  CTAs of different pairs in the same group run over the same
+// blocks at the same time and share their loads in L2.  A last, single tile
+// (half the work) has groups of its own.
+struct Deal {
+    int per;                  // tokens of a tile
+    int pairs, groups;        // full pairs of tiles
+    int single, sgroups;      // 1: a tile is left over, and its groups
+    int blocks;               // blocks of a head
+    int heads;
+    // (every product below fits 32 bits: launches keep line * CTAs below 2^31)
+    __host__ __device__ uint32_t line() const { return (uint32_t)heads * blocks; }
+    __host__ __device__ int slots() const { return pairs * groups + (single ? sgroups : 0); }
+    // first block of group g of G, and the group a block belongs to
+    __host__ __device__ int start(uint32_t g, uint32_t G) const { return (int)(g * line() / G); }
+    __host__ __device__ int group_of(uint32_t block, uint32_t G) const { return (int)(((block + 1) * G - 1) / line()); }
+    // pieces of head h, and a bound for any head
+    __host__ __device__ int pieces(int h, int G) const
+    {
+        return group_of((h + 1) * blocks - 1, G) - group_of(h * blocks, G) + 1;
+    }
+    __host__ __device__ int most_pieces() const
+    {
+        const int G = single && sgroups > groups ? sgroups : groups;
+        const int n = (G + heads - 1) / heads + 1;
+        return n < blocks ? n : blocks;
+    }
+};
+
 // The kernels' launches.  A keys flag says what a row sees: the shared
 // prefix, its own sequence's tokens, or both in that order.
 enum Keys { kPrefix = 1, kOwn = 2 };
+// beside: launched right after launch_tiles of the same call, whose results it does not use, to run at its side.
 cudaError_t launch_rows(const Args& a, int dtype, const CUtensorMap& kmap, const CUtensorMap& vmap, int keys,
-                        int part0, int parts, int tiles_per_part, cudaStream_t s);
+                        int part0, int parts, int tiles_per_part, bool beside, cudaStream_t s);
 // Tokens of a tile of the tile kernel (its rows: that times the group, at most 128).
 inline int tile_tokens(int64_t group) { return (int)(128 / group); }
+// The shared prefix for all tokens, dealt to at most `ctas` CTAs, parts 0 .. most_pieces() - 1.
+cudaError_t launch_tiles_shared(const Args& a, int dtype, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                                const CUtensorMap& vmap, const Deal& d, int ctas, cudaStream_t s);
+// Each sequence's tokens over prefix and own tokens, the keys in `parts` parts.
 cudaError_t launch_tiles(const Args& a, int dtype, const CUtensorMap& qmap, const CUtensorMap& kmap,
-                         const CUtensorMap& vmap, int keys, int part0, int parts, int blocks_per_part, cudaStream_t s);
-cudaError_t launch_join(const Args& a, int parts, cudaStream_t s);
+                         const CUtensorMap& vmap, int parts, int blocks_per_part, cudaStream_t s);
+// Joins, for each row, the pieces of `d` (none when d.blocks = 0) and `parts` parts from part0 on.
+cudaError_t launch_join(const Args& a, const Deal& d, int part0, int parts, cudaStream_t s);
 
 }  // namespace attn
 }  // namespace qg

@@ -24,16 +24,17 @@ namespace {
 constexpr int KT = 64;                       // keys of a stage
 constexpr int kWarps = 4;                    // consumer warps; warp 4 issues the loads
 constexpr int kThreads = (kWarps + 1) * 32;
-constexpr int kStages = 3;
 
 template <int D> struct Cfg {
-    static constexpr int TILE = KT * D * 2;              // bytes of a K or V tile: [dim / 64][key][64 values], swizzled
+    // stages in flight: with 128-wide heads two CTAs an SM (registers) and three stages of 32 KB each stream 6.3 TB/s,
+    // three CTAs of two stages (128 registers, a few spilled) 5.6; with 64-wide heads three CTAs of four 16 KB stages
+    static constexpr int MAX_STAGES = D == 128 ? 3 : 4;
+    static constexpr int TILE = KT * D * 2;              // bytes of a K or V tile: per box [dim / 64][key][64 values], swizzled
     static constexpr int STAGE = 2 * TILE;
-    static constexpr int OFF_BAR = kStages * STAGE;
-    static constexpr int OFF_ML = OFF_BAR + 128;         // (m, l) of the joining warps' rows
-    static constexpr int SMEM = OFF_ML + kWarps * 16 * 8 + 1024;
+    static constexpr int OFF_ML = 2 * 8 * MAX_STAGES;    // after the barriers: (m, l) of the joining warps' rows
+    static constexpr int REST = OFF_ML + kWarps * 16 * 8 + 1024;   // barriers, (m, l), alignment
     // the joining buffers (2 slots of 16 x D fp32) lie over the stages
-    static_assert(2 * 16 * D * 4 <= kStages * STAGE, "joining buffers fit the stages");
+    static_assert(2 * 16 * D * 4 <= STAGE, "joining buffers fit the stages");
 };
 
 template <typename T>
@@ -109,17 +110,18 @@ __device__ __forceinline__ Item find_item(const Args& a, int unit, int row_block
 }
 
 template <typename T, int D, int RW, int KEYS>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
     k_attn_rows(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                const __grid_constant__ Args a, int part0, int parts, int tiles_per_part, int row_blocks)
+                const __grid_constant__ Args a, int part0, int parts, int tiles_per_part, int row_blocks,
+                int stages, int beside)
 {
     using C = Cfg<D>;
     constexpr int KW = kWarps / RW, NK = KT / KW, HALVES = D / 64;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
-    const uint32_t sbase = ptx::smem_u32(smem), bars = sbase + C::OFF_BAR;
+    const uint32_t sbase = ptx::smem_u32(smem), bars = sbase + stages * C::STAGE;
     auto full = [&](int s) { return bars + 8 * s; };
-    auto empty = [&](int s) { return bars + 8 * (kStages + s); };
+    auto empty = [&](int s) { return bars + 8 * (C::MAX_STAGES + s); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // neighbouring CTAs take the heads of one unit (their rows of a page lie together when tokens come first)
@@ -131,13 +133,16 @@ __global__ void __launch_bounds__(kThreads)
     const int row_block = x % row_blocks, unit = x / row_blocks;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; s++) { ptx::mbar_init(full(s), 1); ptx::mbar_init(empty(s), kWarps); }
+        for (int s = 0; s < stages; s++) { ptx::mbar_init(full(s), 1); ptx::mbar_init(empty(s), kWarps); }
         ptx::fence_mbar_init();
     }
     if (warp == kWarps && lane == 0) { ptx::prefetch_tensormap(&kmap); ptx::prefetch_tensormap(&vmap); }
     __syncthreads();
-    kv::pdl_wait();
+    // beside: the kernel ahead writes nothing this one reads or writes, and started only after everything before it
+    // had finished; then one CTA alone waits for it, so that this kernel does not finish first
+    if (!beside) kv::pdl_wait();
     kv::pdl_release();
+    if (beside && blockIdx.x == gridDim.x - 1) kv::pdl_wait();
     const Item it = find_item<KEYS>(a, unit, row_block, part, tiles_per_part, 16 * RW, threadIdx.x == 0);
     if (it.rows == 0) return;
     bool ok = true;
@@ -147,9 +152,8 @@ __global__ void __launch_bounds__(kThreads)
     if (warp == kWarps) {
         // ------------------------------------------------ loads: one lane per box
         const int boxes = KT / a.box_rows;                       // key ranges of a tile, each a page's rows
-        const int mine = lane % boxes, what = lane / boxes;      // what: 64-value half and K or V
-        const bool busy = what < 2 * HALVES;
-        const int half = what % HALVES, is_v = what / HALVES;
+        const int mine = lane % boxes, is_v = lane / boxes;
+        const bool busy = is_v < 2;
         const int* own_table = (KEYS & kOwn) ? a.bt.table + (long long)it.b * a.bt.table_ld : nullptr;
         const int n_prefix = (it.prefix + (1 << a.c.page_shift) - 1) >> a.c.page_shift;
         auto page_at = [&](int j) -> int {   // page of this lane's box of tile j
@@ -166,15 +170,15 @@ __global__ void __launch_bounds__(kThreads)
             ok = __all_sync(0xffffffffu, ptx::mbar_wait(empty(s), ph ^ 1u));
             if (!ok) break;
             const int used = (tile_keys(j) + a.box_rows - 1) / a.box_rows;
-            if (lane == 0) ptx::mbar_expect_tx(full(s), (uint32_t)(used * 2 * HALVES * a.box_rows * 128));
+            if (lane == 0) ptx::mbar_expect_tx(full(s), (uint32_t)(used * a.box_rows * (4 * D)));
             __syncwarp();
             if (busy && mine < used) {
                 const int key = (j < it.np ? j : j - it.np) * KT + mine * a.box_rows;
-                const uint32_t dst = sbase + s * C::STAGE + is_v * C::TILE + half * (KT * 128) + mine * a.box_rows * 128;
-                tma_load_4d(dst, is_v ? &vmap : &kmap, half * 64, key & ((1 << a.c.page_shift) - 1), head, page, full(s));
+                tma_load_5d(sbase + s * C::STAGE + is_v * C::TILE + mine * a.box_rows * (2 * D), is_v ? &vmap : &kmap, 0,
+                            key & ((1 << a.c.page_shift) - 1), 0, head, page, full(s));
             }
             page = next;
-            if (++s == kStages) { s = 0; ph ^= 1u; }
+            if (++s == stages) { s = 0; ph ^= 1u; }
         }
     } else {
         // ------------------------------------------------ products
@@ -199,19 +203,27 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int i = 0; i < D / 8; i++) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
-        // shared-memory rows of the ldmatrix lanes
+        // shared-memory offsets of the ldmatrix lanes' rows, for each 16 keys; halves of the head are `half` apart
+        const uint32_t half = (uint32_t)a.box_rows * 128;
+        uint32_t koff[NK / 16], voff[NK / 16];
         const int krow = (lane / 16) * 8 + lane % 8, kchunk = (lane / 8) % 2;
         const int vrow = ((lane / 8) % 2) * 8 + lane % 8, vchunk = lane / 16;
+#pragma unroll
+        for (int n = 0; n < NK / 16; n++) {
+            const int box = (k0 + 16 * n) / a.box_rows, in = (k0 + 16 * n) % a.box_rows;   // 16 keys lie in one box
+            koff[n] = box * (half * HALVES) + (in + krow) * 128;
+            voff[n] = C::TILE + box * (half * HALVES) + (in + vrow) * 128;
+        }
 
         int s = 0;
         uint32_t ph = 0;
-        for (int j = it.tile0; j < it.tile1 && ok; j++) {
+        for (int j = it.tile0; j < it.tile1; j++) {
             ok = __all_sync(0xffffffffu, ptx::mbar_wait(full(s), ph));
             if (!ok) break;
-            const uint32_t kt = sbase + s * C::STAGE, vt = kt + C::TILE;
+            const uint32_t kt = sbase + s * C::STAGE;
             // keys k0 .. k0 + vis - 1 of the tile are seen by the row
-            int vis0 = tile_keys(j) - k0, vis1 = vis0;
-            const int any = vis0;   // ... by any row
+            const int any = tile_keys(j) - k0;   // ... by any row
+            int vis0 = any, vis1 = any;
             if (j >= it.np) {
                 const int base = (j - it.np) * KT + k0;
                 vis0 = it.own0 + (tok0 - it.t0) - base;
@@ -220,11 +232,12 @@ __global__ void __launch_bounds__(kThreads)
             if (any > 0) {
                 if (any < NK) {
                     // V rows past the last key: whatever the page or an older tile left there times a
-                    // probability of 0 must be 0
-                    for (int i = lane; i < (NK - max(any, 0)) * HALVES * 8; i += 32) {
+                    // probability of 0 must be 0 (the row warps of a stage write the same zeros)
+                    for (int i = lane; i < (NK - any) * HALVES * 8; i += 32) {
                         const int row = k0 + any + i / (HALVES * 8), c = i % (HALVES * 8);
-                        *reinterpret_cast<uint4*>(smem + s * C::STAGE + C::TILE + (c / 8) * (KT * 128) + row * 128 + (c % 8) * 16) =
-                            make_uint4(0u, 0u, 0u, 0u);
+                        const uint32_t off = s * C::STAGE + C::TILE + (row / a.box_rows) * (half * HALVES) + (c / 8) * half +
+                                             (row % a.box_rows) * 128 + (c % 8) * 16;
+                        *reinterpret_cast<uint4*>(smem + off) = make_uint4(0u, 0u, 0u, 0u);
                     }
                     ptx::fence_proxy_async();   // the slot's next TMA write comes after these
                     __syncwarp();
@@ -236,9 +249,8 @@ __global__ void __launch_bounds__(kThreads)
                 for (int i = 0; i < D / 16; i++) {
 #pragma unroll
                     for (int n = 0; n < NK / 16; n++) {
-                        const int row = k0 + 16 * n + krow, ch = (2 * i + kchunk) % 8;
                         uint32_t kf[4];
-                        ldsm4(kf, kt + (i / 4) * (KT * 128) + row * 128 + ((ch ^ (row & 7)) << 4));
+                        ldsm4(kf, kt + koff[n] + (i / 4) * half + ((((2 * i + kchunk) % 8) ^ (lane & 7)) << 4));
                         mma16816<T>(sc[2 * n], qf[i], kf[0], kf[1]);
                         mma16816<T>(sc[2 * n + 1], qf[i], kf[2], kf[3]);
                     }
@@ -294,9 +306,8 @@ __global__ void __launch_bounds__(kThreads)
                 for (int n = 0; n < NK / 16; n++) {
 #pragma unroll
                     for (int i = 0; i < D / 16; i++) {
-                        const int row = k0 + 16 * n + vrow, ch = (2 * i + vchunk) % 8;
                         uint32_t vf[4];
-                        ldsm4t(vf, vt + (i / 4) * (KT * 128) + row * 128 + ((ch ^ (row & 7)) << 4));
+                        ldsm4t(vf, kt + voff[n] + (i / 4) * half + ((((2 * i + vchunk) % 8) ^ (lane & 7)) << 4));
                         mma16816<T>(o[2 * i], pf[n], vf[0], vf[1]);
                         mma16816<T>(o[2 * i + 1], pf[n], vf[2], vf[3]);
                     }
@@ -304,7 +315,7 @@ __global__ void __launch_bounds__(kThreads)
             }
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(empty(s));
-            if (++s == kStages) { s = 0; ph ^= 1u; }
+            if (++s == stages) { s = 0; ph ^= 1u; }
         }
         l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
         l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
@@ -313,7 +324,7 @@ __global__ void __launch_bounds__(kThreads)
 
         // ------------------------------------------------ join the key ranges: the upper half of the warps into the lower
         float4* slots = reinterpret_cast<float4*>(smem);
-        float2* mls = reinterpret_cast<float2*>(smem + C::OFF_ML);
+        float2* mls = reinterpret_cast<float2*>(smem + stages * C::STAGE + C::OFF_ML);
 #pragma unroll
         for (int step = KW / 2; step > 0; step /= 2) {
             consumer_sync();   // the stages, or the last step's slots, are no longer read
@@ -381,50 +392,54 @@ __global__ void __launch_bounds__(kThreads)
 
 template <typename T, int D, int RW, int KEYS>
 cudaError_t launch_one(const Args& a, const CUtensorMap& kmap, const CUtensorMap& vmap, int part0, int parts,
-                       int tiles_per_part, cudaStream_t s)
+                       int tiles_per_part, bool beside, cudaStream_t s)
 {
     auto kernel = k_attn_rows<T, D, RW, KEYS>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+    static std::atomic<unsigned long long> done{0};
+    // no more stages than tiles: more of the shared memory stays with the kernel beside
+    const int stages = std::max(1, std::min(tiles_per_part, Cfg<D>::MAX_STAGES));
+    const int smem = stages * Cfg<D>::STAGE + Cfg<D>::REST;
+    const cudaError_t e = kv::allow_smem(kernel, Cfg<D>::MAX_STAGES * Cfg<D>::STAGE + Cfg<D>::REST, done);
     if (e != cudaSuccess) return e;
     const int64_t units = (KEYS & kOwn) ? a.bt.B : 1;
     const int64_t blocks = ceil_div((int64_t)a.group * ((KEYS & kOwn) ? a.bt.max_q : a.bt.T), 16 * RW);
     const int64_t grid = units * blocks * parts * a.c.heads;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    return kv::launch_dependent(kernel, dim3((unsigned)grid), kThreads, Cfg<D>::SMEM, s, kmap, vmap, a, part0, parts,
-                                tiles_per_part, (int)blocks);
+    return kv::launch_dependent(kernel, dim3((unsigned)grid), kThreads, smem, s, kmap, vmap, a, part0, parts,
+                                tiles_per_part, (int)blocks, stages, beside ? 1 : 0);
 }
 
 template <typename T, int D, int RW>
 cudaError_t by_keys(const Args& a, const CUtensorMap& kmap, const CUtensorMap& vmap, int keys, int part0, int parts,
-                    int tiles_per_part, cudaStream_t s)
+                    int tiles_per_part, bool beside, cudaStream_t s)
 {
     switch (keys) {
-        case kPrefix: return launch_one<T, D, RW, kPrefix>(a, kmap, vmap, part0, parts, tiles_per_part, s);
-        case kOwn: return launch_one<T, D, RW, kOwn>(a, kmap, vmap, part0, parts, tiles_per_part, s);
-        default: return launch_one<T, D, RW, kPrefix | kOwn>(a, kmap, vmap, part0, parts, tiles_per_part, s);
+        case kPrefix: return launch_one<T, D, RW, kPrefix>(a, kmap, vmap, part0, parts, tiles_per_part, beside, s);
+        case kOwn: return launch_one<T, D, RW, kOwn>(a, kmap, vmap, part0, parts, tiles_per_part, beside, s);
+        default: return launch_one<T, D, RW, kPrefix | kOwn>(a, kmap, vmap, part0, parts, tiles_per_part, beside, s);
     }
 }
 
 template <typename T, int D>
 cudaError_t by_rows(const Args& a, const CUtensorMap& kmap, const CUtensorMap& vmap, int keys, int part0, int parts,
-                    int tiles_per_part, cudaStream_t s)
+                    int tiles_per_part, bool beside, cudaStream_t s)
 {
     const int64_t rows = (int64_t)a.group * (keys == kPrefix ? a.bt.T : a.bt.max_q);
-    if (rows <= 16) return by_keys<T, D, 1>(a, kmap, vmap, keys, part0, parts, tiles_per_part, s);
-    if (rows <= 32) return by_keys<T, D, 2>(a, kmap, vmap, keys, part0, parts, tiles_per_part, s);
-    return by_keys<T, D, 4>(a, kmap, vmap, keys, part0, parts, tiles_per_part, s);
+    if (rows <= 16) return by_keys<T, D, 1>(a, kmap, vmap, keys, part0, parts, tiles_per_part, beside, s);
+    if (rows <= 32) return by_keys<T, D, 2>(a, kmap, vmap, keys, part0, parts, tiles_per_part, beside, s);
+    return by_keys<T, D, 4>(a, kmap, vmap, keys, part0, parts, tiles_per_part, beside, s);
 }
 
 }  // namespace
 
 cudaError_t launch_rows(const Args& a, int dtype, const CUtensorMap& kmap, const CUtensorMap& vmap, int keys,
-                        int part0, int parts, int tiles_per_part, cudaStream_t s)
+                        int part0, int parts, int tiles_per_part, bool beside, cudaStream_t s)
 {
     if (dtype == QG_T_BF16)
-        return a.c.dim == 128 ? by_rows<__nv_bfloat16, 128>(a, kmap, vmap, keys, part0, parts, tiles_per_part, s)
-                              : by_rows<__nv_bfloat16, 64>(a, kmap, vmap, keys, part0, parts, tiles_per_part, s);
-    return a.c.dim == 128 ? by_rows<__half, 128>(a, kmap, vmap, keys, part0, parts, tiles_per_part, s)
-                          : by_rows<__half, 64>(a, kmap, vmap, keys, part0, parts, tiles_per_part, s);
+        return a.c.dim == 128 ? by_rows<__nv_bfloat16, 128>(a, kmap, vmap, keys, part0, parts, tiles_per_part, beside, s)
+                              : by_rows<__nv_bfloat16, 64>(a, kmap, vmap, keys, part0, parts, tiles_per_part, beside, s);
+    return a.c.dim == 128 ? by_rows<__half, 128>(a, kmap, vmap, keys, part0, parts, tiles_per_part, beside, s)
+                          : by_rows<__half, 64>(a, kmap, vmap, keys, part0, parts, tiles_per_part, beside, s);
 }
 
 }  // namespace attn

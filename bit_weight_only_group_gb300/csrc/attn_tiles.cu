@@ -18,8 +18,17 @@
 // end.
 //
 // The running maximum is only raised when a row's new maximum is above it by
-// more than 8 (in powers of two): P then stays below 2^8, exact in range for
-// both types, sums are fp32, and O is rescaled in few blocks instead of all.
+// more than 8 (in powers of two): P then stays below 2^8, within both types'
+// range, sums are fp32, and O is rescaled in few blocks instead of all.  P is
+// handed over in halves, so the product with V starts on the first.
+//
+// Bound by the tensor cores: a block and two tiles take 2048 clocks of
+// products (N = 128: 64 clocks each), and QK^T reads shared memory at its full
+// 128 bytes a clock.  Measured, 1024 rows over 128 Ki keys: 310 us with the
+// softmax left out, 350 with it (554 GFLOP: 1.58 PFLOP/s; the card's power
+// limit holds plain products near 1.95).  Steps of 64 keys with two S buffers
+// a stream, which need not wait for S, took 470: products of N = 64 read Q
+// twice as often.
 //
 // Warps: 0-3 softmax of stream 0, 4-7 of stream 1 (a warp may reach only the
 // 32 lanes of tensor memory its index modulo 4 names), 8 loads (one lane per
@@ -74,14 +83,33 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t next64)
            (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
-// D += A B^T with A in tensor memory, issued by one lane of the whole warp.
-__device__ __forceinline__ void mma_ts_elect(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t id, uint32_t accumulate)
+// D (+)= A B^T, A from shared or tensor memory.  One lane issues a whole run
+// of these inside a branch: electing a lane for each instruction instead
+// holds it to one every 77 to 88 clocks, where N = 128 takes 64 (8 steps of
+// K = 16: 655 against 520 clocks).
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t id, bool accumulate)
 {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
-        "r"(a), "l"(bdesc), "r"(id), "r"(accumulate)
-        : "memory");
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+                 "l"(adesc), "l"(bdesc), "r"(id), "r"((uint32_t)accumulate)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t id, bool accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+                 "r"(a), "l"(bdesc), "r"(id), "r"((uint32_t)accumulate)
+                 : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool elect_lane()
+{
+    uint32_t p;
+    asm volatile("{.reg .pred e; elect.sync _|e, 0xffffffff; selp.u32 %0, 1, 0, e;}" : "=r"(p));
+    return p != 0;
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32])
@@ -118,6 +146,31 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// 32 bytes at once: a whole sector of a thread's own row.
+__device__ __forceinline__ void store32(void* p, const uint32_t* r)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+                 "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z)
+{
+    float2 r;
+    asm("{.reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7}; "
+        "fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d;}"
+        : "=f"(r.x), "=f"(r.y) : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y)
+{
+    float2 r;
+    asm("{.reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; add.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d;}"
+        : "=f"(r.x), "=f"(r.y) : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return r;
+}
+
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar)
 {
     asm volatile(
@@ -127,9 +180,9 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// How the keys of a sequence's tokens are split (own keys).
 struct Shape {
-    int parts, blocks_per_part;   // of an item's keys
-    int part0;                    // number of the first part
+    int parts, blocks_per_part;
     int per;                      // tokens of a tile
 };
 
@@ -152,24 +205,53 @@ __device__ __forceinline__ int pairs_of(const Args& a, int b, int per2, int& t0,
     return (t1 - t0 + per2 - 1) / per2;
 }
 
-// Item i of the CTA's list, or false past the end.  marks (own keys, in
-// shared memory): pairs of tiles before every `stride`-th sequence, and in
-// all at kMarks.
+// Where a CTA is in its list of items.
+struct Cursor {
+    int i;      // slot of the deal, or number in the list
+    int head;   // next head of the slot (shared prefix), -1 at its start
+};
+
+// The CTA's next item, or false past the end.  marks (own keys, in shared
+// memory): pairs of tiles before every `stride`-th sequence, and in all at
+// kMarks.
 template <int KEYS>
-__device__ __forceinline__ bool get_item(const Args& a, const Shape& sh, const int* marks, int i, bool tell, Item& it)
+__device__ __forceinline__ bool next_item(const Args& a, const Deal& d, const Shape& sh, const int* marks, Cursor& cur,
+                                          bool tell, Item& it)
 {
-    const int per2 = 2 * sh.per;
-    int pair, t0, t1;
     it.own0 = it.own = 0;
     it.b = 0;
     it.prefix = (KEYS & kPrefix) ? a.bt.prefix_len : 0;
     it.np = (it.prefix + KB - 1) / KB;
-    if (KEYS & kOwn) {
+    if (!(KEYS & kOwn)) {
+        const int used = kv::used_tokens(a.bt);
+        for (; cur.i < d.slots(); cur.i += gridDim.x, cur.head = -1) {
+            const bool left = cur.i >= d.pairs * d.groups;   // the single tile
+            const int pair = left ? d.pairs : cur.i % d.pairs, G = left ? d.sgroups : d.groups;
+            const int g = left ? cur.i - d.pairs * d.groups : cur.i / d.pairs;
+            it.t0 = pair * 2 * d.per;
+            if (it.t0 >= used) continue;
+            const int lo = d.start(g, G), hi = d.start(g + 1, G);
+            if (cur.head < 0) cur.head = lo / d.blocks;
+            const int base = cur.head * d.blocks;
+            if (base >= hi) continue;
+            it.t1 = used;
+            it.two = used - it.t0 > d.per;
+            it.head = cur.head++;
+            it.part = g - d.group_of(base, G);
+            it.blk0 = max(lo, base) - base;
+            it.blk1 = min(hi, base + d.blocks) - base;
+            return true;
+        }
+        return false;
+    } else {
+        const int per2 = 2 * sh.per;
         // heads fastest, then parts, then pairs of tiles
+        int i = cur.i, t0, t1;
+        cur.i += gridDim.x;
         it.head = i % a.c.heads;
         i /= a.c.heads;
         it.part = i % sh.parts;
-        pair = i / sh.parts;
+        int pair = i / sh.parts;
         if (pair >= marks[kMarks]) return false;
         const int stride = (a.bt.B + kMarks - 1) / kMarks;
         int lo = 0, hi = (a.bt.B + stride - 1) / stride;   // the last mark at or before the pair
@@ -181,31 +263,19 @@ __device__ __forceinline__ bool get_item(const Args& a, const Shape& sh, const i
         pair -= marks[lo];
         it.b = lo * stride;
         for (int n; (n = pairs_of(a, it.b, per2, t0, t1)) <= pair && it.b + 1 < a.bt.B; it.b++) pair -= n;
-    } else {
-        // pairs of tiles fastest: CTAs that run together read the same blocks
-        t0 = 0;
-        t1 = kv::used_tokens(a.bt);
-        const int pairs = (t1 + per2 - 1) / per2;
-        if (pairs == 0 || i >= pairs * sh.parts * a.c.heads) return false;
-        pair = i % pairs;
-        i /= pairs;
-        it.part = i % sh.parts;
-        it.head = i / sh.parts;
-    }
-    it.t0 = t0 + pair * per2;
-    it.t1 = t1;
-    it.two = t1 - it.t0 > sh.per;
-    if (KEYS & kOwn) {
+        it.t0 = t0 + pair * per2;
+        it.t1 = t1;
+        it.two = t1 - it.t0 > sh.per;
         int len;
         const bool ok = kv::own_length(a.bt, it.b, len) && t1 - t0 <= a.bt.max_q;
         if (!ok && tell) kv::report(a.status);
         it.own0 = len - (t1 - it.t0) + 1;
         it.own = max(0, it.own0 + min(per2, t1 - it.t0) - 1);
+        const int blocks = it.np + (it.own + KB - 1) / KB;
+        it.blk0 = min(it.part * sh.blocks_per_part, blocks);
+        it.blk1 = min(it.blk0 + sh.blocks_per_part, blocks);
+        return true;
     }
-    const int blocks = it.np + (it.own + KB - 1) / KB;
-    it.blk0 = min(it.part * sh.blocks_per_part, blocks);
-    it.blk1 = min(it.blk0 + sh.blocks_per_part, blocks);
-    return true;
 }
 
 // Ring positions of an item's loads, in the order K0, K1 V0, K2 V1, ...:
@@ -217,7 +287,7 @@ template <typename T, int D, int KEYS>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_tiles(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Args a,
-                 const __grid_constant__ Shape sh)
+                 const __grid_constant__ Deal deal, const __grid_constant__ Shape sh)
 {
     using C = Cfg<D>;
     constexpr int NS = C::SLOTS, HALVES = C::HALVES;
@@ -226,13 +296,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sbase = ptx::smem_u32(smem), bars = sbase + C::OFF_BAR;
     const uint32_t q_full = bars, q_empty = bars + 8;
     auto s_full = [&](int s) { return bars + 16 + 8 * s; };     // S of stream s is in tensor memory
-    auto p_full = [&](int s) { return bars + 32 + 8 * s; };     // P is, and O may be added to
-    auto o_full = [&](int s) { return bars + 48 + 8 * s; };     // O is complete
-    const uint32_t join_full = bars + 64, join_empty = bars + 72;   // stream 1's results for stream 0 to join: ready, read
-    auto kv_full = [&](int x) { return bars + 80 + 8 * x; };
-    auto kv_empty = [&](int x) { return bars + 80 + 8 * (NS + x); };
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 80 + 16 * NS);
-    static_assert(80 + 16 * NS + 4 <= 256, "barriers");
+    auto p_full = [&](int s, int h) { return bars + 32 + 8 * (2 * s + h); };   // half h of P is, and O may be added to
+    auto o_full = [&](int s) { return bars + 64 + 8 * s; };     // O is complete
+    const uint32_t join_full = bars + 80, join_empty = bars + 88;   // stream 1's results for stream 0 to join: ready, read
+    auto kv_full = [&](int x) { return bars + 96 + 8 * x; };
+    auto kv_empty = [&](int x) { return bars + 96 + 8 * (NS + x); };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 96 + 16 * NS);
+    static_assert(96 + 16 * NS + 4 <= 256, "barriers");
     int* marks = reinterpret_cast<int*>(smem + C::OFF_UNITS);
     float2* ml1 = reinterpret_cast<float2*>(smem + C::OFF_ML);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -242,7 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_init(q_empty, 1);
         for (int s = 0; s < 2; s++) {
             ptx::mbar_init(s_full(s), 1);
-            ptx::mbar_init(p_full(s), 4);
+            ptx::mbar_init(p_full(s, 0), 4);
+            ptx::mbar_init(p_full(s, 1), 4);
             ptx::mbar_init(o_full(s), 1);
         }
         ptx::mbar_init(join_full, 4);
@@ -285,6 +356,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     bool ok = true;
     Item it;
+    Cursor cur{(int)blockIdx.x, -1};
+    const int per = (KEYS & kOwn) ? sh.per : deal.per;   // tokens of a tile
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
@@ -296,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int in_page_mask = (1 << a.c.page_shift) - 1;
             int pos = 0;                                       // loads so far
             uint32_t item_phase = 0;
-            for (int i = blockIdx.x; ok && get_item<KEYS>(a, sh, marks, i, false, it); i += gridDim.x, item_phase ^= 1u) {
+            for (; ok && next_item<KEYS>(a, deal, sh, marks, cur, false, it); item_phase ^= 1u) {
                 const int n = it.blk1 - it.blk0;
                 const int n_prefix = (it.prefix + in_page_mask) >> a.c.page_shift;
                 const int* own_table = (KEYS & kOwn) ? a.bt.table + (long long)it.b * a.bt.table_ld : nullptr;
@@ -328,12 +401,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = __all_sync(0xffffffffu, ptx::mbar_wait(q_empty, item_phase ^ 1u));
                 if (!ok) break;
                 if (lane == 0) {
-                    const uint32_t bytes = (uint32_t)(sh.per * a.group) * 128u * HALVES;
+                    const uint32_t bytes = (uint32_t)(per * a.group) * 128u * HALVES;
                     ptx::mbar_expect_tx(q_full, it.two ? 2 * bytes : bytes);
                     for (int s = 0; s < (it.two ? 2 : 1); s++)
                         for (int h = 0; h < HALVES; h++)
                             tma_load_3d(sbase + s * C::TILE + h * C::HALF, &qmap, 64 * h, it.head * a.group,
-                                        it.t0 + s * sh.per, q_full);
+                                        it.t0 + s * per, q_full);
                 }
                 __syncwarp();
                 for (int j = 1; ok && j <= n; j++) {
@@ -353,33 +426,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::tc_fence_after();
                 return r;
             };
+            const bool leader = elect_lane();   // issues the products and their commits
             auto qk = [&](int tile, int s, int pos) {
                 const uint64_t ad = ptx::sw128_desc(sbase + tile * C::TILE);
                 const uint64_t bd = ptx::sw128_desc(sbase + C::OFF_KV + (pos % NS) * C::TILE);
-    #pragma unroll
-                for (int k = 0; k < D / 16; k++) {
-                    const uint64_t off = (uint64_t)(((k / 4) * C::HALF + (k % 4) * 32) >> 4);
-                    ptx::mma_f16_elect(tmem + 128 * s, ad + off, bd + off, id_qk, k != 0);
+                if (leader) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; k++) {
+                        const uint64_t off = (uint64_t)(((k / 4) * C::HALF + (k % 4) * 32) >> 4);
+                        mma_ss(tmem + 128 * s, ad + off, bd + off, id_qk, k != 0);
+                    }
+                    commit(s_full(s));
                 }
-                ptx::tc_commit_elect(s_full(s));
             };
-            auto pv = [&](int s, int pos, bool first) {
+            // half h of P times half h of the V block
+            auto pv = [&](int s, int h, int pos, bool first) {
                 const uint64_t bd = mn_desc(sbase + C::OFF_KV + (pos % NS) * C::TILE, C::HALF);
-    #pragma unroll
-                for (int k = 0; k < KB / 16; k++)
-                    mma_ts_elect(tmem + kColO + 128 * s, tmem + 128 * s + 8 * k, bd + (uint64_t)((k * 2048) >> 4), id_pv,
-                                 !first || k != 0);
+                if (leader) {
+#pragma unroll
+                    for (int k = 4 * h; k < 4 * h + 4; k++)
+                        mma_ts(tmem + kColO + 128 * s, tmem + 128 * s + 8 * k, bd + (uint64_t)((k * 2048) >> 4), id_pv,
+                               !first || k != 0);
+                }
             };
-            auto wait_p = [&](int s) {
-                const bool r = __all_sync(0xffffffffu, ptx::mbar_wait(p_full(s), p_phase[s]));
-                p_phase[s] ^= 1u;
+            auto done = [&](uint32_t bar) {
+                if (leader) commit(bar);
+            };
+            auto wait_p = [&](int s, int h) {
+                const bool r = __all_sync(0xffffffffu, ptx::mbar_wait(p_full(s, h), p_phase[s]));
+                if (h) p_phase[s] ^= 1u;
                 ptx::tc_fence_after();
                 return r;
             };
-            for (int i = blockIdx.x; ok && get_item<KEYS>(a, sh, marks, i, false, it); i += gridDim.x, item_phase ^= 1u) {
+            for (; ok && next_item<KEYS>(a, deal, sh, marks, cur, false, it); item_phase ^= 1u) {
                 const int n = it.blk1 - it.blk0;
                 const int step = it.two ? 1 : 2;       // a stream's next block
-                auto release = [&](int pos) { ptx::tc_commit_elect(kv_empty(pos % NS)); };
+                auto release = [&](int pos) { done(kv_empty(pos % NS)); };
                 ok = __all_sync(0xffffffffu, ptx::mbar_wait(q_full, item_phase));
                 if (!ok) break;
                 if (n > 0) {
@@ -395,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         release(base + pos_k(1));
                     }
                 }
-                if (n <= step) ptx::tc_commit_elect(q_empty);   // (n = 0: at once)
+                if (n <= step) done(q_empty);   // (n = 0: at once)
                 for (int j = 0; ok && j < n; j++) {
                     const int pv_pos = base + pos_v(j, n);
                     ok = wait_kv(pv_pos);
@@ -414,12 +496,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const bool more = j + step < n;
                     const int k_pos = base + pos_k(j + step);
-    #pragma unroll
+#pragma unroll
                     for (int s = 0; s < 2; s++) {
                         if (!it.two && s != (j & 1)) continue;
-                        ok = ok && wait_p(s);
+                        ok = ok && wait_p(s, 0);
                         if (!ok) break;
-                        pv(s, pv_pos, j < step);
+                        pv(s, 0, pv_pos, j < step);
+                        ok = wait_p(s, 1);
+                        if (!ok) break;
+                        pv(s, 1, pv_pos, j < step);
                         if (!it.two || s == 1) release(pv_pos);
                         if (more) {
                             if (!it.two || s == 0) ok = wait_kv(k_pos);
@@ -427,10 +512,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             qk(it.two ? s : 0, s, k_pos);
                             if (!it.two || s == 1) {
                                 release(k_pos);
-                                if (j + step == n - 1) ptx::tc_commit_elect(q_empty);
+                                if (j + step == n - 1) done(q_empty);
                             }
                         } else {
-                            ptx::tc_commit_elect(o_full(s));
+                            done(o_full(s));
                         }
                     }
                 }
@@ -446,10 +531,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = 32 * (warp % 4) + lane;
         const int tok_in_tile = r / a.group;
         uint32_t s_phase = 0, o_phase = 0, join_phase = 0;
-        for (int i = blockIdx.x; ok && get_item<KEYS>(a, sh, marks, i, threadIdx.x == 0, it); i += gridDim.x) {
+        const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
+        while (ok && next_item<KEYS>(a, deal, sh, marks, cur, threadIdx.x == 0, it)) {
             const int n = it.blk1 - it.blk0, step = it.two ? 1 : 2;
-            const int tok = it.t0 + (it.two ? s * sh.per : 0) + tok_in_tile;
-            const bool in = tok_in_tile < sh.per && tok < it.t1;
+            const int tok = it.t0 + (it.two ? s * per : 0) + tok_in_tile;
+            const bool in = tok_in_tile < per && tok < it.t1;
             float m = -INFINITY, l = 0.0f;
             const int first = it.two ? 0 : s;
             for (int j = first; j < n; j += step) {
@@ -470,11 +556,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int e = 0; e < 32; e++)
                             if (32 * c + e >= vis) x[c][e] = 0xFF800000u;   // -inf
                 }
-                float t = __uint_as_float(x[0][0]);
+                float tm[8];   // independent maxima: no chain of 128
+#pragma unroll
+                for (int e = 0; e < 8; e++) tm[e] = __uint_as_float(x[0][e]);
 #pragma unroll
                 for (int c = 0; c < 4; c++)
 #pragma unroll
-                    for (int e = 0; e < 32; e++) t = fmaxf(t, __uint_as_float(x[c][e]));
+                    for (int e = c == 0 ? 8 : 0; e < 32; e += 16)
+#pragma unroll
+                        for (int f = 0; f < 8; f++)
+                            tm[f] = e + 8 + f < 32 ? fmaxf(fmaxf(tm[f], __uint_as_float(x[c][e + f])), __uint_as_float(x[c][(e + 8 + f) & 31]))
+                                                   : fmaxf(tm[f], __uint_as_float(x[c][e + f]));
+                float t = fmaxf(fmaxf(fmaxf(tm[0], tm[1]), fmaxf(tm[2], tm[3])), fmaxf(fmaxf(tm[4], tm[5]), fmaxf(tm[6], tm[7])));
                 t *= a.scale_log2;
                 const bool raise = t > m + kRaise || (m == -INFINITY && t > -INFINITY);
                 if (__any_sync(0xffffffffu, raise)) {
@@ -495,24 +588,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const float u = m == -INFINITY ? 0.0f : m;   // a row that has seen nothing: all terms 2^-inf
-                float sum = 0.0f;
+                const float2 u2 = make_float2(-u, -u);
+                float2 sum[4] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-                for (int c = 0; c < 4; c++) {
-                    uint32_t p[16];
+                for (int h = 0; h < 2; h++) {   // in halves: the product with V starts on the first
 #pragma unroll
-                    for (int e = 0; e < 16; e++) {
-                        const float p0 = exp2_approx(fmaf(__uint_as_float(x[c][2 * e]), a.scale_log2, -u));
-                        const float p1 = exp2_approx(fmaf(__uint_as_float(x[c][2 * e + 1]), a.scale_log2, -u));
-                        sum += p0 + p1;
-                        p[e] = kv::pack2<T>(p0, p1);
+                    for (int c = 2 * h; c < 2 * h + 2; c++) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int e = 0; e < 16; e++) {
+                            const float2 y = fma2(make_float2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])),
+                                                  scale2, u2);
+                            const float2 z = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                            sum[e & 3] = add2(sum[e & 3], z);
+                            p[e] = kv::pack2<T>(z.x, z.y);
+                        }
+                        tmem_st16(t_s + 16 * c, p);
                     }
-                    tmem_st16(t_s + 16 * c, p);
+                    tmem_st_wait();
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(p_full(s, h));
                 }
-                l += sum;
-                tmem_st_wait();
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(p_full(s));
+                sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+                l += sum[0].x + sum[0].y;
             }
             if (!ok) break;
             // ------------------------------------------------ the item's rows
@@ -549,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool final = a.part_o == nullptr;
                 const float inv = l > 0.0f ? 1.0f / l : 0.0f;
                 if (final) { w0 *= inv; w1 *= inv; }
-                const long long at = (long long)(sh.part0 + it.part) * a.rows + row;
+                const long long at = (long long)it.part * a.rows + row;
                 if (in) {
                     if (final) store_lse(a, row, m, l);
                     else a.part_ml[at] = make_float2(m, l);
@@ -575,12 +674,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int e = 0; e < 32; e++) o[e] = 0u;
                     }
                     if (!in) continue;
+                    if (!final) {
+                        if (l > 0.0f)
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 v = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
-                                                     __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
-                        if (final) store_out4(a, tok * a.ldo + (long long)hq * D + 32 * c + e, v);
-                        else if (l > 0.0f) __stcg(reinterpret_cast<float4*>(a.part_o + at * D + 32 * c + e), v);
+                            for (int e = 0; e < 32; e += 8) store32(a.part_o + at * D + 32 * c + e, o + e);
+                    } else {
+                        const long long to = tok * a.ldo + (long long)hq * D + 32 * c;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) store_out8(a, to + e, o + e);
                     }
                 }
             }
@@ -606,44 +707,43 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <typename T, int D, int KEYS>
 cudaError_t launch_one(const Args& a, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                       const Shape& sh, int64_t items, cudaStream_t s)
+                       const Deal& d, const Shape& sh, int64_t ctas, cudaStream_t s)
 {
     auto kernel = k_attn_tiles<T, D, KEYS>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e = kv::allow_smem(kernel, Cfg<D>::SMEM, done);
     if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)std::min<int64_t>(num_sms(), items);
-    return kv::launch_dependent(kernel, dim3(grid), kThreads, Cfg<D>::SMEM, s, qmap, kmap, vmap, a, sh);
+    return kv::launch_dependent(kernel, dim3((unsigned)ctas), kThreads, Cfg<D>::SMEM, s, qmap, kmap, vmap, a, d, sh);
 }
 
-template <typename T>
-cudaError_t by_shape(const Args& a, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                     const Shape& sh, int keys, int64_t items, cudaStream_t s)
+template <int KEYS>
+cudaError_t by_type(const Args& a, int dtype, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                    const Deal& d, const Shape& sh, int64_t ctas, cudaStream_t s)
 {
-    if (keys == kPrefix)
-        return a.c.dim == 128 ? launch_one<T, 128, kPrefix>(a, qmap, kmap, vmap, sh, items, s)
-                              : launch_one<T, 64, kPrefix>(a, qmap, kmap, vmap, sh, items, s);
-    return a.c.dim == 128 ? launch_one<T, 128, kPrefix | kOwn>(a, qmap, kmap, vmap, sh, items, s)
-                          : launch_one<T, 64, kPrefix | kOwn>(a, qmap, kmap, vmap, sh, items, s);
+    if (dtype == QG_T_BF16)
+        return a.c.dim == 128 ? launch_one<__nv_bfloat16, 128, KEYS>(a, qmap, kmap, vmap, d, sh, ctas, s)
+                              : launch_one<__nv_bfloat16, 64, KEYS>(a, qmap, kmap, vmap, d, sh, ctas, s);
+    return a.c.dim == 128 ? launch_one<__half, 128, KEYS>(a, qmap, kmap, vmap, d, sh, ctas, s)
+                          : launch_one<__half, 64, KEYS>(a, qmap, kmap, vmap, d, sh, ctas, s);
 }
 
 }  // namespace
 
-cudaError_t launch_tiles(const Args& a, int dtype, const CUtensorMap& qmap, const CUtensorMap& kmap,
-                         const CUtensorMap& vmap, int keys, int part0, int parts, int blocks_per_part, cudaStream_t s)
+cudaError_t launch_tiles_shared(const Args& a, int dtype, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                                const CUtensorMap& vmap, const Deal& d, int ctas, cudaStream_t s)
 {
-    Shape sh;
-    sh.parts = parts;
-    sh.blocks_per_part = blocks_per_part;
-    sh.part0 = part0;
-    sh.per = tile_tokens(a.group);
-    // pairs of tiles: a whole batch's tokens, or at most so many over the sequences
-    const int64_t pairs = keys == kPrefix ? ceil_div(a.bt.T, 2 * sh.per)
-                                          : std::min<int64_t>(a.bt.T / (2 * sh.per) + a.bt.B,
-                                                              (int64_t)a.bt.B * ceil_div(a.bt.max_q, 2 * sh.per));
+    return by_type<kPrefix>(a, dtype, qmap, kmap, vmap, d, Shape{}, std::min(ctas, d.slots()), s);
+}
+
+cudaError_t launch_tiles(const Args& a, int dtype, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                         const CUtensorMap& vmap, int parts, int blocks_per_part, cudaStream_t s)
+{
+    const Shape sh{parts, blocks_per_part, tile_tokens(a.group)};
+    // at most so many pairs of tiles over the sequences
+    const int64_t pairs = std::min<int64_t>(a.bt.T / (2 * sh.per) + a.bt.B, a.bt.B * ceil_div(a.bt.max_q, 2 * sh.per));
     const int64_t items = pairs * parts * a.c.heads;
     if (items > 0x3FFFFFFF) return cudaErrorInvalidConfiguration;
-    return dtype == QG_T_BF16 ? by_shape<__nv_bfloat16>(a, qmap, kmap, vmap, sh, keys, items, s)
-                              : by_shape<__half>(a, qmap, kmap, vmap, sh, keys, items, s);
+    return by_type<kPrefix | kOwn>(a, dtype, qmap, kmap, vmap, Deal{}, sh, std::min<int64_t>(num_sms(), items), s);
 }
 
 }  // namespace attn

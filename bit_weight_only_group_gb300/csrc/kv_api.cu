@@ -74,6 +74,8 @@ qg_status check_attn(const qg_kv_cache* cache, const qg_kv_batch* batch, int hea
     if (st != QG_OK) return st;
     if (heads_q < 1 || heads_q % cache->heads_kv)
         return fail(QG_ERR_INVALID_ARG, "%s: heads_q=%d is not a multiple of heads_kv=%d", who, heads_q, cache->heads_kv);
+    if ((int64_t)batch->prefix_len * cache->heads_kv > (int64_t)1 << 36)
+        return fail(QG_ERR_UNSUPPORTED, "%s: more than 2^36 prefix keys over all heads", who);
     if ((int64_t)batch->tokens * heads_q > (int64_t)1 << 30)
         return fail(QG_ERR_UNSUPPORTED, "%s: more than 2^30 rows", who);
     return QG_OK;

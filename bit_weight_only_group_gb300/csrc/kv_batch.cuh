@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 #include "qg_internal.h"
@@ -103,6 +104,17 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b)
 {
     const __half2 v = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Lets a kernel use `bytes` of dynamic shared memory, once per context.
+template <typename K>
+inline cudaError_t allow_smem(K kernel, int bytes, std::atomic<unsigned long long>& done)
+{
+    const unsigned long long ctx = current_context_id();
+    if (ctx && done.load(std::memory_order_acquire) == ctx) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.store(ctx, std::memory_order_release);
+    return e;
 }
 
 // Launch that may start before the kernel ahead of it on the stream has
