@@ -21,8 +21,10 @@ enum Path { kRows, kTiles };
 struct Plan {
     bool shared;                      // the prefix once for all rows, apart from the own tokens
     Path prefix_path, own_path;       // kernel of each (own_path: of prefix and own together when not shared)
-    Deal deal;                        // shared, by tiles: the prefix's work, on so many CTAs
-    int ctas;
+    Deal deal;                        // shared, by tiles: the prefix's work
+    int ctas;                         // of the tile kernel
+    int64_t pairs;                    // bound of the pairs of tiles of all sequences, and
+    int min_run;                      // least run of a CTA that keeps an item to own_parts pieces (own tokens by tiles)
     int prefix_parts, prefix_tiles;   // parts, and tiles of one (by rows)
     int own_parts, own_tiles;         // the same of the own tokens, or of prefix and own together
     int parts;                        // in all; 1: no joining, results are written at once
@@ -37,29 +39,6 @@ void split(int64_t units, int64_t tiles, int* parts, int* per)
     const int64_t n = std::min(want, most);
     *per = (int)std::max<int64_t>(1, ceil_div(tiles, n));
     *parts = (int)std::max<int64_t>(1, ceil_div(tiles, *per));
-}
-
-// Parts of `blocks` blocks for `units` pairs of tiles on one CTA an SM: the
-// count whose rounds of the whole card end soonest, an item costing its
-// blocks and about three more to start and finish, and a part's results about
-// a quarter block to write and to join.
-void split_tiles(int64_t units, int64_t blocks, int* parts, int* per)
-{
-    const int64_t sms = num_sms();
-    double best = 0;
-    *parts = 1;
-    *per = (int)std::max<int64_t>(1, blocks);
-    for (int64_t n = 1; n <= 64 && n <= std::max<int64_t>(1, blocks / 2); n++) {
-        const int64_t k = ceil_div(blocks, n);
-        if (n > 1 && ceil_div(blocks, k) != n) continue;
-        const int64_t rounds = ceil_div(units * n, sms);
-        const double cost = (double)rounds * (k + 3) + (n > 1 ? 0.25 * n * ceil_div(units, sms) : 0.0);
-        if (n == 1 || cost < best) {
-            best = cost;
-            *parts = (int)n;
-            *per = (int)std::max<int64_t>(1, k);
-        }
-    }
 }
 
 // The shared prefix dealt to `ctas` CTAs, none with less than two blocks.
@@ -112,6 +91,13 @@ int choose_ctas(const qg_kv_cache& c, const qg_kv_batch& b, int64_t group, int64
     return best;
 }
 
+// The line of prompts is counted in 32 bits.
+bool line_fits(const qg_kv_cache& c, const qg_kv_batch& b, int64_t per2)
+{
+    const int64_t pairs = b.tokens / per2 + b.sequences;
+    return pairs * (ceil_div(b.prefix_len, kBlock) + ceil_div(b.max_kv, kBlock) + 1) < ((int64_t)1 << 30) / c.heads_kv;
+}
+
 Plan make_plan(const qg_kv_cache& c, const qg_kv_batch& b, int heads_q)
 {
     Plan p{};
@@ -119,11 +105,16 @@ Plan make_plan(const qg_kv_cache& c, const qg_kv_batch& b, int heads_q)
     const bool tiles = group <= 128;   // a tile holds whole tokens
     const int64_t per2 = 2 * std::max(1, tile_tokens(group));
     const int64_t own_units = (int64_t)b.sequences * c.heads_kv * ceil_div(group * b.max_q, 64);
-    if (tiles && group * b.max_q > 64) {
-        // rows enough for tiles within a sequence: prefix and own tokens in one pass, nothing to join
+    if (tiles && group * b.max_q > 64 && line_fits(c, b, per2)) {
+        // rows enough for tiles within a sequence: prefix and own tokens in one pass
         p.own_path = kTiles;
-        const int64_t pairs = std::min<int64_t>(b.tokens / per2 + b.sequences, b.sequences * ceil_div(b.max_q, per2));
-        split_tiles(pairs * c.heads_kv, ceil_div(b.prefix_len, kBlock) + ceil_div(b.max_kv, kBlock), &p.own_parts, &p.own_tiles);
+        p.ctas = num_sms();
+        p.pairs = b.tokens / per2 + b.sequences;
+        // an item's pieces, from the run that the card gets when all the bounds are met half way
+        const int64_t np = ceil_div(b.prefix_len, kBlock), longest = std::max<int64_t>(1, np + ceil_div(b.max_kv, kBlock));
+        const int64_t fair = std::max<int64_t>(2, c.heads_kv * ceil_div(b.tokens, per2) * ((np + longest) / 2) / p.ctas);
+        p.own_parts = (int)std::min<int64_t>(32, std::max<int64_t>(2, ceil_div(longest, fair) + 1));
+        p.min_run = (int)std::max<int64_t>(2, ceil_div(longest, p.own_parts - 1));
     } else if (b.sequences > 1 && b.prefix_len >= 256) {
         p.shared = true;
         p.own_path = kRows;
@@ -146,32 +137,39 @@ Plan make_plan(const qg_kv_cache& c, const qg_kv_batch& b, int heads_q)
     return p;
 }
 
-size_t part_o_bytes(const Plan& p, int64_t rows, int dim)
+// The workspace: o of the parts, (m, l) of the parts, the layout of prompts.
+struct Places {
+    size_t ml, line, first, pair, bytes;
+};
+Places places(const Plan& p, const qg_kv_batch& b, int heads_q, int dim)
 {
-    return p.parts > 1 ? align_up((size_t)p.parts * rows * dim * 4, 256) : 0;
+    Places w{};
+    if (p.parts <= 1) return w;
+    const size_t rows = (size_t)b.tokens * heads_q;
+    w.ml = align_up(p.parts * rows * dim * 4, 256);
+    w.line = w.ml + align_up(p.parts * rows * sizeof(float2), 256);
+    w.bytes = w.line;
+    if (p.pairs) {
+        w.first = w.line + align_up(sizeof(Line), 256);
+        w.pair = w.first + align_up((size_t)(b.sequences + 1) * 4, 256);
+        w.bytes = w.pair + align_up((size_t)(p.pairs + 1) * sizeof(Pair), 256);
+    }
+    return w;
 }
 
 // out[r] = sum_p w_p o_p / sum_p w_p l_p with w_p = 2^(m_p - max m), in the
 // order of the parts: one warp a row, a lane 4 (or 2) of the row's values.
-// Bound by latency (the parts were just written and are in L2): the (m, l)
-// and the values of the first four parts are loaded at once, before anything
-// that decides whether they are wanted.
+// Part p < pieces is in slot p, the others follow from slot part0 on.  Bound
+// by latency (the parts were just written and are in L2): the (m, l) and the
+// values of the first four parts are loaded at once, before anything that
+// decides whether they are wanted.
 template <int D>
-__global__ void __launch_bounds__(256, 6) k_attn_join(const __grid_constant__ Args a, const __grid_constant__ Deal d,
-                                                      int part0, int parts)
+__device__ __forceinline__ void join_row(const Args& a, int t, int hq, int pieces, int part0, int n, const int* used)
 {
     using Vec = typename std::conditional<D == 128, float4, float2>::type;
     constexpr int AT_ONCE = 4;
-    kv::pdl_wait();
-    kv::pdl_release();
     const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (row >= a.rows) return;
-    const int t = (int)((uint32_t)row / (uint32_t)a.heads_q), hq = (int)row - t * a.heads_q;
-    // pieces of the prefix first, then the other parts
-    int pieces = 0;
-    if (d.blocks) pieces = d.pieces(hq / a.group, t < d.pairs * 2 * d.per ? d.groups : d.sgroups);
-    const int n = pieces + parts;
+    const long long row = (long long)t * a.heads_q + hq;
     auto slot = [&](int p) { return (long long)(p < pieces ? p : part0 + p - pieces) * a.rows + row; };
     auto load_ml = [&](int p) { return p < n ? __ldcg(a.part_ml + slot(p)) : make_float2(-INFINITY, 0.0f); };
     auto load_o = [&](int p0, Vec (&v)[AT_ONCE]) {   // where a part saw nothing its values are unset, and are not used
@@ -182,7 +180,7 @@ __global__ void __launch_bounds__(256, 6) k_attn_join(const __grid_constant__ Ar
     float2 ml = load_ml(lane);
     Vec v[AT_ONCE];
     load_o(0, v);
-    const int used = kv::used_tokens(a.bt);
+    const bool mine = t < (used ? min(max(__ldg(used), 0), a.bt.T) : a.bt.T);
     float m = ml.y > 0.0f ? ml.x : -INFINITY, l = 0.0f;
     for (int p = 32 + lane; p < n; p += 32) {
         const float2 w = load_ml(p);
@@ -212,12 +210,55 @@ __global__ void __launch_bounds__(256, 6) k_attn_join(const __grid_constant__ Ar
         }
         load_o(p0 + AT_ONCE, v);
     }
-    if (t >= used) return;
+    if (!mine) return;
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
     const long long at = t * a.ldo + (long long)hq * D;
     if constexpr (D == 128) store_out4(a, at + 4 * lane, make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv));
     else store_out2(a, at + 2 * lane, o[0] * inv, o[1] * inv);
     if (lane == 0) store_lse(a, row, m, l);
+}
+
+// All rows: the prefix's pieces first, then the other parts.
+template <int D>
+__global__ void __launch_bounds__(256, 6) k_attn_join(const __grid_constant__ Args a, const __grid_constant__ Deal d,
+                                                      int part0, int parts)
+{
+    kv::pdl_wait();
+    kv::pdl_release();
+    const uint32_t row = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row >= a.rows) return;
+    const int t = (int)(row / (uint32_t)a.heads_q), hq = (int)row - t * a.heads_q;
+    int pieces = 0;
+    if (d.blocks) pieces = d.pieces(hq / a.group, t < d.pairs * 2 * d.per ? d.groups : d.sgroups);
+    join_row<D>(a, t, hq, pieces, part0, pieces + parts, a.bt.cu_q ? a.bt.cu_q + a.bt.B : nullptr);
+}
+
+// The rows of items that the end of a CTA's run cut: 32 CTAs (8 rows each) for
+// each run's end, which leave the item to its first cut.
+template <int D>
+__global__ void __launch_bounds__(256, 6) k_attn_join_line(const __grid_constant__ Args a, const __grid_constant__ Layout lay)
+{
+    kv::pdl_wait();
+    kv::pdl_release();
+    const Line line = *lay.line;
+    const int c = blockIdx.x / 32 + 1;
+    if ((long long)c * line.run >= (long long)a.c.heads * line.head) return;
+    const int head = c * line.run / line.head, at = c * line.run - head * line.head;
+    int lo = 0, hi = line.pairs;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (lay.pair[mid].start <= at) lo = mid;
+        else hi = mid;
+    }
+    const Pair p = lay.pair[lo];
+    const int first = head * line.head + p.start, last = head * line.head + lay.pair[lo + 1].start - 1;
+    if (p.start == at || first / line.run != c - 1) return;
+    const int r = blockIdx.x % 32 * 8 + (threadIdx.x >> 5), t = p.t0 + r / a.group;
+    int t0, t1;
+    kv::token_range(a.bt, p.b, t0, t1);
+    if (r >= 2 * lay.per * a.group || t >= t1) return;
+    const int n = last / line.run - first / line.run + 1;
+    join_row<D>(a, t, head * a.group + r % a.group, n, 0, n, nullptr);
 }
 
 }  // namespace
@@ -227,6 +268,14 @@ cudaError_t launch_join(const Args& a, const Deal& d, int part0, int parts, cuda
     const dim3 grid((unsigned)ceil_div(a.rows, 8));
     return a.c.dim == 128 ? kv::launch_dependent(k_attn_join<128>, grid, 256, 0, s, a, d, part0, parts)
                           : kv::launch_dependent(k_attn_join<64>, grid, 256, 0, s, a, d, part0, parts);
+}
+
+cudaError_t launch_join_line(const Args& a, const Layout& lay, cudaStream_t s)
+{
+    const dim3 grid((unsigned)(32 * (lay.ctas - 1)));
+    if (!grid.x) return cudaSuccess;
+    return a.c.dim == 128 ? kv::launch_dependent(k_attn_join_line<128>, grid, 256, 0, s, a, lay)
+                          : kv::launch_dependent(k_attn_join_line<64>, grid, 256, 0, s, a, lay);
 }
 
 namespace {
@@ -290,10 +339,7 @@ qg_status encode_rows(CUtensorMap* map, int dtype, const void* q, int dim, int h
 
 size_t attn_workspace_bytes(const qg_kv_cache& cache, const qg_kv_batch& batch, int heads_q)
 {
-    const attn::Plan p = attn::make_plan(cache, batch, heads_q);
-    const int64_t rows = (int64_t)batch.tokens * heads_q;
-    if (p.parts <= 1) return 0;
-    return attn::part_o_bytes(p, rows, cache.head_dim) + align_up((size_t)p.parts * rows * sizeof(float2), 256);
+    return attn::places(attn::make_plan(cache, batch, heads_q), batch, heads_q, cache.head_dim).bytes;
 }
 
 qg_status launch_attn(const qg_kv_cache& cache, const qg_kv_batch& batch, const void* q, int64_t ldq, int heads_q,
@@ -308,9 +354,10 @@ qg_status launch_attn(const qg_kv_cache& cache, const qg_kv_batch& batch, const 
     a.scale_log2 = scale * 1.4426950408889634f;
     a.out = out; a.ldo = ldo; a.out_type = ot; a.lse = lse;
     a.rows = (int64_t)batch.tokens * heads_q;
-    a.part_o = p.parts > 1 ? static_cast<float*>(ws) : nullptr;
-    a.part_ml = p.parts > 1 ? reinterpret_cast<float2*>(static_cast<char*>(ws) + attn::part_o_bytes(p, a.rows, cache.head_dim))
-                            : nullptr;
+    const attn::Places w = attn::places(p, batch, heads_q, cache.head_dim);
+    char* base = static_cast<char*>(ws);
+    a.part_o = p.parts > 1 ? reinterpret_cast<float*>(base) : nullptr;
+    a.part_ml = p.parts > 1 ? reinterpret_cast<float2*>(base + w.ml) : nullptr;
     a.status = device_status_ptr();
     const bool tiles = p.shared ? p.prefix_path == attn::kTiles : p.own_path == attn::kTiles;
     const bool rows = !(tiles && !p.shared);
@@ -323,8 +370,14 @@ qg_status launch_attn(const qg_kv_cache& cache, const qg_kv_batch& batch, const 
         if (st == QG_OK) st = attn::encode_pages(&kmap, cache, cache.k, a.box_rows, false);
         if (st == QG_OK) st = attn::encode_pages(&vmap, cache, cache.v, a.box_rows, false);
         if (st != QG_OK) return st;
-        e = p.shared ? attn::launch_tiles_shared(a, cache.dtype, qmap, kmap, vmap, p.deal, p.ctas, s)
-                     : attn::launch_tiles(a, cache.dtype, qmap, kmap, vmap, p.own_parts, p.own_tiles, s);
+        if (p.shared) {
+            e = attn::launch_tiles_shared(a, cache.dtype, qmap, kmap, vmap, p.deal, p.ctas, s);
+        } else {
+            const attn::Layout lay{reinterpret_cast<attn::Line*>(base + w.line), reinterpret_cast<int*>(base + w.first),
+                                   reinterpret_cast<attn::Pair*>(base + w.pair), attn::tile_tokens(a.group), p.ctas, p.min_run};
+            e = attn::launch_tiles(a, cache.dtype, qmap, kmap, vmap, lay, s);
+            if (e == cudaSuccess) e = attn::launch_join_line(a, lay, s);
+        }
     }
     if (rows) {
         a.box_rows = std::min(cache.page_size, attn::kTile);
@@ -337,7 +390,7 @@ qg_status launch_attn(const qg_kv_cache& cache, const qg_kv_batch& batch, const 
             e = attn::launch_rows(a, cache.dtype, kmap, vmap, p.shared ? attn::kOwn : attn::kPrefix | attn::kOwn,
                                   p.prefix_parts, p.own_parts, p.own_tiles, tiles, s);
     }
-    if (e == cudaSuccess && p.parts > 1) {
+    if (e == cudaSuccess && rows && p.parts > 1) {
         // parts of the row kernel follow one another from 0 on when the prefix was not dealt to tiles
         const bool dealt = p.shared && tiles;
         e = attn::launch_join(a, p.deal, dealt ? p.prefix_parts : 0, dealt ? p.own_parts : p.parts, s);

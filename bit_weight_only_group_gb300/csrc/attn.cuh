@@ -161,6 +161,31 @@ struct Deal {
     }
 };
 
+// How the tile kernel's work on prompts is dealt.  The pairs of tiles of all
+// sequences, each with the blocks its last token sees, are laid end to end for
+// a head, the heads after one another, and each CTA takes an equal run of
+// that line.  An item (a pair, a head) inside one run is written at once; one
+// that runs cross falls into pieces, one part each, joined afterwards.  The
+// lengths are on the device, so a small kernel lays the line out.
+struct Line {
+    int run;                  // blocks of a CTA
+    int head;                 // blocks of a head
+    int pairs;
+};
+struct Pair {
+    int start;                // blocks of a head before it
+    int t0;                   // its first token
+    int b;                    // its sequence
+};
+struct Layout {
+    Line* line;
+    int* first;               // [B + 1] pairs before each sequence
+    Pair* pair;               // [pairs + 1], the last one's start the end of the line
+    int per;                  // tokens of a tile
+    int ctas;
+    int min_run;
+};
+
 // The kernels' launches.  A keys flag says what a row sees: the shared
 // prefix, its own sequence's tokens, or both in that order.
 enum Keys { kPrefix = 1, kOwn = 2 };
@@ -172,11 +197,13 @@ inline int tile_tokens(int64_t group) { return (int)(128 / group); }
 // The shared prefix for all tokens, dealt to at most `ctas` CTAs, parts 0 .. most_pieces() - 1.
 cudaError_t launch_tiles_shared(const Args& a, int dtype, const CUtensorMap& qmap, const CUtensorMap& kmap,
                                 const CUtensorMap& vmap, const Deal& d, int ctas, cudaStream_t s);
-// Each sequence's tokens over prefix and own tokens, the keys in `parts` parts.
+// Each sequence's tokens over prefix and own tokens: lays the line out and works through it.
 cudaError_t launch_tiles(const Args& a, int dtype, const CUtensorMap& qmap, const CUtensorMap& kmap,
-                         const CUtensorMap& vmap, int parts, int blocks_per_part, cudaStream_t s);
+                         const CUtensorMap& vmap, const Layout& lay, cudaStream_t s);
 // Joins, for each row, the pieces of `d` (none when d.blocks = 0) and `parts` parts from part0 on.
 cudaError_t launch_join(const Args& a, const Deal& d, int part0, int parts, cudaStream_t s);
+// Joins the items of a line that fell into pieces.
+cudaError_t launch_join_line(const Args& a, const Layout& lay, cudaStream_t s);
 
 }  // namespace attn
 }  // namespace qg

@@ -50,7 +50,6 @@ constexpr int kThreads = 384;                // warps 10 and 11 only fill the th
 // 120 for the other: 2 * 192 + 120 = 3 * 168.
 constexpr int kRegsSoftmax = 192, kRegsOther = 120;
 static_assert(2 * kRegsSoftmax + kRegsOther == 3 * 168, "registers shared out are those of the launch");
-constexpr int kMarks = 128;                  // sequences whose place in the list of tile pairs is kept in shared memory
 constexpr float kRaise = 8.0f;               // see above
 
 template <int D> struct Cfg {
@@ -61,8 +60,7 @@ template <int D> struct Cfg {
     static constexpr int OFF_KV = 2 * TILE;
     static constexpr int OFF_BAR = OFF_KV + SLOTS * TILE;
     static constexpr int OFF_ML = OFF_BAR + 256;           // (m, l) of stream 1's rows (joining)
-    static constexpr int OFF_UNITS = OFF_ML + 128 * 8;
-    static constexpr int SMEM = OFF_UNITS + (kMarks + 1) * 4 + 1024 /* alignment */;
+    static constexpr int SMEM = OFF_ML + 128 * 8 + 1024 /* alignment */;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 constexpr int kTmemCols = 512, kColO = 256;  // S and P of stream s at 128 s, O at 256 + 128 s
@@ -180,12 +178,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-// How the keys of a sequence's tokens are split (own keys).
-struct Shape {
-    int parts, blocks_per_part;
-    int per;                      // tokens of a tile
-};
-
 // One item: a pair of tiles (or one) of a unit's rows, a key/value head, a part of the keys.
 struct Item {
     int head, part;
@@ -195,34 +187,25 @@ struct Item {
     int own;            // own places any row sees
     int prefix, np;     // prefix tokens, their blocks
     int blk0, blk1;     // this part's blocks
+    bool whole;         // all there are
     int b;
 };
 
-// Pairs of tiles of sequence b.
-__device__ __forceinline__ int pairs_of(const Args& a, int b, int per2, int& t0, int& t1)
-{
-    kv::token_range(a.bt, b, t0, t1);
-    return (t1 - t0 + per2 - 1) / per2;
-}
-
-// Where a CTA is in its list of items.
+// Where a CTA is in its work.
 struct Cursor {
-    int i;      // slot of the deal, or number in the list
+    int i;      // slot of the deal, or place on the line
     int head;   // next head of the slot (shared prefix), -1 at its start
 };
 
-// The CTA's next item, or false past the end.  marks (own keys, in shared
-// memory): pairs of tiles before every `stride`-th sequence, and in all at
-// kMarks.
+// The CTA's next item, or false past the end.
 template <int KEYS>
-__device__ __forceinline__ bool next_item(const Args& a, const Deal& d, const Shape& sh, const int* marks, Cursor& cur,
-                                          bool tell, Item& it)
+__device__ __forceinline__ bool next_item(const Args& a, const Deal& d, const Layout& lay, Cursor& cur, bool tell, Item& it)
 {
     it.own0 = it.own = 0;
     it.b = 0;
     it.prefix = (KEYS & kPrefix) ? a.bt.prefix_len : 0;
     it.np = (it.prefix + KB - 1) / KB;
-    if (!(KEYS & kOwn)) {
+    if constexpr (!(KEYS & kOwn)) {
         const int used = kv::used_tokens(a.bt);
         for (; cur.i < d.slots(); cur.i += gridDim.x, cur.head = -1) {
             const bool left = cur.i >= d.pairs * d.groups;   // the single tile
@@ -240,41 +223,117 @@ __device__ __forceinline__ bool next_item(const Args& a, const Deal& d, const Sh
             it.part = g - d.group_of(base, G);
             it.blk0 = max(lo, base) - base;
             it.blk1 = min(hi, base + d.blocks) - base;
+            it.whole = false;   // the own tokens are still to be joined
             return true;
         }
         return false;
     } else {
-        const int per2 = 2 * sh.per;
-        // heads fastest, then parts, then pairs of tiles
-        int i = cur.i, t0, t1;
-        cur.i += gridDim.x;
-        it.head = i % a.c.heads;
-        i /= a.c.heads;
-        it.part = i % sh.parts;
-        int pair = i / sh.parts;
-        if (pair >= marks[kMarks]) return false;
-        const int stride = (a.bt.B + kMarks - 1) / kMarks;
-        int lo = 0, hi = (a.bt.B + stride - 1) / stride;   // the last mark at or before the pair
+        const Line line = *lay.line;
+        const int end = min((int)(blockIdx.x + 1) * line.run, a.c.heads * line.head);
+        if (cur.i >= end) return false;
+        it.head = cur.i / line.head;
+        const int at = cur.i - it.head * line.head;
+        int lo = 0, hi = line.pairs;   // the pair the place lies in
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
-            if (marks[mid] <= pair) lo = mid;
+            if (lay.pair[mid].start <= at) lo = mid;
             else hi = mid;
         }
-        pair -= marks[lo];
-        it.b = lo * stride;
-        for (int n; (n = pairs_of(a, it.b, per2, t0, t1)) <= pair && it.b + 1 < a.bt.B; it.b++) pair -= n;
-        it.t0 = t0 + pair * per2;
-        it.t1 = t1;
-        it.two = t1 - it.t0 > sh.per;
+        const Pair p = lay.pair[lo];
+        const int blocks = lay.pair[lo + 1].start - p.start, first = it.head * line.head + p.start;
+        int t0;
+        it.b = p.b;
+        it.t0 = p.t0;
+        kv::token_range(a.bt, p.b, t0, it.t1);
+        it.two = it.t1 - it.t0 > lay.per;
         int len;
-        const bool ok = kv::own_length(a.bt, it.b, len) && t1 - t0 <= a.bt.max_q;
+        const bool ok = kv::own_length(a.bt, p.b, len) && it.t1 - t0 <= a.bt.max_q;
         if (!ok && tell) kv::report(a.status);
-        it.own0 = len - (t1 - it.t0) + 1;
-        it.own = max(0, it.own0 + min(per2, t1 - it.t0) - 1);
-        const int blocks = it.np + (it.own + KB - 1) / KB;
-        it.blk0 = min(it.part * sh.blocks_per_part, blocks);
-        it.blk1 = min(it.blk0 + sh.blocks_per_part, blocks);
+        it.own0 = len - (it.t1 - it.t0) + 1;
+        it.own = max(0, it.own0 + min(2 * lay.per, it.t1 - it.t0) - 1);
+        it.blk0 = at - p.start;
+        it.blk1 = min(blocks, it.blk0 + end - cur.i);
+        it.part = (int)blockIdx.x - first / line.run;
+        it.whole = it.blk0 == 0 && it.blk1 == blocks;
+        cur.i += it.blk1 - it.blk0;
         return true;
+    }
+}
+
+// Inclusive sums over the block's threads; scratch holds 33 ints.
+__device__ __forceinline__ int block_sums(int v, int* scratch, int& total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int i = 1; i < 32; i *= 2) {
+        const int u = __shfl_up_sync(0xffffffffu, v, i);
+        if (lane >= i) v += u;
+    }
+    if (lane == 31) scratch[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+        int w = lane < (int)blockDim.x / 32 ? scratch[lane] : 0;
+#pragma unroll
+        for (int i = 1; i < 32; i *= 2) {
+            const int u = __shfl_up_sync(0xffffffffu, w, i);
+            if (lane >= i) w += u;
+        }
+        scratch[lane] = w;
+    }
+    __syncthreads();
+    total = scratch[31];
+    if (warp) v += scratch[warp - 1];
+    __syncthreads();
+    return v;
+}
+
+// Lays the line of prompts out: one CTA, two runs of sums (pairs over the
+// sequences, blocks over the pairs).
+__global__ void __launch_bounds__(1024) k_attn_layout(const __grid_constant__ Args a, const __grid_constant__ Layout lay)
+{
+    __shared__ int scratch[33];
+    kv::pdl_wait();
+    kv::pdl_release();
+    const int per2 = 2 * lay.per;
+    int pairs = 0, total;
+    for (int b0 = 0; b0 < a.bt.B; b0 += (int)blockDim.x) {
+        const int b = b0 + (int)threadIdx.x;
+        int t0 = 0, t1 = 0;
+        if (b < a.bt.B) kv::token_range(a.bt, b, t0, t1);
+        const int n = (t1 - t0 + per2 - 1) / per2, upto = block_sums(n, scratch, total);
+        if (b < a.bt.B) lay.first[b] = pairs + upto - n;
+        pairs += total;
+    }
+    if (threadIdx.x == 0) lay.first[a.bt.B] = pairs;
+    __syncthreads();
+    const int np = (a.bt.prefix_len + KB - 1) / KB;
+    int blocks = 0;
+    for (int i0 = 0; i0 < pairs; i0 += (int)blockDim.x) {
+        const int i = i0 + (int)threadIdx.x;
+        Pair p{0, 0, 0};
+        int n = 0;
+        if (i < pairs) {
+            int hi = a.bt.B;   // the last sequence that starts at or before pair i
+            while (hi - p.b > 1) {
+                const int mid = (p.b + hi) / 2;
+                if (lay.first[mid] <= i) p.b = mid;
+                else hi = mid;
+            }
+            int t0, t1, len;
+            kv::token_range(a.bt, p.b, t0, t1);
+            kv::own_length(a.bt, p.b, len);
+            p.t0 = t0 + (i - lay.first[p.b]) * per2;
+            const int own = len - (t1 - min(p.t0 + per2, t1));   // own tokens the pair's last token sees
+            n = max(1, np + (max(0, own) + KB - 1) / KB);        // 1: a pair that sees nothing is still written
+        }
+        const int upto = block_sums(n, scratch, total);
+        p.start = blocks + upto - n;
+        if (i < pairs) lay.pair[i] = p;
+        blocks += total;
+    }
+    if (threadIdx.x == 0) {
+        lay.pair[pairs] = Pair{blocks, 0, 0};
+        *lay.line = Line{max(lay.min_run, (a.c.heads * blocks + lay.ctas - 1) / lay.ctas), blocks, pairs};
     }
 }
 
@@ -287,7 +346,7 @@ template <typename T, int D, int KEYS>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_tiles(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Args a,
-                 const __grid_constant__ Deal deal, const __grid_constant__ Shape sh)
+                 const __grid_constant__ Deal deal, const __grid_constant__ Layout lay)
 {
     using C = Cfg<D>;
     constexpr int NS = C::SLOTS, HALVES = C::HALVES;
@@ -303,7 +362,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto kv_empty = [&](int x) { return bars + 96 + 8 * (NS + x); };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 96 + 16 * NS);
     static_assert(96 + 16 * NS + 4 <= 256, "barriers");
-    int* marks = reinterpret_cast<int*>(smem + C::OFF_UNITS);
     float2* ml1 = reinterpret_cast<float2*>(smem + C::OFF_ML);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -332,32 +390,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     kv::pdl_wait();
     kv::pdl_release();
-    if ((KEYS & kOwn) && warp == 0) {
-        const int stride = (a.bt.B + kMarks - 1) / kMarks;
-        int sum = 0;
-        for (int b0 = 0; b0 < a.bt.B; b0 += 32) {
-            const int b = b0 + lane;
-            int t0, t1;
-            const int n = b < a.bt.B ? pairs_of(a, b, 2 * sh.per, t0, t1) : 0;
-            int upto = n;
-#pragma unroll
-            for (int i = 1; i < 32; i *= 2) {
-                const int v = __shfl_up_sync(0xffffffffu, upto, i);
-                if (lane >= i) upto += v;
-            }
-            if (b < a.bt.B && b % stride == 0) marks[b / stride] = sum + upto - n;
-            sum += __shfl_sync(0xffffffffu, upto, 31);
-        }
-        if (lane == 0) marks[kMarks] = sum;
-    }
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     bool ok = true;
     Item it;
-    Cursor cur{(int)blockIdx.x, -1};
-    const int per = (KEYS & kOwn) ? sh.per : deal.per;   // tokens of a tile
+    Cursor cur{(KEYS & kOwn) ? (int)blockIdx.x * lay.line->run : (int)blockIdx.x, -1};
+    const int per = (KEYS & kOwn) ? lay.per : deal.per;   // tokens of a tile
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
@@ -369,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int in_page_mask = (1 << a.c.page_shift) - 1;
             int pos = 0;                                       // loads so far
             uint32_t item_phase = 0;
-            for (; ok && next_item<KEYS>(a, deal, sh, marks, cur, false, it); item_phase ^= 1u) {
+            for (; ok && next_item<KEYS>(a, deal, lay, cur, false, it); item_phase ^= 1u) {
                 const int n = it.blk1 - it.blk0;
                 const int n_prefix = (it.prefix + in_page_mask) >> a.c.page_shift;
                 const int* own_table = (KEYS & kOwn) ? a.bt.table + (long long)it.b * a.bt.table_ld : nullptr;
@@ -458,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::tc_fence_after();
                 return r;
             };
-            for (; ok && next_item<KEYS>(a, deal, sh, marks, cur, false, it); item_phase ^= 1u) {
+            for (; ok && next_item<KEYS>(a, deal, lay, cur, false, it); item_phase ^= 1u) {
                 const int n = it.blk1 - it.blk0;
                 const int step = it.two ? 1 : 2;       // a stream's next block
                 auto release = [&](int pos) { done(kv_empty(pos % NS)); };
@@ -532,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tok_in_tile = r / a.group;
         uint32_t s_phase = 0, o_phase = 0, join_phase = 0;
         const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
-        while (ok && next_item<KEYS>(a, deal, sh, marks, cur, threadIdx.x == 0, it)) {
+        while (ok && next_item<KEYS>(a, deal, lay, cur, threadIdx.x == 0, it)) {
             const int n = it.blk1 - it.blk0, step = it.two ? 1 : 2;
             const int tok = it.t0 + (it.two ? s * per : 0) + tok_in_tile;
             const bool in = tok_in_tile < per && tok < it.t1;
@@ -645,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (it.two || s == 0) {
                 const int hq = it.head * a.group + (r - tok_in_tile * a.group);
                 const long long row = (long long)tok * a.heads_q + hq;
-                const bool final = a.part_o == nullptr;
+                const bool final = it.whole;
                 const float inv = l > 0.0f ? 1.0f / l : 0.0f;
                 if (final) { w0 *= inv; w1 *= inv; }
                 const long long at = (long long)it.part * a.rows + row;
@@ -707,24 +747,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <typename T, int D, int KEYS>
 cudaError_t launch_one(const Args& a, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                       const Deal& d, const Shape& sh, int64_t ctas, cudaStream_t s)
+                       const Deal& d, const Layout& lay, int ctas, cudaStream_t s)
 {
     auto kernel = k_attn_tiles<T, D, KEYS>;
     static std::atomic<unsigned long long> done{0};
     const cudaError_t e = kv::allow_smem(kernel, Cfg<D>::SMEM, done);
     if (e != cudaSuccess) return e;
-    return kv::launch_dependent(kernel, dim3((unsigned)ctas), kThreads, Cfg<D>::SMEM, s, qmap, kmap, vmap, a, d, sh);
+    return kv::launch_dependent(kernel, dim3((unsigned)ctas), kThreads, Cfg<D>::SMEM, s, qmap, kmap, vmap, a, d, lay);
 }
 
 template <int KEYS>
 cudaError_t by_type(const Args& a, int dtype, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                    const Deal& d, const Shape& sh, int64_t ctas, cudaStream_t s)
+                    const Deal& d, const Layout& lay, int ctas, cudaStream_t s)
 {
     if (dtype == QG_T_BF16)
-        return a.c.dim == 128 ? launch_one<__nv_bfloat16, 128, KEYS>(a, qmap, kmap, vmap, d, sh, ctas, s)
-                              : launch_one<__nv_bfloat16, 64, KEYS>(a, qmap, kmap, vmap, d, sh, ctas, s);
-    return a.c.dim == 128 ? launch_one<__half, 128, KEYS>(a, qmap, kmap, vmap, d, sh, ctas, s)
-                          : launch_one<__half, 64, KEYS>(a, qmap, kmap, vmap, d, sh, ctas, s);
+        return a.c.dim == 128 ? launch_one<__nv_bfloat16, 128, KEYS>(a, qmap, kmap, vmap, d, lay, ctas, s)
+                              : launch_one<__nv_bfloat16, 64, KEYS>(a, qmap, kmap, vmap, d, lay, ctas, s);
+    return a.c.dim == 128 ? launch_one<__half, 128, KEYS>(a, qmap, kmap, vmap, d, lay, ctas, s)
+                          : launch_one<__half, 64, KEYS>(a, qmap, kmap, vmap, d, lay, ctas, s);
 }
 
 }  // namespace
@@ -732,18 +772,15 @@ cudaError_t by_type(const Args& a, int dtype, const CUtensorMap& qmap, const CUt
 cudaError_t launch_tiles_shared(const Args& a, int dtype, const CUtensorMap& qmap, const CUtensorMap& kmap,
                                 const CUtensorMap& vmap, const Deal& d, int ctas, cudaStream_t s)
 {
-    return by_type<kPrefix>(a, dtype, qmap, kmap, vmap, d, Shape{}, std::min(ctas, d.slots()), s);
+    return by_type<kPrefix>(a, dtype, qmap, kmap, vmap, d, Layout{}, std::min(ctas, d.slots()), s);
 }
 
 cudaError_t launch_tiles(const Args& a, int dtype, const CUtensorMap& qmap, const CUtensorMap& kmap,
-                         const CUtensorMap& vmap, int parts, int blocks_per_part, cudaStream_t s)
+                         const CUtensorMap& vmap, const Layout& lay, cudaStream_t s)
 {
-    const Shape sh{parts, blocks_per_part, tile_tokens(a.group)};
-    // at most so many pairs of tiles over the sequences
-    const int64_t pairs = std::min<int64_t>(a.bt.T / (2 * sh.per) + a.bt.B, a.bt.B * ceil_div(a.bt.max_q, 2 * sh.per));
-    const int64_t items = pairs * parts * a.c.heads;
-    if (items > 0x3FFFFFFF) return cudaErrorInvalidConfiguration;
-    return by_type<kPrefix | kOwn>(a, dtype, qmap, kmap, vmap, Deal{}, sh, std::min<int64_t>(num_sms(), items), s);
+    const cudaError_t e = kv::launch_dependent(k_attn_layout, dim3(1), 1024, 0, s, a, lay);
+    if (e != cudaSuccess) return e;
+    return by_type<kPrefix | kOwn>(a, dtype, qmap, kmap, vmap, Deal{}, lay, lay.ctas, s);
 }
 
 }  // namespace attn
