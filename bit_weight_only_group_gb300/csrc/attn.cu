@@ -5,7 +5,6 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
-#include <type_traits>
 #include <atomic>
 
 namespace qg {
@@ -139,7 +138,7 @@ Plan make_plan(const qg_kv_cache& c, const qg_kv_batch& b, int heads_q)
 
 // The workspace: o of the parts, (m, l) of the parts, the layout of prompts.
 struct Places {
-    size_t ml, line, first, pair, bytes;
+    size_t ml, line, first, pair, cut, bytes;
 };
 Places places(const Plan& p, const qg_kv_batch& b, int heads_q, int dim)
 {
@@ -152,80 +151,92 @@ Places places(const Plan& p, const qg_kv_batch& b, int heads_q, int dim)
     if (p.pairs) {
         w.first = w.line + align_up(sizeof(Line), 256);
         w.pair = w.first + align_up((size_t)(b.sequences + 1) * 4, 256);
-        w.bytes = w.pair + align_up((size_t)(p.pairs + 1) * sizeof(Pair), 256);
+        w.cut = w.pair + align_up((size_t)(p.pairs + 1) * sizeof(Pair), 256);
+        w.bytes = w.cut + align_up((size_t)p.ctas * 4, 256);
     }
     return w;
 }
 
 // out[r] = sum_p w_p o_p / sum_p w_p l_p with w_p = 2^(m_p - max m), in the
-// order of the parts: one warp a row, a lane 4 (or 2) of the row's values.
-// Part p < pieces is in slot p, the others follow from slot part0 on.  Bound
-// by latency (the parts were just written and are in L2): the (m, l) and the
-// values of the first four parts are loaded at once, before anything that
-// decides whether they are wanted.
+// order of the parts: dim / 8 lanes a row, 8 of its values a lane.  Part p <
+// pieces is in slot p, the others follow from slot part0 on.  Bound by latency
+// (the parts were just written and are in L2): the (m, l) and the values of
+// the first two parts are loaded at once, before anything that decides
+// whether they are wanted, and 40 registers let a decoding step's rows run in
+// one round (a warp a row with four parts in flight: 2.3 rounds at 16384 rows).
 template <int D>
 __device__ __forceinline__ void join_row(const Args& a, int t, int hq, int pieces, int part0, int n, const int* used)
 {
-    using Vec = typename std::conditional<D == 128, float4, float2>::type;
-    constexpr int AT_ONCE = 4;
-    const int lane = threadIdx.x & 31;
+    constexpr int LANES = D / 8, AT_ONCE = 2;
+    const int lane = threadIdx.x % LANES;
+    const uint32_t mask = (LANES == 32 ? 0xffffffffu : (1u << LANES) - 1u) << (threadIdx.x % 32 / LANES * LANES);
     const long long row = (long long)t * a.heads_q + hq;
     auto slot = [&](int p) { return (long long)(p < pieces ? p : part0 + p - pieces) * a.rows + row; };
     auto load_ml = [&](int p) { return p < n ? __ldcg(a.part_ml + slot(p)) : make_float2(-INFINITY, 0.0f); };
-    auto load_o = [&](int p0, Vec (&v)[AT_ONCE]) {   // where a part saw nothing its values are unset, and are not used
+    float4 v[AT_ONCE][2];
+    auto load_o = [&](int p0) {   // where a part saw nothing its values are unset, and are not used
 #pragma unroll
         for (int i = 0; i < AT_ONCE; i++)
-            if (p0 + i < n) v[i] = __ldcg(reinterpret_cast<const Vec*>(a.part_o + slot(p0 + i) * D) + lane);
+            if (p0 + i < n) {
+                const float4* src = reinterpret_cast<const float4*>(a.part_o + slot(p0 + i) * D) + 2 * lane;
+                v[i][0] = __ldcg(src);
+                v[i][1] = __ldcg(src + 1);
+            }
     };
     float2 ml = load_ml(lane);
-    Vec v[AT_ONCE];
-    load_o(0, v);
+    load_o(0);
     const bool mine = t < (used ? min(max(__ldg(used), 0), a.bt.T) : a.bt.T);
     float m = ml.y > 0.0f ? ml.x : -INFINITY, l = 0.0f;
-    for (int p = 32 + lane; p < n; p += 32) {
+    for (int p = LANES + lane; p < n; p += LANES) {
         const float2 w = load_ml(p);
         if (w.y > 0.0f) m = fmaxf(m, w.x);
     }
 #pragma unroll
-    for (int i = 16; i > 0; i /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
-    float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = LANES / 2; i > 0; i /= 2) m = fmaxf(m, __shfl_xor_sync(mask, m, i, LANES));
+    float o[8];
+#pragma unroll
+    for (int e = 0; e < 8; e++) o[e] = 0.0f;
     float w = ml.y > 0.0f ? exp2_approx(ml.x - m) : 0.0f;
     for (int p0 = 0; p0 < n; p0 += AT_ONCE) {
-        if (p0 && p0 % 32 == 0) {
+        if (p0 && p0 % LANES == 0) {
             ml = load_ml(p0 + lane);
             w = ml.y > 0.0f ? exp2_approx(ml.x - m) : 0.0f;
         }
 #pragma unroll
         for (int i = 0; i < AT_ONCE; i++) {
-            const float wp = __shfl_sync(0xffffffffu, w, (p0 + i) % 32), lp = __shfl_sync(0xffffffffu, ml.y, (p0 + i) % 32);
+            const float wp = __shfl_sync(mask, w, (p0 + i) % LANES, LANES);
+            const float lp = __shfl_sync(mask, ml.y, (p0 + i) % LANES, LANES);
             if (p0 + i < n && wp > 0.0f) {
                 l = fmaf(wp, lp, l);
-                o[0] = fmaf(wp, v[i].x, o[0]);
-                o[1] = fmaf(wp, v[i].y, o[1]);
-                if constexpr (D == 128) {
-                    o[2] = fmaf(wp, v[i].z, o[2]);
-                    o[3] = fmaf(wp, v[i].w, o[3]);
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    o[4 * h] = fmaf(wp, v[i][h].x, o[4 * h]);
+                    o[4 * h + 1] = fmaf(wp, v[i][h].y, o[4 * h + 1]);
+                    o[4 * h + 2] = fmaf(wp, v[i][h].z, o[4 * h + 2]);
+                    o[4 * h + 3] = fmaf(wp, v[i][h].w, o[4 * h + 3]);
                 }
             }
         }
-        load_o(p0 + AT_ONCE, v);
+        load_o(p0 + AT_ONCE);
     }
     if (!mine) return;
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    const long long at = t * a.ldo + (long long)hq * D;
-    if constexpr (D == 128) store_out4(a, at + 4 * lane, make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv));
-    else store_out2(a, at + 2 * lane, o[0] * inv, o[1] * inv);
+    uint32_t bits[8];
+#pragma unroll
+    for (int e = 0; e < 8; e++) bits[e] = __float_as_uint(o[e] * inv);
+    store_out8(a, t * a.ldo + (long long)hq * D + 8 * lane, bits);
     if (lane == 0) store_lse(a, row, m, l);
 }
+template <int D> constexpr int kJoinRows = 256 / (D / 8);   // rows of a joining CTA
 
 // All rows: the prefix's pieces first, then the other parts.
 template <int D>
-__global__ void __launch_bounds__(256, 6) k_attn_join(const __grid_constant__ Args a, const __grid_constant__ Deal d,
+__global__ void __launch_bounds__(256, 5) k_attn_join(const __grid_constant__ Args a, const __grid_constant__ Deal d,
                                                       int part0, int parts)
 {
     kv::pdl_wait();
     kv::pdl_release();
-    const uint32_t row = blockIdx.x * 8 + (threadIdx.x >> 5);
+    const uint32_t row = blockIdx.x * kJoinRows<D> + threadIdx.x / (D / 8);
     if (row >= a.rows) return;
     const int t = (int)(row / (uint32_t)a.heads_q), hq = (int)row - t * a.heads_q;
     int pieces = 0;
@@ -233,27 +244,23 @@ __global__ void __launch_bounds__(256, 6) k_attn_join(const __grid_constant__ Ar
     join_row<D>(a, t, hq, pieces, part0, pieces + parts, a.bt.cu_q ? a.bt.cu_q + a.bt.B : nullptr);
 }
 
-// The rows of items that the end of a CTA's run cut: 32 CTAs (8 rows each) for
-// each run's end, which leave the item to its first cut.
+// The rows of items that the end of a CTA's run cut: CTAs for 256 rows at each
+// run's end, which leave the item to its first cut.
 template <int D>
-__global__ void __launch_bounds__(256, 6) k_attn_join_line(const __grid_constant__ Args a, const __grid_constant__ Layout lay)
+__global__ void __launch_bounds__(256, 5) k_attn_join_line(const __grid_constant__ Args a, const __grid_constant__ Layout lay)
 {
     kv::pdl_wait();
     kv::pdl_release();
     const Line line = *lay.line;
-    const int c = blockIdx.x / 32 + 1;
+    constexpr int CTAS = 256 / kJoinRows<D>;
+    const int c = blockIdx.x / CTAS + 1;
     if ((long long)c * line.run >= (long long)a.c.heads * line.head) return;
     const int head = c * line.run / line.head, at = c * line.run - head * line.head;
-    int lo = 0, hi = line.pairs;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (lay.pair[mid].start <= at) lo = mid;
-        else hi = mid;
-    }
+    const int lo = lay.cut[c];
     const Pair p = lay.pair[lo];
     const int first = head * line.head + p.start, last = head * line.head + lay.pair[lo + 1].start - 1;
     if (p.start == at || first / line.run != c - 1) return;
-    const int r = blockIdx.x % 32 * 8 + (threadIdx.x >> 5), t = p.t0 + r / a.group;
+    const int r = blockIdx.x % CTAS * kJoinRows<D> + threadIdx.x / (D / 8), t = p.t0 + r / a.group;
     int t0, t1;
     kv::token_range(a.bt, p.b, t0, t1);
     if (r >= 2 * lay.per * a.group || t >= t1) return;
@@ -265,14 +272,14 @@ __global__ void __launch_bounds__(256, 6) k_attn_join_line(const __grid_constant
 
 cudaError_t launch_join(const Args& a, const Deal& d, int part0, int parts, cudaStream_t s)
 {
-    const dim3 grid((unsigned)ceil_div(a.rows, 8));
+    const dim3 grid((unsigned)ceil_div(a.rows, a.c.dim == 128 ? kJoinRows<128> : kJoinRows<64>));
     return a.c.dim == 128 ? kv::launch_dependent(k_attn_join<128>, grid, 256, 0, s, a, d, part0, parts)
                           : kv::launch_dependent(k_attn_join<64>, grid, 256, 0, s, a, d, part0, parts);
 }
 
 cudaError_t launch_join_line(const Args& a, const Layout& lay, cudaStream_t s)
 {
-    const dim3 grid((unsigned)(32 * (lay.ctas - 1)));
+    const dim3 grid((unsigned)(256 / (a.c.dim == 128 ? kJoinRows<128> : kJoinRows<64>) * (lay.ctas - 1)));
     if (!grid.x) return cudaSuccess;
     return a.c.dim == 128 ? kv::launch_dependent(k_attn_join_line<128>, grid, 256, 0, s, a, lay)
                           : kv::launch_dependent(k_attn_join_line<64>, grid, 256, 0, s, a, lay);
@@ -374,7 +381,8 @@ qg_status launch_attn(const qg_kv_cache& cache, const qg_kv_batch& batch, const 
             e = attn::launch_tiles_shared(a, cache.dtype, qmap, kmap, vmap, p.deal, p.ctas, s);
         } else {
             const attn::Layout lay{reinterpret_cast<attn::Line*>(base + w.line), reinterpret_cast<int*>(base + w.first),
-                                   reinterpret_cast<attn::Pair*>(base + w.pair), attn::tile_tokens(a.group), p.ctas, p.min_run};
+                                   reinterpret_cast<attn::Pair*>(base + w.pair), reinterpret_cast<int*>(base + w.cut),
+                                   attn::tile_tokens(a.group), p.ctas, p.min_run};
             e = attn::launch_tiles(a, cache.dtype, qmap, kmap, vmap, lay, s);
             if (e == cudaSuccess) e = attn::launch_join_line(a, lay, s);
         }

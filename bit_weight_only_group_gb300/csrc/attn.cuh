@@ -40,7 +40,7 @@ struct Args {
 
 constexpr float kLn2 = 0.69314718055994530942f;
 
-// Values of a finished row, two or four at a time.
+// Values of a finished row.
 __device__ __forceinline__ void store_out2(const Args& a, long long at, float x, float y)
 {
     if (a.out_type == QG_T_F32)
@@ -48,17 +48,6 @@ __device__ __forceinline__ void store_out2(const Args& a, long long at, float x,
     else
         *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at) =
             a.out_type == QG_T_BF16 ? kv::pack2<__nv_bfloat16>(x, y) : kv::pack2<__half>(x, y);
-}
-__device__ __forceinline__ void store_out4(const Args& a, long long at, float4 v)
-{
-    if (a.out_type == QG_T_F32)
-        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = v;
-    else if (a.out_type == QG_T_BF16)
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
-            make_uint2(kv::pack2<__nv_bfloat16>(v.x, v.y), kv::pack2<__nv_bfloat16>(v.z, v.w));
-    else
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
-            make_uint2(kv::pack2<__half>(v.x, v.y), kv::pack2<__half>(v.z, v.w));
 }
 // Eight fp32 values (as bits).
 __device__ __forceinline__ void store_out8(const Args& a, long long at, const uint32_t* v)
@@ -181,6 +170,7 @@ struct Layout {
     Line* line;
     int* first;               // [B + 1] pairs before each sequence
     Pair* pair;               // [pairs + 1], the last one's start the end of the line
+    int* cut;                 // [ctas] pair in which the run of each CTA starts
     int per;                  // tokens of a tile
     int ctas;
     int min_run;

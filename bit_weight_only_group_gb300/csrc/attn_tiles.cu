@@ -24,17 +24,19 @@
 //
 // Bound by the tensor cores: a block and two tiles take 2048 clocks of
 // products (N = 128: 64 clocks each), and QK^T reads shared memory at its full
-// 128 bytes a clock.  Measured, 1024 rows over 128 Ki keys: 310 us with the
-// softmax left out, 350 with it (554 GFLOP: 1.58 PFLOP/s; the card's power
-// limit holds plain products near 1.95).  Steps of 64 keys with two S buffers
-// a stream, which need not wait for S, took 470: products of N = 64 read Q
-// twice as often.
+// 128 bytes a clock.  Measured, 1024 rows over 128 Ki keys: 2570 clocks a block,
+// 2410 with the softmax left out; 554 GFLOP in 350 us on the whole card, where
+// its power limit holds plain products near 1.95 PFLOP/s.  Measured and
+// dropped: steps of 64 keys with two S buffers a stream, which need not wait
+// for S (470 us: products of N = 64 read Q twice as often); two threads a row
+// (5 % slower); waits that poll without being suspended (6 % slower).
 //
 // Warps: 0-3 softmax of stream 0, 4-7 of stream 1 (a warp may reach only the
 // 32 lanes of tensor memory its index modulo 4 names), 8 loads (one lane per
 // TMA box), 9 the matrix products.  One persistent CTA an SM (all 512 columns
 // of tensor memory); items of work are dealt in turn.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn.cuh"
 
@@ -46,7 +48,7 @@ constexpr int KB = 128;                      // keys of a block
 constexpr int kWarpLoad = 8, kWarpMma = 9;
 constexpr int kThreads = 384;                // warps 10 and 11 only fill the third warpgroup
 // Registers of a thread: 168 at launch (65536 over 384), then shared out by
-// warpgroup, 208 for the softmax's (a row of S, 128 values, in registers) and
+// warpgroup, 192 for the softmax's (a row of S, 128 values, in registers) and
 // 120 for the other: 2 * 192 + 120 = 3 * 168.
 constexpr int kRegsSoftmax = 192, kRegsOther = 120;
 static_assert(2 * kRegsSoftmax + kRegsOther == 3 * 168, "registers shared out are those of the launch");
@@ -60,10 +62,11 @@ template <int D> struct Cfg {
     static constexpr int OFF_KV = 2 * TILE;
     static constexpr int OFF_BAR = OFF_KV + SLOTS * TILE;
     static constexpr int OFF_ML = OFF_BAR + 256;           // (m, l) of stream 1's rows (joining)
-    static constexpr int SMEM = OFF_ML + 128 * 8 + 1024 /* alignment */;
+    static constexpr int SMEM = OFF_ML + 128 * 8;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 constexpr int kTmemCols = 512, kColO = 256;  // S and P of stream s at 128 s, O at 256 + 128 s
+template <int X> using Const = std::integral_constant<int, X>;
 
 // kind::f16 instruction descriptor: M = 128, fp32 accumulator; B's head dimension contiguous when `mn`.
 template <typename T>
@@ -72,31 +75,31 @@ __device__ constexpr uint32_t idesc(int N, bool mn)
     const uint32_t fmt = std::is_same<T, __half>::value ? 0u : 1u;
     return (1u << 4) | (fmt << 7) | (fmt << 10) | ((mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
 }
-// Descriptor of an operand whose M or N dimension is contiguous, 128-byte
-// swizzle: 8 k rows of 64 values are 1024 bytes, the next 8 follow (stride),
-// the next 64 values are `next64` bytes away (leading).
-__device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t next64)
-{
-    return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(next64 >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
-           (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
+// Upper words of the operands' descriptors (128-byte swizzle); the lower word
+// is the address / 16 and the leading offset / 16 << 16, and is advanced by
+// 32-bit additions, since all of a product's operands are moved to uniform
+// registers for it, and eight products of N = 128 leave 64 clocks for each.
+//  K contiguous: rows of 128 bytes, 8-row groups 1024 bytes apart.
+//  N contiguous (V): 8 k rows of 64 values are 1024 bytes, the next 8 follow
+//  (stride), the next 64 values are a leading offset away.
+constexpr uint32_t kDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t leading) { return addr >> 4 | (leading >> 4) << 16; }
 
 // D (+)= A B^T, A from shared or tensor memory.  One lane issues a whole run
 // of these inside a branch: electing a lane for each instruction instead
-// holds it to one every 77 to 88 clocks, where N = 128 takes 64 (8 steps of
-// K = 16: 655 against 520 clocks).
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t id, bool accumulate)
+// holds it to one every 77 to 88 clocks (8 steps of K = 16: 655 against 520).
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t id, bool accumulate)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-                 "l"(adesc), "l"(bdesc), "r"(id), "r"((uint32_t)accumulate)
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\t"
+                 "mov.b64 b, {%2, %5};\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}\n" ::"r"(d),
+                 "r"(a_low), "r"(b_low), "r"(id), "r"((uint32_t)accumulate), "n"(kDescHigh)
                  : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t id, bool accumulate)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_low, uint32_t id, bool accumulate)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
-                 "r"(a), "l"(bdesc), "r"(id), "r"((uint32_t)accumulate)
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}\n" ::"r"(d),
+                 "r"(a), "r"(b_low), "r"(id), "r"((uint32_t)accumulate), "n"(kDescHigh)
                  : "memory");
 }
 __device__ __forceinline__ void commit(uint32_t bar)
@@ -194,7 +197,8 @@ struct Item {
 // Where a CTA is in its work.
 struct Cursor {
     int i;      // slot of the deal, or place on the line
-    int head;   // next head of the slot (shared prefix), -1 at its start
+    int head;   // next head of the slot (-1 at its start), or of the line
+    int pair;   // pair the place on the line lies in
 };
 
 // The CTA's next item, or false past the end.
@@ -231,14 +235,8 @@ __device__ __forceinline__ bool next_item(const Args& a, const Deal& d, const La
         const Line line = *lay.line;
         const int end = min((int)(blockIdx.x + 1) * line.run, a.c.heads * line.head);
         if (cur.i >= end) return false;
-        it.head = cur.i / line.head;
-        const int at = cur.i - it.head * line.head;
-        int lo = 0, hi = line.pairs;   // the pair the place lies in
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (lay.pair[mid].start <= at) lo = mid;
-            else hi = mid;
-        }
+        it.head = cur.head;
+        const int at = cur.i - it.head * line.head, lo = cur.pair;
         const Pair p = lay.pair[lo];
         const int blocks = lay.pair[lo + 1].start - p.start, first = it.head * line.head + p.start;
         int t0;
@@ -256,6 +254,10 @@ __device__ __forceinline__ bool next_item(const Args& a, const Deal& d, const La
         it.part = (int)blockIdx.x - first / line.run;
         it.whole = it.blk0 == 0 && it.blk1 == blocks;
         cur.i += it.blk1 - it.blk0;
+        if (++cur.pair == line.pairs) {
+            cur.pair = 0;
+            cur.head++;
+        }
         return true;
     }
 }
@@ -331,9 +333,21 @@ __global__ void __launch_bounds__(1024) k_attn_layout(const __grid_constant__ Ar
         if (i < pairs) lay.pair[i] = p;
         blocks += total;
     }
+    const int run = max(lay.min_run, (a.c.heads * blocks + lay.ctas - 1) / lay.ctas);
     if (threadIdx.x == 0) {
         lay.pair[pairs] = Pair{blocks, 0, 0};
-        *lay.line = Line{max(lay.min_run, (a.c.heads * blocks + lay.ctas - 1) / lay.ctas), blocks, pairs};
+        *lay.line = Line{run, blocks, pairs};
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < lay.ctas; c += (int)blockDim.x) {
+        const int at = blocks ? c * run % blocks : 0;
+        int lo = 0, hi = pairs;   // the pair the place lies in
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (lay.pair[mid].start <= at) lo = mid;
+            else hi = mid;
+        }
+        lay.cut[c] = lo;
     }
 }
 
@@ -350,24 +364,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 {
     using C = Cfg<D>;
     constexpr int NS = C::SLOTS, HALVES = C::HALVES;
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) unsigned char smem[];   // the tiles' swizzle counts from 1024-byte boundaries
     const uint32_t sbase = ptx::smem_u32(smem), bars = sbase + C::OFF_BAR;
     const uint32_t q_full = bars, q_empty = bars + 8;
     auto s_full = [&](int s) { return bars + 16 + 8 * s; };     // S of stream s is in tensor memory
     auto p_full = [&](int s, int h) { return bars + 32 + 8 * (2 * s + h); };   // half h of P is, and O may be added to
     auto o_full = [&](int s) { return bars + 64 + 8 * s; };     // O is complete
     const uint32_t join_full = bars + 80, join_empty = bars + 88;   // stream 1's results for stream 0 to join: ready, read
-    auto kv_full = [&](int x) { return bars + 96 + 8 * x; };
-    auto kv_empty = [&](int x) { return bars + 96 + 8 * (NS + x); };
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 96 + 16 * NS);
-    static_assert(96 + 16 * NS + 4 <= 256, "barriers");
+    const uint32_t tail = bars + 96;      // a block of V with rows past the last key has arrived
+    auto kv_full = [&](int x) { return bars + 104 + 8 * x; };
+    auto kv_empty = [&](int x) { return bars + 104 + 8 * (NS + x); };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 104 + 16 * NS);
+    static_assert(104 + 16 * NS + 4 <= 256, "barriers");
     float2* ml1 = reinterpret_cast<float2*>(smem + C::OFF_ML);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         ptx::mbar_init(q_full, 1);
         ptx::mbar_init(q_empty, 1);
+        ptx::mbar_init(tail, 1);
         for (int s = 0; s < 2; s++) {
             ptx::mbar_init(s_full(s), 1);
             ptx::mbar_init(p_full(s, 0), 4);
@@ -393,10 +408,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    // all columns are taken, so they start at 0, and the kernel's only shared memory starts at a multiple of its
+    // alignment: known addresses let the products' operands be constants
+    constexpr uint32_t tmem = 0;
+    if (*tmem_slot != 0 || (sbase & 1023u)) {
+        kv::report(a.status);
+        __syncthreads();
+        if (warp == kWarpMma) ptx::tmem_dealloc(*tmem_slot, kTmemCols);
+        return;
+    }
     bool ok = true;
     Item it;
-    Cursor cur{(KEYS & kOwn) ? (int)blockIdx.x * lay.line->run : (int)blockIdx.x, -1};
+    Cursor cur{(int)blockIdx.x, -1, 0};
+    if constexpr (KEYS & kOwn) {
+        const Line line = *lay.line;
+        cur.i = (int)blockIdx.x * line.run;
+        cur.head = line.head ? cur.i / line.head : 0;
+        cur.pair = lay.cut[blockIdx.x];
+    }
     const int per = (KEYS & kOwn) ? lay.per : deal.per;   // tokens of a tile
 
     if (warp >= 8) {
@@ -408,34 +437,49 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool busy = half < HALVES;
             const int in_page_mask = (1 << a.c.page_shift) - 1;
             int pos = 0;                                       // loads so far
-            uint32_t item_phase = 0;
+            uint32_t item_phase = 0, tail_phase = 0;
             for (; ok && next_item<KEYS>(a, deal, lay, cur, false, it); item_phase ^= 1u) {
                 const int n = it.blk1 - it.blk0;
                 const int n_prefix = (it.prefix + in_page_mask) >> a.c.page_shift;
                 const int* own_table = (KEYS & kOwn) ? a.bt.table + (long long)it.b * a.bt.table_ld : nullptr;
-                auto keys_of = [&](int blk) { return blk < it.np ? min(KB, it.prefix - blk * KB) : min(KB, it.own - (blk - it.np) * KB); };
+                auto keys_of = [&](int blk) { return blk < it.np ? min(KB, it.prefix - blk * KB) : max(0, min(KB, it.own - (blk - it.np) * KB)); };
                 auto page_at = [&](int blk) -> int {
                     if (!busy || blk >= it.blk1 || mine * a.box_rows >= keys_of(blk)) return 0;
                     const int key = (blk < it.np ? blk : blk - it.np) * KB + mine * a.box_rows;
                     return blk < it.np ? page_of(a, a.bt.prefix_table, n_prefix, key >> a.c.page_shift)
                                        : page_of(a, own_table, a.bt.table_ld, key >> a.c.page_shift);
                 };
-                auto load = [&](const CUtensorMap* map, int blk, int page) -> bool {
-                    const int x = pos % NS;
+                auto load = [&](bool is_v, int blk, int page) -> bool {
+                    const int x = pos % NS, keys = keys_of(blk), used = (keys + a.box_rows - 1) / a.box_rows;
+                    const uint32_t slot = C::OFF_KV + x * C::TILE;
                     if (!__all_sync(0xffffffffu, ptx::mbar_wait(kv_empty(x), ((pos / NS) & 1) ^ 1u))) return false;
                     pos++;
-                    const int used = (keys_of(blk) + a.box_rows - 1) / a.box_rows;
-                    if (lane == 0) ptx::mbar_expect_tx(kv_full(x), (uint32_t)(used * HALVES * a.box_rows * 128));
+                    // V rows past the last key: what the page or an older block left there times 0 must be 0, so this warp waits
+                    // for such a block itself and clears them
+                    const bool ends = is_v && keys < KB;
+                    const uint32_t bar = ends ? tail : kv_full(x);
+                    if (lane == 0) ptx::mbar_expect_tx(bar, (uint32_t)(used * HALVES * a.box_rows * 128));
                     __syncwarp();
                     if (busy && mine < used) {
                         const int key = (blk < it.np ? blk : blk - it.np) * KB + mine * a.box_rows;
-                        tma_load_4d(sbase + C::OFF_KV + x * C::TILE + half * C::HALF + mine * a.box_rows * 128, map, half * 64,
-                                    key & in_page_mask, it.head, page, kv_full(x));
+                        tma_load_4d(sbase + slot + half * C::HALF + mine * a.box_rows * 128, is_v ? &vmap : &kmap, half * 64,
+                                    key & in_page_mask, it.head, page, bar);
+                    }
+                    if (ends) {
+                        if (!__all_sync(0xffffffffu, ptx::mbar_wait(tail, tail_phase))) return false;
+                        tail_phase ^= 1u;
+                        for (int e = lane; e < (KB - keys) * 8 * HALVES; e += 32) {
+                            const int row = keys + e / (8 * HALVES), c = e % (8 * HALVES);
+                            *reinterpret_cast<uint4*>(smem + slot + (c / 8) * C::HALF + row * 128 + (c % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        ptx::fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(kv_full(x));
                     }
                     return true;
                 };
                 int page = page_at(it.blk0);
-                if (n > 0) ok = load(&kmap, it.blk0, page);
+                if (n > 0) ok = load(false, it.blk0, page);
                 if (!ok) break;
                 // the last item's Q is no longer read
                 ok = __all_sync(0xffffffffu, ptx::mbar_wait(q_empty, item_phase ^ 1u));
@@ -451,49 +495,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 for (int j = 1; ok && j <= n; j++) {
                     const int next = j < n ? page_at(it.blk0 + j) : 0;
-                    if (j < n) ok = load(&kmap, it.blk0 + j, next);
-                    if (ok) ok = load(&vmap, it.blk0 + j - 1, page);
+                    if (j < n) ok = load(false, it.blk0 + j, next);
+                    if (ok) ok = load(true, it.blk0 + j - 1, page);
                     page = next;
                 }
             }
-        } else if (warp == kWarpMma) {
-            // ------------------------------------------------ matrix products
+        } else if (warp == kWarpMma && elect_lane()) {
+            // ------------------------------------------------ matrix products, by one lane
             constexpr uint32_t id_qk = idesc<T>(KB, false), id_pv = idesc<T>(D, true);
             uint32_t item_phase = 0, p_phase[2] = {0, 0};
             int base = 0;   // ring position of the item's first load
-            auto wait_kv = [&](int pos) {
-                const bool r = __all_sync(0xffffffffu, ptx::mbar_wait(kv_full(pos % NS), (pos / NS) & 1));
-                ptx::tc_fence_after();
-                return r;
-            };
-            const bool leader = elect_lane();   // issues the products and their commits
-            auto qk = [&](int tile, int s, int pos) {
-                const uint64_t ad = ptx::sw128_desc(sbase + tile * C::TILE);
-                const uint64_t bd = ptx::sw128_desc(sbase + C::OFF_KV + (pos % NS) * C::TILE);
-                if (leader) {
+            auto wait_kv = [&](int pos) { return ptx::mbar_wait(kv_full(pos % NS), (pos / NS) & 1); };
+            auto release = [&](int pos) { commit(kv_empty(pos % NS)); };
+            auto qk = [&](auto tile, auto s, int pos) {
+                const uint32_t ad = desc_low(sbase + tile.value * C::TILE, 16);
+                const uint32_t bd = desc_low(sbase + C::OFF_KV + (pos % NS) * C::TILE, 16);
 #pragma unroll
-                    for (int k = 0; k < D / 16; k++) {
-                        const uint64_t off = (uint64_t)(((k / 4) * C::HALF + (k % 4) * 32) >> 4);
-                        mma_ss(tmem + 128 * s, ad + off, bd + off, id_qk, k != 0);
-                    }
-                    commit(s_full(s));
+                for (int k = 0; k < D / 16; k++) {
+                    const uint32_t off = (uint32_t)(((k / 4) * C::HALF + (k % 4) * 32) >> 4);
+                    mma_ss(tmem + 128 * s.value, ad + off, bd + off, id_qk, k != 0);
                 }
+                commit(s_full(s.value));
             };
             // half h of P times half h of the V block
-            auto pv = [&](int s, int h, int pos, bool first) {
-                const uint64_t bd = mn_desc(sbase + C::OFF_KV + (pos % NS) * C::TILE, C::HALF);
-                if (leader) {
+            auto pv = [&](auto s, auto h, int pos, bool first) {
+                const uint32_t bd = desc_low(sbase + C::OFF_KV + (pos % NS) * C::TILE, C::HALF);
 #pragma unroll
-                    for (int k = 4 * h; k < 4 * h + 4; k++)
-                        mma_ts(tmem + kColO + 128 * s, tmem + 128 * s + 8 * k, bd + (uint64_t)((k * 2048) >> 4), id_pv,
-                               !first || k != 0);
-                }
-            };
-            auto done = [&](uint32_t bar) {
-                if (leader) commit(bar);
+                for (int k = 4 * h.value; k < 4 * h.value + 4; k++)
+                    mma_ts(tmem + kColO + 128 * s.value, tmem + 128 * s.value + 8 * k, bd + (uint32_t)((k * 2048) >> 4),
+                           id_pv, k != 0 || !first);
             };
             auto wait_p = [&](int s, int h) {
-                const bool r = __all_sync(0xffffffffu, ptx::mbar_wait(p_full(s, h), p_phase[s]));
+                const bool r = ptx::mbar_wait(p_full(s, h), p_phase[s]);
                 if (h) p_phase[s] ^= 1u;
                 ptx::tc_fence_after();
                 return r;
@@ -501,62 +534,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (; ok && next_item<KEYS>(a, deal, lay, cur, false, it); item_phase ^= 1u) {
                 const int n = it.blk1 - it.blk0;
                 const int step = it.two ? 1 : 2;       // a stream's next block
-                auto release = [&](int pos) { done(kv_empty(pos % NS)); };
-                ok = __all_sync(0xffffffffu, ptx::mbar_wait(q_full, item_phase));
-                if (!ok) break;
-                if (n > 0) {
-                    ok = wait_kv(base + pos_k(0));
+                ok = ptx::mbar_wait(q_full, item_phase);
+                // S of the streams' first blocks
+                for (int j = 0; ok && j < min(step, n); j++) {
+                    ok = wait_kv(base + pos_k(j));
                     if (!ok) break;
-                    qk(0, 0, base + pos_k(0));
-                    if (it.two) qk(1, 1, base + pos_k(0));
-                    release(base + pos_k(0));
-                    if (!it.two && n > 1) {
-                        ok = wait_kv(base + pos_k(1));
-                        if (!ok) break;
-                        qk(0, 1, base + pos_k(1));
-                        release(base + pos_k(1));
-                    }
+                    ptx::tc_fence_after();
+                    if (j == 0) qk(Const<0>{}, Const<0>{}, base + pos_k(j));
+                    else qk(Const<0>{}, Const<1>{}, base + pos_k(j));
+                    if (it.two) qk(Const<1>{}, Const<1>{}, base + pos_k(j));
+                    release(base + pos_k(j));
                 }
-                if (n <= step) done(q_empty);   // (n = 0: at once)
-                for (int j = 0; ok && j < n; j++) {
-                    const int pv_pos = base + pos_v(j, n);
-                    ok = wait_kv(pv_pos);
-                    if (!ok) break;
-                    const int blk = it.blk0 + j;
-                    const int keys = blk < it.np ? it.prefix - blk * KB : it.own - (blk - it.np) * KB;
-                    if (keys < KB) {
-                        // V rows past the last key: what the page or an older block left there times 0 must be 0
-                        unsigned char* v = smem + C::OFF_KV + (pv_pos % NS) * C::TILE;
-                        for (int e = lane; e < (KB - keys) * 8 * HALVES; e += 32) {
-                            const int row = keys + e / (8 * HALVES), c = e % (8 * HALVES);
-                            *reinterpret_cast<uint4*>(v + (c / 8) * C::HALF + row * 128 + (c % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                if (n <= step) commit(q_empty);
+                // one stream's turn in round j: its P of block j, then its S of block j + step
+                auto turn = [&](auto tile, auto s, int j, bool last_use) {
+                    const int v_pos = base + pos_v(j, n), k_pos = base + pos_k(j + step);
+                    if (!(ok = ok && wait_p(s.value, 0))) return;
+                    pv(s, Const<0>{}, v_pos, j < step);
+                    if (!(ok = wait_p(s.value, 1))) return;
+                    pv(s, Const<1>{}, v_pos, j < step);
+                    if (j + step < n) {
+                        qk(tile, s, k_pos);
+                        if (last_use) {
+                            release(k_pos);
+                            if (j + step == n - 1) commit(q_empty);
                         }
-                        ptx::fence_proxy_async();
-                        __syncwarp();
+                    } else {
+                        commit(o_full(s.value));
                     }
-                    const bool more = j + step < n;
-                    const int k_pos = base + pos_k(j + step);
-#pragma unroll
-                    for (int s = 0; s < 2; s++) {
-                        if (!it.two && s != (j & 1)) continue;
-                        ok = ok && wait_p(s, 0);
-                        if (!ok) break;
-                        pv(s, 0, pv_pos, j < step);
-                        ok = wait_p(s, 1);
-                        if (!ok) break;
-                        pv(s, 1, pv_pos, j < step);
-                        if (!it.two || s == 1) release(pv_pos);
-                        if (more) {
-                            if (!it.two || s == 0) ok = wait_kv(k_pos);
-                            if (!ok) break;
-                            qk(it.two ? s : 0, s, k_pos);
-                            if (!it.two || s == 1) {
-                                release(k_pos);
-                                if (j + step == n - 1) done(q_empty);
-                            }
-                        } else {
-                            done(o_full(s));
-                        }
+                    if (last_use) release(v_pos);
+                };
+                for (int j = 0; ok && j < n; j++) {
+                    // the loads of this round first: they have mostly arrived, and P has not
+                    ok = wait_kv(base + pos_v(j, n)) && (j + step >= n || wait_kv(base + pos_k(j + step)));
+                    if (it.two) {
+                        turn(Const<0>{}, Const<0>{}, j, false);
+                        turn(Const<1>{}, Const<1>{}, j, true);
+                    } else if (j & 1) {
+                        turn(Const<0>{}, Const<1>{}, j, true);
+                    } else {
+                        turn(Const<0>{}, Const<0>{}, j, true);
                     }
                 }
                 base += 2 * n;

@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(512) k_kv_append(const __grid_constant__ Appen
     const int t = blockIdx.x;
     const int per_head = a.c.dim / 16, hq = a.heads_q, hk = a.c.heads;
     const int tasks = (hq + 2 * hk) * per_head, turned = a.rope ? a.rot / 16 : 0;
-    if (t >= used_tokens(a.bt)) return;
+    const int used = used_tokens(a.bt);   // waited for only after the values' loads are under way
 
     // of a task: its head's values, and where in the head its two runs are
     auto place = [&](int task, int& head, int& i0, int& i1, bool& turn) {
@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(512) k_kv_append(const __grid_constant__ Appen
             }
         }
         if (base == 0) {   // the token's sequence, page and position
+            if (t >= used) return;
             b = find_sequence(a.bt, t);
             int t0, t1, len;
             token_range(a.bt, b, t0, t1);
