@@ -14,28 +14,31 @@ namespace {
 constexpr int kTile = 64;     // keys of a tile of the row kernel
 constexpr int kBlock = 128;   // keys of a block of the tile kernel
 
-enum Path { kRows, kTiles };
+// How a call is run.
+enum Way {
+    kAlone,         // row kernel: each sequence over prefix and own tokens
+    kRowsShared,    // row kernel: the prefix for all rows and the own tokens in one launch
+    kTilesShared,   // tile kernel for the prefix, row kernel for the own tokens beside it
+    kPrompts,       // tile kernel: each sequence over prefix and own tokens
+};
 
 // How a call is split.  Parts are numbered prefix first.
 struct Plan {
-    bool shared;                      // the prefix once for all rows, apart from the own tokens
-    Path prefix_path, own_path;       // kernel of each (own_path: of prefix and own together when not shared)
-    Deal deal;                        // shared, by tiles: the prefix's work
-    int ctas;                         // of the tile kernel
-    int64_t pairs;                    // bound of the pairs of tiles of all sequences, and
-    int min_run;                      // least run of a CTA that keeps an item to own_parts pieces (own tokens by tiles)
-    int prefix_parts, prefix_tiles;   // parts, and tiles of one (by rows)
-    int own_parts, own_tiles;         // the same of the own tokens, or of prefix and own together
-    int parts;                        // in all; 1: no joining, results are written at once
+    Way way;
+    Parts n;        // parts of the row kernel's keys; most parts of an item (kTilesShared: of the prefix, kPrompts: own)
+    int parts;      // in all; 1: no joining, results are written at once
+    int ctas;       // of the tile kernel
+    Deal deal;      // kTilesShared
+    int64_t pairs;  // kPrompts: bound of the pairs of tiles of all sequences, and
+    int min_run;    // the least run of a CTA that keeps an item to its most parts
 };
 
-// Parts of `tiles` tiles for `units` independent units of work: enough for
-// three CTAs on each SM, none below four tiles.
-void split(int64_t units, int64_t tiles, int* parts, int* per)
+// Parts of `tiles` tiles for `units` independent units of work: about `ctas`
+// CTAs in all, none with fewer than `least` tiles.
+void split(int64_t units, int64_t tiles, int64_t ctas, int least, int* parts, int* per)
 {
-    const int64_t want = std::max<int64_t>(1, ceil_div(3 * num_sms(), std::max<int64_t>(1, units)));
-    const int64_t most = std::max<int64_t>(1, tiles / 4);
-    const int64_t n = std::min(want, most);
+    const int64_t want = std::max<int64_t>(1, ceil_div(ctas, std::max<int64_t>(1, units)));
+    const int64_t n = std::min(want, std::max<int64_t>(1, tiles / least));
     *per = (int)std::max<int64_t>(1, ceil_div(tiles, n));
     *parts = (int)std::max<int64_t>(1, ceil_div(tiles, *per));
 }
@@ -57,27 +60,44 @@ Deal make_deal(const qg_kv_cache& c, const qg_kv_batch& b, int64_t group, int ct
     return d;
 }
 
+// Microseconds the row kernel takes on the whole card for the own tokens,
+// which fill half of max_kv, say: 6.4 TB/s, or, with more than 16 rows a
+// sequence and head, 0.7 an SM for each 32 rows and 64 keys.
+double own_time(const qg_kv_cache& c, const qg_kv_batch& b, int64_t group)
+{
+    const double pairs = 0.5 * b.sequences * c.heads_kv, rows = (double)group * b.max_q;
+    const double bytes = pairs * b.max_kv * c.head_dim * 4 / 6.4e6;
+    const double products = rows > 16 ? pairs * ceil_div((int64_t)rows, 32) * ceil_div(b.max_kv, kTile) * 0.7 / num_sms() : 0.0;
+    return 5.0 + std::max(bytes, products);
+}
+
+// Microseconds the tile kernel takes on an SM for a block and so many tiles:
+// 1.35 for a pair, 1.2 for a single tile (bound by its loads), two thirds of
+// that with 64-wide heads.
+double block_time(const qg_kv_cache& c, int64_t tiles)
+{
+    return (c.head_dim == 128 ? 1.0 : 0.67) * ((double)(tiles / 2) * 1.35 + (double)(tiles % 2) * 1.2);
+}
+
 // CTAs (one an SM) for the shared prefix, so that the own tokens' kernel, which
 // runs beside on the other SMs and takes over the rest when they end, ends
-// with them.  In microseconds: a CTA of the tile kernel takes about 10 and
-// then 1.45 for a block and a pair of tiles, 1.2 for a single tile (bound by
-// its loads), two thirds of that with 64-wide heads, slowed by up to 0.7
-// where the other kernel has the memory; the row kernel streams 6.4 TB/s of
-// own tokens (which fill half of max_kv, say) and takes 0.006 a CTA.  Measured
-// over 32 to 152 CTAs: 256 sequences over 8192 + 1024 keys best at 64 (134 us,
-// 158 on all SMs), 64 over 32768 + 2048 at 96 to 112 (103, 120), 128 over 131072 +
-// 2048 at 136 (429, 446), 32 over 2011 + 700 with a key/value head per query
-// head at 32 (48, 56).
+// with them.  A CTA of the tile kernel takes about 10 us before and after its
+// blocks, and is slowed by up to 0.7 where the other kernel has the memory;
+// the row kernel takes 0.006 us a CTA.  Measured over 32 to 152 CTAs: 256
+// sequences over 8192 + 1024 keys best at 64 (134 us, 158 on all SMs), 64 over
+// 32768 + 2048 at 96 to 112 (103, 120), 128 over 131072 + 2048 at 136 (429,
+// 446), 32 over 2011 + 700 with a key/value head per query head at 32 (48, 56).
 int choose_ctas(const qg_kv_cache& c, const qg_kv_batch& b, int64_t group, int64_t own_ctas)
 {
-    const double sms = num_sms(), dim = c.head_dim == 128 ? 1.0 : 0.67;
-    const double own = 5.0 + 0.5 * b.sequences * b.max_kv * c.heads_kv * c.head_dim * 4 / 6.4e6 + 0.006 * own_ctas;
+    const double sms = num_sms();
+    const double own = own_time(c, b, group) + 0.006 * own_ctas;
     int best = num_sms();
     double least = 1e30;
     for (int x = num_sms(); x >= 8; x -= 4) {
         const Deal d = make_deal(c, b, group, x);
         const double line = (double)d.heads * d.blocks, rounds = (double)ceil_div(d.slots(), x);
-        const double each = dim * rounds * std::max(d.pairs ? 1.45 * line / d.groups : 0.0, d.single ? 1.2 * line / d.sgroups : 0.0);
+        const double each = rounds * std::max(d.pairs ? block_time(c, 2) * line / d.groups : 0.0,
+                                              d.single ? block_time(c, 1) * line / d.sgroups : 0.0);
         const double busy = std::min(x, d.slots());
         const double tile_end = (10.0 + each) * (1.0 + 0.7 * (sms - busy) / sms);
         const double all_end = own + (10.0 + each) * busy / sms;
@@ -100,39 +120,59 @@ bool line_fits(const qg_kv_cache& c, const qg_kv_batch& b, int64_t per2)
 Plan make_plan(const qg_kv_cache& c, const qg_kv_batch& b, int heads_q)
 {
     Plan p{};
-    const int64_t group = heads_q / c.heads_kv;
-    const bool tiles = group <= 128;   // a tile holds whole tokens
-    const int64_t per2 = 2 * std::max(1, tile_tokens(group));
+    const int64_t group = heads_q / c.heads_kv, sms = num_sms();
+    const int64_t per = std::max(1, tile_tokens(group)), rows = group * b.tokens;
+    const int64_t np = ceil_div(b.prefix_len, kBlock), no = ceil_div(b.max_kv, kBlock);
+    const int64_t prefix_tiles = ceil_div(b.prefix_len, kTile), own_tiles = ceil_div(b.max_kv, kTile);
     const int64_t own_units = (int64_t)b.sequences * c.heads_kv * ceil_div(group * b.max_q, 64);
-    if (tiles && group * b.max_q > 64 && line_fits(c, b, per2)) {
-        // rows enough for tiles within a sequence: prefix and own tokens in one pass
-        p.own_path = kTiles;
-        p.ctas = num_sms();
-        p.pairs = b.tokens / per2 + b.sequences;
-        // an item's pieces, from the run that the card gets when all the bounds are met half way
-        const int64_t np = ceil_div(b.prefix_len, kBlock), longest = std::max<int64_t>(1, np + ceil_div(b.max_kv, kBlock));
-        const int64_t fair = std::max<int64_t>(2, c.heads_kv * ceil_div(b.tokens, per2) * ((np + longest) / 2) / p.ctas);
-        p.own_parts = (int)std::min<int64_t>(32, std::max<int64_t>(2, ceil_div(longest, fair) + 1));
-        p.min_run = (int)std::max<int64_t>(2, ceil_div(longest, p.own_parts - 1));
-    } else if (b.sequences > 1 && b.prefix_len >= 256) {
-        p.shared = true;
-        p.own_path = kRows;
-        if (tiles) {
-            p.prefix_path = kTiles;
-            split(own_units, ceil_div(b.max_kv, kTile), &p.own_parts, &p.own_tiles);
-            p.ctas = choose_ctas(c, b, group, own_units * p.own_parts);
-            p.deal = make_deal(c, b, group, p.ctas);
-            p.prefix_parts = p.deal.most_pieces();
-        } else {
-            p.prefix_path = kRows;
-            split(c.heads_kv * ceil_div(group * b.tokens, 64), ceil_div(b.prefix_len, kTile), &p.prefix_parts, &p.prefix_tiles);
-            split(own_units, ceil_div(b.max_kv, kTile), &p.own_parts, &p.own_tiles);
-        }
-    } else {
-        p.own_path = kRows;
-        split(own_units, ceil_div(b.prefix_len, kTile) + ceil_div(b.max_kv, kTile), &p.own_parts, &p.own_tiles);
+    const bool tiles = group <= 128;   // a tile holds whole tokens
+    const bool share = b.sequences > 1 && b.prefix_len >= 256;
+    p.way = share ? kTilesShared : kAlone;
+    if (share) {
+        // little work on the prefix, in blocks of 64 rows and 64 keys over the heads, is done sooner by the row kernel,
+        // which starts sooner and needs one launch less (512 blocks: 128 rows over 2048 keys of 8 heads 19.3 us, 20.8 by
+        // tiles; 1024 blocks: 64 rows over 8192 keys 28.2, 24.5), and longer where it is bound by the keys (16 rows over
+        // 8192 keys 14.6, 23.7)
+        const int64_t work = c.heads_kv * ceil_div(rows, 64) * prefix_tiles;
+        if (!tiles || work <= (rows <= 16 ? 4096 : 600)) p.way = kRowsShared;
     }
-    p.parts = p.prefix_parts + p.own_parts;
+    if (tiles && group * b.max_q > 64 && line_fits(c, b, 2 * per)) {
+        // rows enough for tiles within a sequence: prefix and own tokens in one pass, unless packing the rows of all
+        // sequences into tiles for the prefix saves more than the row kernel costs for the own tokens
+        const int64_t each = std::min<int64_t>(ceil_div(b.max_q, per), ceil_div(b.tokens, per * std::max(1, b.sequences)));
+        const double apart = b.sequences * c.heads_kv * block_time(c, each) * (np + 0.5 * no) / sms;
+        const double packed = c.heads_kv * block_time(c, ceil_div(b.tokens, per)) * np / sms + own_time(c, b, group);
+        if (!share || apart <= packed) p.way = kPrompts;
+        else p.way = kTilesShared;
+    }
+    switch (p.way) {
+        case kAlone:
+            split(own_units, prefix_tiles + own_tiles, 3 * sms, 4, &p.n.own_parts, &p.n.own_tiles);
+            break;
+        case kRowsShared: {
+            const int64_t units = c.heads_kv * ceil_div(rows, 64);
+            split(units, prefix_tiles, sms, 2, &p.n.prefix_parts, &p.n.prefix_tiles);
+            split(own_units, own_tiles, 3 * sms, 4, &p.n.own_parts, &p.n.own_tiles);
+            break;
+        }
+        case kTilesShared:
+            split(own_units, own_tiles, 3 * sms, 4, &p.n.own_parts, &p.n.own_tiles);
+            p.ctas = choose_ctas(c, b, group, own_units * p.n.own_parts);
+            p.deal = make_deal(c, b, group, p.ctas);
+            p.n.prefix_parts = p.deal.most_pieces();
+            break;
+        case kPrompts: {
+            p.ctas = (int)sms;
+            p.pairs = b.tokens / (2 * per) + b.sequences;
+            // an item's parts, from the run that the card gets when all the bounds are met half way
+            const int64_t longest = std::max<int64_t>(1, np + no);
+            const int64_t fair = std::max<int64_t>(2, c.heads_kv * ceil_div(b.tokens, 2 * per) * ((np + longest) / 2) / sms);
+            p.n.own_parts = (int)std::min<int64_t>(32, std::max<int64_t>(2, ceil_div(longest, fair) + 1));
+            p.min_run = (int)std::max<int64_t>(2, ceil_div(longest, p.n.own_parts - 1));
+            break;
+        }
+    }
+    p.parts = p.n.prefix_parts + p.n.own_parts;
     return p;
 }
 
@@ -366,42 +406,37 @@ qg_status launch_attn(const qg_kv_cache& cache, const qg_kv_batch& batch, const 
     a.part_o = p.parts > 1 ? reinterpret_cast<float*>(base) : nullptr;
     a.part_ml = p.parts > 1 ? reinterpret_cast<float2*>(base + w.ml) : nullptr;
     a.status = device_status_ptr();
-    const bool tiles = p.shared ? p.prefix_path == attn::kTiles : p.own_path == attn::kTiles;
-    const bool rows = !(tiles && !p.shared);
     qg_status st = QG_OK;
     CUtensorMap qmap, kmap, vmap;
     cudaError_t e = cudaSuccess;
-    if (tiles) {
+    if (p.way == attn::kTilesShared || p.way == attn::kPrompts) {
         a.box_rows = std::min(cache.page_size, attn::kBlock / 2);
         st = attn::encode_rows(&qmap, cache.dtype, q, cache.head_dim, heads_q, ldq, batch.tokens, a.group);
         if (st == QG_OK) st = attn::encode_pages(&kmap, cache, cache.k, a.box_rows, false);
         if (st == QG_OK) st = attn::encode_pages(&vmap, cache, cache.v, a.box_rows, false);
         if (st != QG_OK) return st;
-        if (p.shared) {
-            e = attn::launch_tiles_shared(a, cache.dtype, qmap, kmap, vmap, p.deal, p.ctas, s);
-        } else {
+        if (p.way == attn::kPrompts) {
             const attn::Layout lay{reinterpret_cast<attn::Line*>(base + w.line), reinterpret_cast<int*>(base + w.first),
                                    reinterpret_cast<attn::Pair*>(base + w.pair), reinterpret_cast<int*>(base + w.cut),
                                    attn::tile_tokens(a.group), p.ctas, p.min_run};
             e = attn::launch_tiles(a, cache.dtype, qmap, kmap, vmap, lay, s);
             if (e == cudaSuccess) e = attn::launch_join_line(a, lay, s);
+        } else {
+            e = attn::launch_tiles_shared(a, cache.dtype, qmap, kmap, vmap, p.deal, p.ctas, s);
         }
     }
-    if (rows) {
+    if (p.way != attn::kPrompts && e == cudaSuccess) {
         a.box_rows = std::min(cache.page_size, attn::kTile);
         st = attn::encode_pages(&kmap, cache, cache.k, a.box_rows, true);
         if (st == QG_OK) st = attn::encode_pages(&vmap, cache, cache.v, a.box_rows, true);
         if (st != QG_OK) return st;
-        if (e == cudaSuccess && p.shared && !tiles)
-            e = attn::launch_rows(a, cache.dtype, kmap, vmap, attn::kPrefix, 0, p.prefix_parts, p.prefix_tiles, false, s);
-        if (e == cudaSuccess)
-            e = attn::launch_rows(a, cache.dtype, kmap, vmap, p.shared ? attn::kOwn : attn::kPrefix | attn::kOwn,
-                                  p.prefix_parts, p.own_parts, p.own_tiles, tiles, s);
-    }
-    if (e == cudaSuccess && rows && p.parts > 1) {
-        // parts of the row kernel follow one another from 0 on when the prefix was not dealt to tiles
-        const bool dealt = p.shared && tiles;
-        e = attn::launch_join(a, p.deal, dealt ? p.prefix_parts : 0, dealt ? p.own_parts : p.parts, s);
+        if (p.way == attn::kRowsShared) e = attn::launch_rows_shared(a, cache.dtype, kmap, vmap, p.n, s);
+        else if (p.way == attn::kTilesShared) e = attn::launch_rows(a, cache.dtype, kmap, vmap, attn::kOwn, p.n, true, s);
+        else e = attn::launch_rows(a, cache.dtype, kmap, vmap, attn::kPrefix | attn::kOwn, p.n, false, s);
+        // the deal's pieces come first; parts of the row kernel alone follow one another from 0 on
+        if (e == cudaSuccess && p.parts > 1)
+            e = p.way == attn::kTilesShared ? attn::launch_join(a, p.deal, p.n.prefix_parts, p.n.own_parts, s)
+                                            : attn::launch_join(a, p.deal, 0, p.parts, s);
     }
     if (e != cudaSuccess) return cuda_fail(e, "qattn_forward launch");
     return QG_OK;

@@ -179,9 +179,18 @@ struct Layout {
 // The kernels' launches.  A keys flag says what a row sees: the shared
 // prefix, its own sequence's tokens, or both in that order.
 enum Keys { kPrefix = 1, kOwn = 2 };
-// beside: launched right after launch_tiles of the same call, whose results it does not use, to run at its side.
+// Parts of the keys and tiles (64 keys) of one, for the row kernel; own: of the
+// own tokens, or of prefix and own tokens together.  Parts of the prefix come
+// first.
+struct Parts {
+    int prefix_parts, prefix_tiles, own_parts, own_tiles;
+};
+// beside: launched right after the tile kernel of the same call, whose results it does not use, to run at its side.
 cudaError_t launch_rows(const Args& a, int dtype, const CUtensorMap& kmap, const CUtensorMap& vmap, int keys,
-                        int part0, int parts, int tiles_per_part, bool beside, cudaStream_t s);
+                        const Parts& p, bool beside, cudaStream_t s);
+// The shared prefix for all rows and the own tokens in one launch.
+cudaError_t launch_rows_shared(const Args& a, int dtype, const CUtensorMap& kmap, const CUtensorMap& vmap, const Parts& p,
+                               cudaStream_t s);
 // Tokens of a tile of the tile kernel (its rows: that times the group, at most 128).
 inline int tile_tokens(int64_t group) { return (int)(128 / group); }
 // The shared prefix for all tokens, dealt to at most `ctas` CTAs, parts 0 .. most_pieces() - 1.

@@ -109,11 +109,14 @@ __device__ __forceinline__ Item find_item(const Args& a, int unit, int row_block
     return it;
 }
 
+// The CTA numbered x of a launch's (unit, row block, part, head) CTAs.
+struct Split {
+    int part0, parts, tiles_per_part, row_blocks;
+};
+
 template <typename T, int D, int RW, int KEYS>
-__global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
-    k_attn_rows(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                const __grid_constant__ Args a, int part0, int parts, int tiles_per_part, int row_blocks,
-                int stages, int beside)
+__device__ __forceinline__ void work(const CUtensorMap& kmap, const CUtensorMap& vmap, const Args& a, const Split& sp, int x,
+                                     int stages, bool beside)
 {
     using C = Cfg<D>;
     constexpr int KW = kWarps / RW, NK = KT / KW, HALVES = D / 64;
@@ -125,12 +128,11 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // neighbouring CTAs take the heads of one unit (their rows of a page lie together when tokens come first)
-    int x = blockIdx.x;
     const int head = x % a.c.heads;
     x /= a.c.heads;
-    const int part = x % parts;
-    x /= parts;
-    const int row_block = x % row_blocks, unit = x / row_blocks;
+    const int part = x % sp.parts;
+    x /= sp.parts;
+    const int row_block = x % sp.row_blocks, unit = x / sp.row_blocks;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; s++) { ptx::mbar_init(full(s), 1); ptx::mbar_init(empty(s), kWarps); }
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
     if (!beside) kv::pdl_wait();
     kv::pdl_release();
     if (beside && blockIdx.x == gridDim.x - 1) kv::pdl_wait();
-    const Item it = find_item<KEYS>(a, unit, row_block, part, tiles_per_part, 16 * RW, threadIdx.x == 0);
+    const Item it = find_item<KEYS>(a, unit, row_block, part, sp.tiles_per_part, 16 * RW, threadIdx.x == 0);
     if (it.rows == 0) return;
     bool ok = true;
     // keys of tile j that any row sees
@@ -376,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
                                    o[i][2 * e + 1] * inv);
                     if (lane % 4 == 0) store_lse(a, row, m, l);
                 } else {
-                    const long long at = (long long)(part0 + part) * a.rows + row;
+                    const long long at = (long long)(sp.part0 + part) * a.rows + row;
                     if (lane % 4 == 0) a.part_ml[at] = make_float2(m, l);
                     if (l > 0.0f)
 #pragma unroll
@@ -391,55 +393,115 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
 }
 
 template <typename T, int D, int RW, int KEYS>
+__global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
+    k_attn_rows(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                const __grid_constant__ Args a, const __grid_constant__ Split sp, int stages, int beside)
+{
+    work<T, D, RW, KEYS>(kmap, vmap, a, sp, blockIdx.x, stages, beside != 0);
+}
+
+// The shared prefix for all rows (its CTAs first) and the own tokens in one launch.
+template <typename T, int D, int RWP, int RWO>
+__global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
+    k_attn_rows_shared(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                       const __grid_constant__ Args a, const __grid_constant__ Split prefix,
+                       const __grid_constant__ Split own, int prefix_ctas, int stages)
+{
+    if ((int)blockIdx.x < prefix_ctas) work<T, D, RWP, kPrefix>(kmap, vmap, a, prefix, blockIdx.x, stages, false);
+    else work<T, D, RWO, kOwn>(kmap, vmap, a, own, (int)blockIdx.x - prefix_ctas, stages, false);
+}
+
+// Row blocks of 16 rows that a CTA takes for so many rows a unit.
+int row_warps(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+
+struct Launch {
+    Split sp;
+    int64_t ctas;
+};
+Launch plan(const Args& a, int keys, int rw, int part0, int parts, int tiles_per_part)
+{
+    const int64_t units = (keys & kOwn) ? a.bt.B : 1;
+    const int64_t blocks = ceil_div((int64_t)a.group * ((keys & kOwn) ? a.bt.max_q : a.bt.T), 16 * rw);
+    return Launch{Split{part0, parts, tiles_per_part, (int)blocks}, units * blocks * parts * a.c.heads};
+}
+
+// No more stages than tiles: more of the shared memory stays with the kernel beside.
+template <int D> int stages_for(int tiles) { return std::max(1, std::min(tiles, Cfg<D>::MAX_STAGES)); }
+template <int D> int smem_for(int stages) { return stages * Cfg<D>::STAGE + Cfg<D>::REST; }
+
+template <typename T, int D, int RW, int KEYS>
 cudaError_t launch_one(const Args& a, const CUtensorMap& kmap, const CUtensorMap& vmap, int part0, int parts,
                        int tiles_per_part, bool beside, cudaStream_t s)
 {
     auto kernel = k_attn_rows<T, D, RW, KEYS>;
     static std::atomic<unsigned long long> done{0};
-    // no more stages than tiles: more of the shared memory stays with the kernel beside
-    const int stages = std::max(1, std::min(tiles_per_part, Cfg<D>::MAX_STAGES));
-    const int smem = stages * Cfg<D>::STAGE + Cfg<D>::REST;
-    const cudaError_t e = kv::allow_smem(kernel, Cfg<D>::MAX_STAGES * Cfg<D>::STAGE + Cfg<D>::REST, done);
+    const cudaError_t e = kv::allow_smem(kernel, smem_for<D>(Cfg<D>::MAX_STAGES), done);
     if (e != cudaSuccess) return e;
-    const int64_t units = (KEYS & kOwn) ? a.bt.B : 1;
-    const int64_t blocks = ceil_div((int64_t)a.group * ((KEYS & kOwn) ? a.bt.max_q : a.bt.T), 16 * RW);
-    const int64_t grid = units * blocks * parts * a.c.heads;
-    if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    return kv::launch_dependent(kernel, dim3((unsigned)grid), kThreads, smem, s, kmap, vmap, a, part0, parts,
-                                tiles_per_part, (int)blocks, stages, beside ? 1 : 0);
+    const Launch l = plan(a, KEYS, RW, part0, parts, tiles_per_part);
+    if (l.ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    const int stages = stages_for<D>(tiles_per_part);
+    return kv::launch_dependent(kernel, dim3((unsigned)l.ctas), kThreads, smem_for<D>(stages), s, kmap, vmap, a, l.sp,
+                                stages, beside ? 1 : 0);
 }
 
-template <typename T, int D, int RW>
-cudaError_t by_keys(const Args& a, const CUtensorMap& kmap, const CUtensorMap& vmap, int keys, int part0, int parts,
-                    int tiles_per_part, bool beside, cudaStream_t s)
+template <typename T, int D, int RWP, int RWO>
+cudaError_t launch_both(const Args& a, const CUtensorMap& kmap, const CUtensorMap& vmap, const Parts& p, cudaStream_t s)
 {
-    switch (keys) {
-        case kPrefix: return launch_one<T, D, RW, kPrefix>(a, kmap, vmap, part0, parts, tiles_per_part, beside, s);
-        case kOwn: return launch_one<T, D, RW, kOwn>(a, kmap, vmap, part0, parts, tiles_per_part, beside, s);
-        default: return launch_one<T, D, RW, kPrefix | kOwn>(a, kmap, vmap, part0, parts, tiles_per_part, beside, s);
-    }
+    auto kernel = k_attn_rows_shared<T, D, RWP, RWO>;
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e = kv::allow_smem(kernel, smem_for<D>(Cfg<D>::MAX_STAGES), done);
+    if (e != cudaSuccess) return e;
+    const Launch l = plan(a, kPrefix, RWP, 0, p.prefix_parts, p.prefix_tiles);
+    const Launch m = plan(a, kOwn, RWO, p.prefix_parts, p.own_parts, p.own_tiles);
+    if (l.ctas + m.ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    const int stages = stages_for<D>(std::max(p.prefix_tiles, p.own_tiles));
+    return kv::launch_dependent(kernel, dim3((unsigned)(l.ctas + m.ctas)), kThreads, smem_for<D>(stages), s, kmap, vmap, a,
+                                l.sp, m.sp, (int)l.ctas, stages);
 }
 
 template <typename T, int D>
-cudaError_t by_rows(const Args& a, const CUtensorMap& kmap, const CUtensorMap& vmap, int keys, int part0, int parts,
-                    int tiles_per_part, bool beside, cudaStream_t s)
+cudaError_t by_keys(const Args& a, const CUtensorMap& kmap, const CUtensorMap& vmap, int keys, const Parts& p, bool beside,
+                    cudaStream_t s)
 {
-    const int64_t rows = (int64_t)a.group * (keys == kPrefix ? a.bt.T : a.bt.max_q);
-    if (rows <= 16) return by_keys<T, D, 1>(a, kmap, vmap, keys, part0, parts, tiles_per_part, beside, s);
-    if (rows <= 32) return by_keys<T, D, 2>(a, kmap, vmap, keys, part0, parts, tiles_per_part, beside, s);
-    return by_keys<T, D, 4>(a, kmap, vmap, keys, part0, parts, tiles_per_part, beside, s);
+    const int part0 = keys == kOwn ? p.prefix_parts : 0, n = p.own_parts, t = p.own_tiles;
+    const int rw = row_warps((int64_t)a.group * a.bt.max_q);
+    if (keys == kOwn)
+        return rw == 1   ? launch_one<T, D, 1, kOwn>(a, kmap, vmap, part0, n, t, beside, s)
+               : rw == 2 ? launch_one<T, D, 2, kOwn>(a, kmap, vmap, part0, n, t, beside, s)
+                         : launch_one<T, D, 4, kOwn>(a, kmap, vmap, part0, n, t, beside, s);
+    return rw == 1   ? launch_one<T, D, 1, kPrefix | kOwn>(a, kmap, vmap, part0, n, t, beside, s)
+           : rw == 2 ? launch_one<T, D, 2, kPrefix | kOwn>(a, kmap, vmap, part0, n, t, beside, s)
+                     : launch_one<T, D, 4, kPrefix | kOwn>(a, kmap, vmap, part0, n, t, beside, s);
+}
+
+template <typename T, int D>
+cudaError_t both(const Args& a, const CUtensorMap& kmap, const CUtensorMap& vmap, const Parts& p, cudaStream_t s)
+{
+    const int rw = row_warps((int64_t)a.group * a.bt.max_q);
+    if ((int64_t)a.group * a.bt.T <= 16) return launch_both<T, D, 1, 1>(a, kmap, vmap, p, s);
+    return rw == 1   ? launch_both<T, D, 4, 1>(a, kmap, vmap, p, s)
+           : rw == 2 ? launch_both<T, D, 4, 2>(a, kmap, vmap, p, s)
+                     : launch_both<T, D, 4, 4>(a, kmap, vmap, p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_rows(const Args& a, int dtype, const CUtensorMap& kmap, const CUtensorMap& vmap, int keys,
-                        int part0, int parts, int tiles_per_part, bool beside, cudaStream_t s)
+                        const Parts& p, bool beside, cudaStream_t s)
 {
     if (dtype == QG_T_BF16)
-        return a.c.dim == 128 ? by_rows<__nv_bfloat16, 128>(a, kmap, vmap, keys, part0, parts, tiles_per_part, beside, s)
-                              : by_rows<__nv_bfloat16, 64>(a, kmap, vmap, keys, part0, parts, tiles_per_part, beside, s);
-    return a.c.dim == 128 ? by_rows<__half, 128>(a, kmap, vmap, keys, part0, parts, tiles_per_part, beside, s)
-                          : by_rows<__half, 64>(a, kmap, vmap, keys, part0, parts, tiles_per_part, beside, s);
+        return a.c.dim == 128 ? by_keys<__nv_bfloat16, 128>(a, kmap, vmap, keys, p, beside, s)
+                              : by_keys<__nv_bfloat16, 64>(a, kmap, vmap, keys, p, beside, s);
+    return a.c.dim == 128 ? by_keys<__half, 128>(a, kmap, vmap, keys, p, beside, s)
+                          : by_keys<__half, 64>(a, kmap, vmap, keys, p, beside, s);
+}
+
+cudaError_t launch_rows_shared(const Args& a, int dtype, const CUtensorMap& kmap, const CUtensorMap& vmap, const Parts& p,
+                               cudaStream_t s)
+{
+    if (dtype == QG_T_BF16)
+        return a.c.dim == 128 ? both<__nv_bfloat16, 128>(a, kmap, vmap, p, s) : both<__nv_bfloat16, 64>(a, kmap, vmap, p, s);
+    return a.c.dim == 128 ? both<__half, 128>(a, kmap, vmap, p, s) : both<__half, 64>(a, kmap, vmap, p, s);
 }
 
 }  // namespace attn

@@ -64,6 +64,25 @@ def test_batch_sizes(qg, B):
     check_attention(c, *_run(qg, c))
 
 
+@pytest.mark.parametrize("heads_q,heads_kv,dim,dtype,page,heads_first", [
+    (64, 8, 128, BF, 64, True), (64, 8, 128, FP, 16, False), (32, 8, 64, FP, 128, True), (28, 4, 128, BF, 32, False),
+    (32, 32, 128, BF, 64, True), (48, 1, 64, BF, 256, True), (100, 1, 128, FP, 64, True)])
+@pytest.mark.parametrize("n_q,prefix", [([1] * 33, 2500), ([1] * 90, 2049), ([3, 1, 5, 0, 2] * 9, 2431)])
+def test_much_shared_prefix(qg, heads_q, heads_kv, dim, dtype, page, heads_first, n_q, prefix):
+    # enough rows and keys that the prefix is worked on in tiles: pairs of tiles, a single one, a cut last block
+    kv = [max(n, 1) + (31 * b) % 150 for b, n in enumerate(n_q)]
+    c = Case(n_q, kv, prefix, heads_q, heads_kv, dim, page, dtype, heads_first, seed=len(n_q) + page, spare_tokens=2)
+    check_attention(c, *_run(qg, c))
+
+
+@pytest.mark.parametrize("heads_q,heads_kv,dim", [(16, 2, 128), (32, 8, 64)])
+def test_rows_packed_across_sequences(qg, heads_q, heads_kv, dim):
+    # more than 64 rows a sequence and head, few of its own keys: the prefix's tiles hold rows of several sequences
+    n_q = [20, 17, 1, 19] * 10
+    c = Case(n_q, [n + b for b, n in enumerate(n_q)], 4000, heads_q, heads_kv, dim, 64, BF, seed=30)
+    check_attention(c, *_run(qg, c))
+
+
 @pytest.mark.parametrize("n_q,kv", [([1, 5, 2], [1, 9, 200]), ([8, 8], [8, 64]), ([3, 0, 4, 1], [70, 50, 4, 1]),
                                     ([17, 33], [17, 129]), ([64], [300]), ([130, 1, 90], [130, 65, 191]),
                                     ([257, 3], [400, 3])])
@@ -149,7 +168,7 @@ def test_looser_bounds_change_nothing(qg):
     check_attention(c, *_run(qg, c, max_kv=1000, max_q=9))
 
 
-@pytest.mark.parametrize("n_q,kv,prefix", [([1] * 20, [300] * 20, 5000), ([200, 200], [200, 500], 700), ([1], [9000], 0)])
+@pytest.mark.parametrize("n_q,kv,prefix", [([1] * 20, [300] * 20, 5000), ([1] * 60, [300] * 60, 20000), ([200, 200], [200, 500], 700), ([1], [9000], 0)])
 def test_repeatable_bit_for_bit(qg, n_q, kv, prefix):
     c = Case(n_q, kv, prefix, 16, 2, 128, 64, BF, seed=15)
     a, la = _run(qg, c)
