@@ -418,7 +418,7 @@ qg_status launch_attn(const qg_kv_cache& cache, const qg_kv_batch& batch, const 
         if (p.way == attn::kPrompts) {
             const attn::Layout lay{reinterpret_cast<attn::Line*>(base + w.line), reinterpret_cast<int*>(base + w.first),
                                    reinterpret_cast<attn::Pair*>(base + w.pair), reinterpret_cast<int*>(base + w.cut),
-                                   attn::tile_tokens(a.group), p.ctas, p.min_run};
+                                   attn::tile_tokens(a.group), p.ctas, p.min_run, (int)p.pairs};
             e = attn::launch_tiles(a, cache.dtype, qmap, kmap, vmap, lay, s);
             if (e == cudaSuccess) e = attn::launch_join_line(a, lay, s);
         } else {

@@ -174,6 +174,7 @@ struct Layout {
     int per;                  // tokens of a tile
     int ctas;
     int min_run;
+    int max_pairs;            // entries of `pair` but one
 };
 
 // The kernels' launches.  A keys flag says what a row sees: the shared

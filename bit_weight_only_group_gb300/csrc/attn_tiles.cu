@@ -307,6 +307,10 @@ __global__ void __launch_bounds__(1024) k_attn_layout(const __grid_constant__ Ar
         pairs += total;
     }
     if (threadIdx.x == 0) lay.first[a.bt.B] = pairs;
+    if (pairs > lay.max_pairs) {   // offsets that are not ascending: more pairs than the tokens can make
+        if (threadIdx.x == 0) kv::report(a.status);
+        pairs = lay.max_pairs;
+    }
     __syncthreads();
     const int np = (a.bt.prefix_len + KB - 1) / KB;
     int blocks = 0;

@@ -137,7 +137,7 @@ qg_status qattn_forward(const qg_kv_cache* cache, const qg_kv_batch* batch, cons
     qg_status st = check_attn(cache, batch, heads_q, who);
     if (st != QG_OK) return st;
     if (ot != QG_T_F32 && ot != QG_T_BF16 && ot != QG_T_F16) return fail(QG_ERR_INVALID_ARG, "%s: bad ot %d", who, (int)ot);
-    if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(QG_ERR_INVALID_ARG, "%s: scale must be positive and finite", who);
+    if (!(scale > 0.0f) || !std::isfinite(scale * 1.4426950408889634f)) return fail(QG_ERR_INVALID_ARG, "%s: scale must be positive and finite", who);
     if (batch->sequences == 0 || batch->tokens == 0) return QG_OK;
     const int64_t width = (int64_t)heads_q * cache->head_dim;
     st = check_rows(q, ldq, width, 2, "q", who);

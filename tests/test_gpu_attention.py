@@ -269,6 +269,13 @@ def test_bad_lengths_and_pages_are_reported(qg):
     # more new tokens than max_q says
     c = Case([5, 1], [40, 30], 300, 8, 2, 128, 16, BF, seed=22)
     assert status(c, max_q=1) == -7
+    # offsets that are not ascending, in each of the ways a call is run
+    for n_q, prefix in (([1, 1, 1], 0), ([1] * 40, 2500), ([100, 90, 70], 300)):
+        c = Case(n_q, [n + 100 for n in n_q], prefix, 64, 8, 128, 64, BF, seed=24)
+        c.cu_q[1::2] = c.T
+        c.cu_q[2::2] = 0
+        c.cu_q[-1] = c.T
+        status(c)   # finishes, whatever it reports
     # a sound call afterwards
     c = make()
     check_attention(c, *_run(qg, c))
