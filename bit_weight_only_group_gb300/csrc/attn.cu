@@ -201,13 +201,13 @@ Places places(const Plan& p, const qg_kv_batch& b, int heads_q, int dim)
 // order of the parts: dim / 8 lanes a row, 8 of its values a lane.  Part p <
 // pieces is in slot p, the others follow from slot part0 on.  Bound by latency
 // (the parts were just written and are in L2): the (m, l) and the values of
-// the first two parts are loaded at once, before anything that decides
-// whether they are wanted, and 40 registers let a decoding step's rows run in
-// one round (a warp a row with four parts in flight: 2.3 rounds at 16384 rows).
-template <int D>
+// the first AT_ONCE parts are loaded at once, before anything that decides
+// whether they are wanted.  Few rows take eight parts at once; many take two,
+// in 48 registers, so that more rows run in a round.
+template <int D, int AT_ONCE>
 __device__ __forceinline__ void join_row(const Args& a, int t, int hq, int pieces, int part0, int n, const int* used)
 {
-    constexpr int LANES = D / 8, AT_ONCE = 2;
+    constexpr int LANES = D / 8;
     const int lane = threadIdx.x % LANES;
     const uint32_t mask = (LANES == 32 ? 0xffffffffu : (1u << LANES) - 1u) << (threadIdx.x % 32 / LANES * LANES);
     const long long row = (long long)t * a.heads_q + hq;
@@ -270,8 +270,8 @@ __device__ __forceinline__ void join_row(const Args& a, int t, int hq, int piece
 template <int D> constexpr int kJoinRows = 256 / (D / 8);   // rows of a joining CTA
 
 // All rows: the prefix's pieces first, then the other parts.
-template <int D>
-__global__ void __launch_bounds__(256, 5) k_attn_join(const __grid_constant__ Args a, const __grid_constant__ Deal d,
+template <int D, int AT_ONCE>
+__global__ void __launch_bounds__(256, AT_ONCE == 2 ? 5 : 2) k_attn_join(const __grid_constant__ Args a, const __grid_constant__ Deal d,
                                                       int part0, int parts)
 {
     kv::pdl_wait();
@@ -281,45 +281,53 @@ __global__ void __launch_bounds__(256, 5) k_attn_join(const __grid_constant__ Ar
     const int t = (int)(row / (uint32_t)a.heads_q), hq = (int)row - t * a.heads_q;
     int pieces = 0;
     if (d.blocks) pieces = d.pieces(hq / a.group, t < d.pairs * 2 * d.per ? d.groups : d.sgroups);
-    join_row<D>(a, t, hq, pieces, part0, pieces + parts, a.bt.cu_q ? a.bt.cu_q + a.bt.B : nullptr);
+    join_row<D, AT_ONCE>(a, t, hq, pieces, part0, pieces + parts, a.bt.cu_q ? a.bt.cu_q + a.bt.B : nullptr);
 }
 
-// The rows of items that the end of a CTA's run cut: CTAs for 256 rows at each
-// run's end, which leave the item to its first cut.
+// The rows of items that the end of a CTA's run cut: kCutCtas CTAs for the 256
+// rows at each run's end, which leave the item to its first cut.  (Four rounds
+// of rows a CTA: with one, 151 cuts take three waves of CTAs.)
+constexpr int kCutCtas = 4;
 template <int D>
 __global__ void __launch_bounds__(256, 5) k_attn_join_line(const __grid_constant__ Args a, const __grid_constant__ Layout lay)
 {
     kv::pdl_wait();
     kv::pdl_release();
     const Line line = *lay.line;
-    constexpr int CTAS = 256 / kJoinRows<D>;
-    const int c = blockIdx.x / CTAS + 1;
+    const int c = blockIdx.x / kCutCtas + 1, lo = lay.cut[c];
     if ((long long)c * line.run >= (long long)a.c.heads * line.head) return;
     const int head = c * line.run / line.head, at = c * line.run - head * line.head;
-    const int lo = lay.cut[c];
     const Pair p = lay.pair[lo];
     const int first = head * line.head + p.start, last = head * line.head + lay.pair[lo + 1].start - 1;
     if (p.start == at || first / line.run != c - 1) return;
-    const int r = blockIdx.x % CTAS * kJoinRows<D> + threadIdx.x / (D / 8), t = p.t0 + r / a.group;
     int t0, t1;
     kv::token_range(a.bt, p.b, t0, t1);
-    if (r >= 2 * lay.per * a.group || t >= t1) return;
     const int n = last / line.run - first / line.run + 1;
-    join_row<D>(a, t, head * a.group + r % a.group, n, 0, n, nullptr);
+    for (int r = blockIdx.x % kCutCtas * (256 / kCutCtas) + threadIdx.x / (D / 8); r < (blockIdx.x % kCutCtas + 1) * (256 / kCutCtas);
+         r += kJoinRows<D>) {
+        const int t = p.t0 + r / a.group;
+        if (r >= 2 * lay.per * a.group || t >= t1) return;
+        join_row<D, 2>(a, t, head * a.group + r % a.group, n, 0, n, nullptr);
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_join(const Args& a, const Deal& d, int part0, int parts, cudaStream_t s)
 {
-    const dim3 grid((unsigned)ceil_div(a.rows, a.c.dim == 128 ? kJoinRows<128> : kJoinRows<64>));
-    return a.c.dim == 128 ? kv::launch_dependent(k_attn_join<128>, grid, 256, 0, s, a, d, part0, parts)
-                          : kv::launch_dependent(k_attn_join<64>, grid, 256, 0, s, a, d, part0, parts);
+    const int each = a.c.dim == 128 ? kJoinRows<128> : kJoinRows<64>;
+    const dim3 grid((unsigned)ceil_div(a.rows, each));
+    const bool few = grid.x <= 2u * num_sms();   // one round of the wide form: 1024 rows of 13 parts 6.2 us, 8.0 in the narrow
+    if (a.c.dim == 128)
+        return few ? kv::launch_dependent(k_attn_join<128, 8>, grid, 256, 0, s, a, d, part0, parts)
+                   : kv::launch_dependent(k_attn_join<128, 2>, grid, 256, 0, s, a, d, part0, parts);
+    return few ? kv::launch_dependent(k_attn_join<64, 8>, grid, 256, 0, s, a, d, part0, parts)
+               : kv::launch_dependent(k_attn_join<64, 2>, grid, 256, 0, s, a, d, part0, parts);
 }
 
 cudaError_t launch_join_line(const Args& a, const Layout& lay, cudaStream_t s)
 {
-    const dim3 grid((unsigned)(256 / (a.c.dim == 128 ? kJoinRows<128> : kJoinRows<64>) * (lay.ctas - 1)));
+    const dim3 grid((unsigned)(kCutCtas * (lay.ctas - 1)));
     if (!grid.x) return cudaSuccess;
     return a.c.dim == 128 ? kv::launch_dependent(k_attn_join_line<128>, grid, 256, 0, s, a, lay)
                           : kv::launch_dependent(k_attn_join_line<64>, grid, 256, 0, s, a, lay);
