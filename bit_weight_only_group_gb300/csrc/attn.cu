@@ -156,7 +156,7 @@ Plan make_plan(const qg_kv_cache& c, const qg_kv_batch& b, int heads_q)
             break;
         }
         case kTilesShared:
-            split(own_units, own_tiles, 3 * sms, 4, &p.n.own_parts, &p.n.own_tiles);
+            split(own_units, own_tiles, 4 * sms, 4, &p.n.own_parts, &p.n.own_tiles);
             p.ctas = choose_ctas(c, b, group, own_units * p.n.own_parts);
             p.deal = make_deal(c, b, group, p.ctas);
             p.n.prefix_parts = p.deal.most_pieces();

@@ -76,21 +76,25 @@ __device__ __forceinline__ bool own_length(const Batch& bt, int b, int& len)
     return l == len;
 }
 
-// Sequence of token t < used_tokens, the same in every lane of a whole warp:
-// the last b with cu_q[b] <= t, found 32 bounds at a time (two dependent
-// loads for up to 1024 sequences, where a binary search takes ten).
-__device__ __forceinline__ int find_sequence(const Batch& bt, int t)
+// Sequence of each lane's token (of a whole warp): the last b with cu_q[b] <= t.
+// 32 bounds are loaded at once and searched by shuffles, so that up to 32
+// sequences take one load and 256 four, one after another.
+__device__ __forceinline__ int find_sequences(const Batch& bt, int t)
 {
-    if (!bt.cu_q) return t;
-    const int lane = threadIdx.x & 31;
-    int lo = 0, hi = bt.B;
+    if (!bt.cu_q) return min(t, bt.B - 1);
+    const int lane = threadIdx.x & 31, step = (bt.B + 31) / 32;
+    const int bound = lane * step < bt.B ? __ldg(bt.cu_q + lane * step) : 0x7FFFFFFF;
+    int at = 0;
+#pragma unroll
+    for (int i = 16; i > 0; i /= 2)
+        if (__shfl_sync(0xffffffffu, bound, at + i) <= t) at += i;
+    int lo = at * step, hi = min(lo + step, bt.B);
     while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32, i = lo + lane * step;
-        const bool below = i < hi && (lane == 0 || __ldg(bt.cu_q + i) <= t);
-        lo += (__popc(__ballot_sync(0xffffffffu, below)) - 1) * step;
-        hi = min(hi, lo + step);
+        const int mid = (lo + hi) / 2;
+        if (__ldg(bt.cu_q + mid) <= t) lo = mid;
+        else hi = mid;
     }
-    return lo;
+    return min(lo, bt.B - 1);
 }
 
 // fp32 pair -> two values of the cache's type in one word, rounded to nearest even.
