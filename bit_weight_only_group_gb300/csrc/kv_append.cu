@@ -155,7 +155,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_append(const __grid_constant
         places[n % kPlaces] = p;
     };
     for (int i = 0; i < stages; i++) load(blockIdx.x + i * stride, i);
-    if (blockIdx.x < units) find(0);
+    if (blockIdx.x >= units) return;   // fewer tokens in use than rows
+    find(0);
     __syncthreads();
 
     // a thread keeps its 16 values' place in the head, and with it its cosines and sines, for all its heads
@@ -237,7 +238,7 @@ cudaError_t launch(const AppendArgs& a, cudaStream_t s)
     const int heads = a.heads_q + 2 * a.c.heads, chunks = (int)ceil_div(heads, kStageBytes / (D * (int)sizeof(TI)));
     const int64_t units = (int64_t)a.bt.T * chunks, grid = std::min<int64_t>(units, 2 * num_sms());
     const int stages = (int)std::min<int64_t>(kStages, ceil_div(units, grid)), smem = stages * kStageBytes;
-    if (smem > 48 * 1024) {
+    if (stages > 1) {   // with the places, above the 48 KB that need no attribute
         static std::atomic<unsigned long long> done{0};
         const cudaError_t e = allow_smem(kernel, kStages * kStageBytes, done);
         if (e != cudaSuccess) return e;

@@ -106,6 +106,30 @@ def test_batch_sizes_and_empty_sequences(qg, B):
     _check(qg, c, BF, 64)
 
 
+@pytest.mark.parametrize("used", [0, 1, 5])
+def test_fewer_tokens_than_rows(qg, used):
+    # rows of no sequence, as in a captured step whose batch has shrunk: nothing is read or written for them
+    c = Case([1] * used or [0], [3] * max(used, 1), 9, 4, 2, 128, 16, BF, seed=40, spare_tokens=300, garbage=3.0)
+    if used:
+        _check(qg, c, BF, 128)
+    else:
+        before = c.k.clone()
+        k = torch.randn((c.T, 2, 128), device="cuda").to(BF)
+        qg.qkv_append(c.cache(qg), c.batch(qg), k, k, rope=_rope(20, 128))
+        torch.cuda.synchronize()
+        assert qg.qgemm_device_status() == 0 and torch.equal(before.view(torch.int16), c.k.view(torch.int16))
+
+
+def test_many_tokens_a_cta(qg):
+    # more than 32 units a CTA, over sequences of all lengths, heads that take several units a token
+    n_q = [(37 * b) % 61 for b in range(330)]
+    c = Case(n_q, [n + b % 7 for b, n in enumerate(n_q)], 5, 2, 2, 64, 16, FP, seed=41, garbage=3.0)
+    _check(qg, c, F32, 32)
+    n_q = [150, 0, 211, 3]
+    c = Case(n_q, [n + 3 for n in n_q], 5, 128, 32, 128, 64, BF, False, seed=42, garbage=3.0)
+    _check(qg, c, F32, 128, interleaved=True)
+
+
 def test_given_positions(qg):
     c = Case([3, 2], [3, 40], 10, 4, 2, 128, 16, BF, seed=4, garbage=3.0)
     _check(qg, c, BF, 128, positions=torch.tensor([0, 44, 7, 7, 1], dtype=torch.int32, device="cuda"))

@@ -201,6 +201,16 @@ def test_offsets_past_32_bits(qg):
     torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("prefix", [0, 400, 3000])
+def test_fewer_tokens_than_rows(qg, prefix):
+    # a batch that has shrunk: most rows belong to no sequence, in each of the ways a call is run
+    for n_q in ([1, 1], [100, 3], [0, 0], [0, 7]):
+        c = Case(n_q, [n + 5 for n in n_q], prefix, 64, 8, 128, 64, BF, seed=43, spare_tokens=200)
+        check_attention(c, *_run(qg, c))
+    c = Case([1, 0, 1] + [0] * 60, [9] * 63, prefix, 64, 8, 128, 64, BF, seed=44, spare_tokens=61)
+    check_attention(c, *_run(qg, c))
+
+
 def test_captured_graph_with_new_lengths(qg):
     # lengths and tables are read when the graph runs
     c = Case([1] * 4, [10, 60, 100, 128], 300, 8, 2, 128, 16, BF, seed=18, poison=False)
