@@ -399,9 +399,11 @@ QG_API qg_status qgemm_moe_grouped_multi(const uint16_t* x, int32_t T, const int
 
 /* Status word of the library's kernels on the current device: QG_OK, or
  * QG_ERR_TIMEOUT once a bounded wait of the tensor-core product (M above the
- * decode range) on its shared-memory rings gave up (the kernel then finished
- * without hanging, and the outputs of that call are not valid).  The pages define no such call; it exists because
- * the kernels never trap or spin without a limit.
+ * decode range) or of the paged-cache kernels on their shared-memory rings gave
+ * up (the kernel then finished without hanging, and the outputs of that call
+ * are not valid), or QG_ERR_DEVICE_STATUS once a paged-cache kernel met a
+ * length, page or position outside its bounds.  The pages define no such call;
+ * it exists because the kernels never trap or spin without a limit.
  *   status  host int32: receives the word.
  *   reset   non-zero: clear the word after reading it.
  * Synchronous: waits for the device (cudaMemcpy), so it is a check between
@@ -411,8 +413,9 @@ QG_API qg_status qgemm_device_status(int32_t* status, int32_t reset);
 
 /*
  * Programmatic dependent launch of the dense products (decode and
- * tensor-core kernels, with their x conversion and split-K sum), process-wide
- * (default on).  On, a product may start, and read its weight buffers,
+ * tensor-core kernels, with their x conversion and split-K sum) and of the
+ * paged-cache kernels (which read nothing before the kernel ahead of the call
+ * has finished), process-wide (default on).  On, a product may start, and read its weight buffers,
  * before the kernel launched just before it on the stream has finished (see
  * qgemm_forward's ordering note).  enable = 0 turns this off for every later
  * call: each kernel then starts only after the previous kernel on its
