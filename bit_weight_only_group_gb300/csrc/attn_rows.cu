@@ -164,7 +164,7 @@ __device__ __forceinline__ void work(const CUtensorMap& kmap, const CUtensorMap&
             return j < it.np ? page_of(a, a.bt.prefix_table, n_prefix, key >> a.c.page_shift)
                              : page_of(a, own_table, a.bt.table_ld, key >> a.c.page_shift);
         };
-        int s = 0;
+        int s = 0, issued = 0;
         uint32_t ph = 0;
         int page = page_at(it.tile0);
         for (int j = it.tile0; j < it.tile1; j++) {
@@ -180,7 +180,13 @@ __device__ __forceinline__ void work(const CUtensorMap& kmap, const CUtensorMap&
                             key & ((1 << a.c.page_shift) - 1), 0, head, page, full(s));
             }
             page = next;
+            issued++;
             if (++s == stages) { s = 0; ph ^= 1u; }
+        }
+        // no copy is in flight when the CTA leaves, not even after a wait that gave up
+        for (int i = min(stages, issued); i > 0; i--) {
+            if (s-- == 0) { s = stages - 1; ph ^= 1u; }
+            ok = ptx::mbar_wait(full(s), ph) && ok;
         }
     } else {
         // ------------------------------------------------ products

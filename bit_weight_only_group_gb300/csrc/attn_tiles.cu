@@ -441,6 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool busy = half < HALVES;
             const int in_page_mask = (1 << a.c.page_shift) - 1;
             int pos = 0;                                       // loads so far
+            int q_loaded = -1;                                 // phase of the last load of Q
             uint32_t item_phase = 0, tail_phase = 0;
             for (; ok && next_item<KEYS>(a, deal, lay, cur, false, it); item_phase ^= 1u) {
                 const int n = it.blk1 - it.blk0;
@@ -496,6 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tma_load_3d(sbase + s * C::TILE + h * C::HALF, &qmap, 64 * h, it.head * a.group,
                                         it.t0 + s * per, q_full);
                 }
+                q_loaded = (int)item_phase;
                 __syncwarp();
                 for (int j = 1; ok && j <= n; j++) {
                     const int next = j < n ? page_at(it.blk0 + j) : 0;
@@ -504,6 +506,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     page = next;
                 }
             }
+            // no copy is in flight when the CTA leaves, not even after a wait that gave up
+            for (int i = max(0, pos - NS); i < pos; i++) ok = ptx::mbar_wait(kv_full(i % NS), (i / NS) & 1) && ok;
+            if (q_loaded >= 0) ok = ptx::mbar_wait(q_full, (uint32_t)q_loaded) && ok;
         } else if (warp == kWarpMma && elect_lane()) {
             // ------------------------------------------------ matrix products, by one lane
             constexpr uint32_t id_qk = idesc<T>(KB, false), id_pv = idesc<T>(D, true);

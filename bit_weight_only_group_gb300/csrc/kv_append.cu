@@ -224,6 +224,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_append(const __grid_constant
         // the stage has been read, and the next place is there
         if (__syncthreads_or(!ok)) {
             if (threadIdx.x == 0 && a.status) atomicExch(a.status, (int)QG_ERR_TIMEOUT);
+            // no copy is in flight when the CTA leaves
+            for (int i = 0; i < stages && unit + i * stride < units; i++) {
+                ptx::mbar_wait(bars + 8 * stage, phase);
+                if (++stage == stages) { stage = 0; phase ^= 1u; }
+            }
             return;
         }
         load(unit + stages * stride, stage);
