@@ -226,27 +226,27 @@ __device__ __forceinline__ void join_row(const Args& a, int t, int hq, int piece
     float2 ml = load_ml(lane);
     load_o(0);
     const bool mine = t < (used ? min(max(__ldg(used), 0), a.bt.T) : a.bt.T);
-    float m = ml.y > 0.0f ? ml.x : -INFINITY, l = 0.0f;
+    float m = ml.y != 0.0f ? ml.x : -INFINITY, l = 0.0f;
     for (int p = LANES + lane; p < n; p += LANES) {
         const float2 w = load_ml(p);
-        if (w.y > 0.0f) m = fmaxf(m, w.x);
+        if (w.y != 0.0f) m = fmaxf(m, w.x);
     }
 #pragma unroll
     for (int i = LANES / 2; i > 0; i /= 2) m = fmaxf(m, __shfl_xor_sync(mask, m, i, LANES));
     float o[8];
 #pragma unroll
     for (int e = 0; e < 8; e++) o[e] = 0.0f;
-    float w = ml.y > 0.0f ? exp2_approx(ml.x - m) : 0.0f;
+    float w = ml.y != 0.0f ? exp2_approx(ml.x - m) : 0.0f;
     for (int p0 = 0; p0 < n; p0 += AT_ONCE) {
         if (p0 && p0 % LANES == 0) {
             ml = load_ml(p0 + lane);
-            w = ml.y > 0.0f ? exp2_approx(ml.x - m) : 0.0f;
+            w = ml.y != 0.0f ? exp2_approx(ml.x - m) : 0.0f;
         }
 #pragma unroll
         for (int i = 0; i < AT_ONCE; i++) {
             const float wp = __shfl_sync(mask, w, (p0 + i) % LANES, LANES);
             const float lp = __shfl_sync(mask, ml.y, (p0 + i) % LANES, LANES);
-            if (p0 + i < n && wp > 0.0f) {
+            if (p0 + i < n && lp != 0.0f) {
                 l = fmaf(wp, lp, l);
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
@@ -260,7 +260,7 @@ __device__ __forceinline__ void join_row(const Args& a, int t, int hq, int piece
         load_o(p0 + AT_ONCE);
     }
     if (!mine) return;
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const float inv = inverse(l);
     uint32_t bits[8];
 #pragma unroll
     for (int e = 0; e < 8; e++) bits[e] = __float_as_uint(o[e] * inv);

@@ -68,9 +68,12 @@ __device__ __forceinline__ void store_out8(const Args& a, long long at, const ui
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at) = w;
     }
 }
+// A sum l of 0 says that nothing was seen.  A NaN among the logits makes l a
+// NaN, which is not 0: such a row, or part of one, is kept and stays a NaN.
+__device__ __forceinline__ float inverse(float l) { return l != 0.0f ? 1.0f / l : 0.0f; }
 __device__ __forceinline__ void store_lse(const Args& a, long long row, float m, float l)
 {
-    if (a.lse) a.lse[row] = l > 0.0f ? kLn2 * (m + log2f(l)) : -INFINITY;
+    if (a.lse) a.lse[row] = l != 0.0f ? kLn2 * (m + log2f(l)) : -INFINITY;
 }
 
 __device__ __forceinline__ float exp2_approx(float x)

@@ -377,7 +377,7 @@ __device__ __forceinline__ void work(const CUtensorMap& kmap, const CUtensorMap&
                 const float m = e ? m1 : m0, l = e ? l1 : l0;
                 const long long row = (long long)tok * a.heads_q + hq;
                 if (final) {
-                    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                    const float inv = inverse(l);
 #pragma unroll
                     for (int i = 0; i < D / 8; i++)
                         store_out2(a, tok * a.ldo + (long long)hq * D + 8 * i + 2 * (lane % 4), o[i][2 * e] * inv,
@@ -386,7 +386,7 @@ __device__ __forceinline__ void work(const CUtensorMap& kmap, const CUtensorMap&
                 } else {
                     const long long at = (long long)(sp.part0 + part) * a.rows + row;
                     if (lane % 4 == 0) a.part_ml[at] = make_float2(m, l);
-                    if (l > 0.0f)
+                    if (l != 0.0f)
 #pragma unroll
                         for (int i = 0; i < D / 8; i++)
                             *reinterpret_cast<float2*>(a.part_o + at * D + 8 * i + 2 * (lane % 4)) =

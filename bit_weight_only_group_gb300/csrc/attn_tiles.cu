@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int hq = it.head * a.group + (r - tok_in_tile * a.group);
                 const long long row = (long long)tok * a.heads_q + hq;
                 const bool final = it.whole;
-                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                const float inv = inverse(l);
                 if (final) { w0 *= inv; w1 *= inv; }
                 const long long at = (long long)it.part * a.rows + row;
                 if (in) {
@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (!in) continue;
                     if (!final) {
-                        if (l > 0.0f)
+                        if (l != 0.0f)
 #pragma unroll
                             for (int e = 0; e < 32; e += 8) store32(a.part_o + at * D + 32 * c + e, o + e);
                     } else {

@@ -581,9 +581,10 @@ QG_API qg_status qkv_append(const qg_kv_cache* cache, const qg_kv_batch* batch, 
  *            be kept or cleared between calls.
  * A token that sees nothing (kv_len below n_b, no prefix) gets out = 0 and
  * lse = -inf.  What lies past kv_len or prefix_len in a page is never used,
- * whatever it holds; cached values in reach must be finite.  Logits, the
- * softmax's maximum and sum, and the sums over v are held in fp32; p is
- * rounded to the cache's type for the product with v.  The result does not
+ * whatever it holds.  A value in reach that is not finite stays in its
+ * sequence (and its key/value head), where also new tokens before its own may
+ * become NaN.  Logits, the softmax's maximum and sum, and the sums over v are
+ * held in fp32; p is rounded to the cache's type for the product with v.  The result does not
  * depend on the order in which blocks run (repeatable bit for bit).
  * Errors: QG_ERR_INVALID_ARG, QG_ERR_UNSUPPORTED, QG_ERR_ALIGNMENT,
  * QG_ERR_WORKSPACE, QG_ERR_CUDA.

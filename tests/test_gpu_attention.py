@@ -110,6 +110,46 @@ def test_whatever_lies_past_a_length(qg, garbage, n_q, kv):
     check_attention(c, *_run(qg, c))
 
 
+@pytest.mark.parametrize("n_q,kv,prefix", [([1, 1, 1], [70, 2000, 33], 0), ([1] * 5, [9, 300, 1, 64, 65], 700),
+                                           ([1] * 33, [200] * 33, 2500), ([4] * 20, [70] * 20, 2500),
+                                           ([130, 90, 70], [130, 200, 70], 333)])
+def test_not_finite_stays_not_finite_and_in_its_place(qg, n_q, kv, prefix):
+    # a NaN key makes the rows that see it NaN in any way a call is split, and changes no bit of any other row
+    c = Case(n_q, kv, prefix, 64, 8, 128, 16, BF, seed=40)
+    clean, lse0 = _run(qg, c)
+    check_attention(c, clean, lse0)
+    rows = torch.arange(c.cu[1], c.cu[2], device="cuda")
+
+    def places(key):   # of sequence 1
+        return c.table[1, key // c.page].item(), key % c.page
+
+    def expect(seen, out, lse, heads):
+        bad = torch.zeros((c.T, c.heads_q), dtype=torch.bool, device="cuda")
+        bad[seen[:, None], torch.tensor(heads, device="cuda")] = True
+        assert out[bad].isnan().all() and lse[bad].isnan().all()
+        assert torch.equal(out[~bad], clean[~bad]) and torch.equal(lse[~bad], lse0[~bad])
+
+    for key, seen in ((0, rows), (kv[1] - 1, rows[-1:])):   # seen by all of the sequence's tokens, by its last alone
+        page, at = places(key)
+        kept = c.k[page, at, 2, 5].clone()
+        c.k[page, at, 2, 5] = math.nan
+        expect(seen, *_run(qg, c), list(range(16, 24)))
+        c.k[page, at, 2, 5] = kept
+    if prefix:
+        page = c.prefix_table[prefix // 2 // c.page].item()
+        kept = c.k[page, 0, 7, 100].clone()
+        c.k[page, 0, 7, 100] = math.nan
+        expect(torch.arange(c.T, device="cuda"), *_run(qg, c), list(range(56, 64)))
+        c.k[page, 0, 7, 100] = kept
+    # an infinite value of the first own key: that column of its rows alone
+    page, at = places(0)
+    c.v[page, at, 0, 9] = math.inf
+    out, lse = _run(qg, c)
+    bad = torch.zeros_like(out, dtype=torch.bool)
+    bad[c.cu[1]:c.cu[2], :8, 9] = True
+    assert (~torch.isfinite(out[bad])).all() and torch.equal(out[~bad], clean[~bad]) and torch.equal(lse, lse0)
+
+
 @pytest.mark.parametrize("out_dtype", [torch.float32, BF, FP])
 def test_output_types_and_scale(qg, out_dtype):
     c = Case([1, 1, 40], [50, 3, 90], 500, 8, 4, 128, 32, BF, seed=8)
