@@ -18,10 +18,17 @@ Entry points (same names as the C ABI):
   written to the pages of a :class:`KVCache`
 * ``qattn_forward(q, cache, batch)`` -> attention over a shared prefix and each
   sequence's own cached tokens (:class:`KVBatch`)
+
+``stream`` (every call that launches kernels): a torch stream or a raw
+cudaStream_t, the current stream by default.  What a call allocates itself, its
+results and its scratch memory, is allocated on that stream, as under
+``torch.cuda.stream(stream)``.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 from dataclasses import dataclass
 
@@ -151,6 +158,32 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _as_stream(stream) -> torch.cuda.Stream:
+    """torch's view of a stream argument that is not None."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if handle in (0, 1):   # the legacy default stream, by either of its handles
+        return torch.cuda.default_stream()
+    return torch.cuda.ExternalStream(handle)
+
+
+def _on_stream(f):
+    """Runs f with its ``stream`` argument as the current stream: a block of
+    the caching allocator is reused in the order of the stream it was allocated
+    on, so what f allocates for kernels of another stream must come from there."""
+    at = list(inspect.signature(f).parameters).index("stream")
+
+    @functools.wraps(f)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return f(*args, **kw)
+        with torch.cuda.stream(_as_stream(stream)):
+            return f(*args, **kw)
+    return call
+
+
 def _ptr(t: torch.Tensor | None):
     return ctypes.c_void_p(t.data_ptr()) if t is not None and t.numel() else None
 
@@ -239,6 +272,7 @@ class QWeight:
                    if t is not None)
 
 
+@_on_stream
 def qpack_quantize(W: torch.Tensor, bits: int, group: int, outlier_frac: float = 0.0,
                    out: QWeight | None = None, workspace: torch.Tensor | None = None, stream=None,
                    mode: str = "asymmetric", scale_fmt: str = "fp16", fb_cap: int | None = None) -> QWeight:
@@ -262,6 +296,7 @@ def qpack_quantize(W: torch.Tensor, bits: int, group: int, outlier_frac: float =
     return qw
 
 
+@_on_stream
 def qpack_quantize_noalloc(W: torch.Tensor, bits: int, group: int, outlier_frac: float = 0.0,
                            out: QWeight | None = None, stream=None, scale_fmt: str = "fp16") -> QWeight:
     """qpack_quantize for callers that cannot allocate device memory: the
@@ -286,6 +321,7 @@ def qgemm_workspace_size(M: int, qw: QWeight) -> int:
     return b.value
 
 
+@_on_stream
 def qgemm_forward(x: torch.Tensor, qw: QWeight, out: torch.Tensor | None = None,
                   out_dtype: torch.dtype = torch.float32, workspace: torch.Tensor | None = None,
                   stream=None) -> torch.Tensor:
@@ -308,6 +344,7 @@ def qgemm_forward(x: torch.Tensor, qw: QWeight, out: torch.Tensor | None = None,
     return out
 
 
+@_on_stream
 def qgemm_forward_multi(x: torch.Tensor, qws, outs=None, out_dtype: torch.dtype = torch.float32,
                         workspace: torch.Tensor | None = None, stream=None):
     """[y_q [M, N_q] for each weight]: the products of x with up to four
@@ -349,6 +386,7 @@ def qgemm_moe_workspace_size(T: int, k: int, experts) -> int:
     return b.value
 
 
+@_on_stream
 def qgemm_moe_grouped(x: torch.Tensor, topk_ids: torch.Tensor, experts, out: torch.Tensor | None = None,
                       out_dtype: torch.dtype = torch.float32, workspace: torch.Tensor | None = None,
                       stream=None) -> torch.Tensor:
@@ -371,6 +409,7 @@ def qgemm_moe_grouped(x: torch.Tensor, topk_ids: torch.Tensor, experts, out: tor
     return out
 
 
+@_on_stream
 def qgemm_moe_grouped_multi(x: torch.Tensor, topk_ids: torch.Tensor, experts_per_product, outs=None,
                             out_dtype: torch.dtype = torch.float32, workspace: torch.Tensor | None = None,
                             stream=None) -> list:
@@ -418,6 +457,7 @@ def qgemm_device_status(reset: bool = False) -> int:
     return v.value
 
 
+@_on_stream
 def qgemm_selftest_bounded_wait(poll_limit: int = 2, stream=None) -> None:
     """Launch the kernel whose bounded mbarrier wait must give up; afterwards
     qgemm_device_status() reads QG_ERR_TIMEOUT (-6)."""
@@ -430,6 +470,7 @@ class QgDiag(ctypes.Structure):
                 ("max_range_ratio", ctypes.c_double), ("groups_over", ctypes.c_int64)]
 
 
+@_on_stream
 def qdiag_layer(W: torch.Tensor, qw: QWeight, threshold: float = 8.0, ratio: bool = False, stream=None):
     """Diagnostics of qw against the original fp16 W [N, K] (CUDA), computed
     on the device: dict of max_abs_err, rmse, cosine, max_range_ratio,
@@ -454,6 +495,7 @@ def qdiag_layer(W: torch.Tensor, qw: QWeight, threshold: float = 8.0, ratio: boo
     return o
 
 
+@_on_stream
 def qgemm_forward_w8a8(x: torch.Tensor, qw: QWeight, out: torch.Tensor | None = None,
                        out_dtype: torch.dtype = torch.float32, workspace: torch.Tensor | None = None,
                        stream=None) -> torch.Tensor:
@@ -476,6 +518,7 @@ def qgemm_forward_w8a8(x: torch.Tensor, qw: QWeight, out: torch.Tensor | None = 
     return out
 
 
+@_on_stream
 def qrepack_tiles(qw: QWeight, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The tile-ordered copy of qw (uint8 CUDA tensor) for qgemm_forward_tiles."""
     b = ctypes.c_size_t()
@@ -487,6 +530,7 @@ def qrepack_tiles(qw: QWeight, out: torch.Tensor | None = None, stream=None) -> 
     return out
 
 
+@_on_stream
 def qgemm_forward_tiles(x: torch.Tensor, qw: QWeight, tiles: torch.Tensor, out: torch.Tensor | None = None,
                         out_dtype: torch.dtype = torch.float32, workspace: torch.Tensor | None = None,
                         stream=None) -> torch.Tensor:
@@ -603,6 +647,7 @@ def _raw_stream(stream, index: int) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+@_on_stream
 def qkv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, q: torch.Tensor | None = None,
                rope: torch.Tensor | None = None, positions: torch.Tensor | None = None, interleaved: bool = False,
                q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
@@ -650,6 +695,7 @@ def qattn_workspace_size(cache: KVCache, batch: KVBatch, heads_q: int) -> int:
     return b.value
 
 
+@_on_stream
 def qattn_forward(q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: float | None = None,
                   out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
                   lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
