@@ -566,6 +566,8 @@ class KVCache:
             raise ValueError("k and v must be 4-D with the same shape, strides and dtype")
         if k.dtype not in (torch.bfloat16, torch.float16) or not k.is_cuda or not v.is_cuda or k.stride(3) != 1:
             raise ValueError("k and v must be bfloat16 or float16 CUDA tensors with unit inner stride")
+        if k.device != v.device:
+            raise ValueError("k and v must lie on one device")
         self.k, self.v, self.dtype, self.device = k, v, k.dtype, k.device
         self.num_pages, self.page_size, self.heads_kv, self.head_dim = k.shape
         self._desc = QgKvCache(k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype], *k.shape, *k.stride()[:3])
@@ -603,6 +605,10 @@ class KVBatch:
             if table.dtype != torch.int32 or not table.is_cuda or table.dim() != 2 or table.shape[0] != B or \
                     (table.shape[1] > 1 and table.stride(1) != 1):
                 raise ValueError("table must be an int32 CUDA tensor [B, width] with unit inner stride")
+        self.device = kv_len.device
+        for name, t in (("table", table), ("cu_q", cu_q), ("prefix_table", prefix_table)):
+            if t is not None and t.device != self.device:
+                raise ValueError(f"{name} must lie on the device of kv_len")
         if cu_q is None and tokens not in (None, B):
             raise ValueError("without cu_q every sequence has one new token")
         if cu_q is not None and tokens is None:
@@ -620,7 +626,10 @@ class KVBatch:
         self._ref = ctypes.byref(self._desc)
 
     def check(self, cache: KVCache):
-        """The tables hold an entry for every page the bounds reach."""
+        """The tables hold an entry for every page the bounds reach, and lie on
+        the cache's device."""
+        if self.device != cache.device:
+            raise ValueError(f"the batch lies on {self.device}, the cache on {cache.device}")
         if self._width * cache.page_size < self.max_kv:
             raise ValueError(f"table width {self._width} holds fewer than max_kv={self.max_kv} tokens")
         if self._shared * cache.page_size < self.prefix_len:
@@ -640,11 +649,15 @@ def _rows(t: torch.Tensor, name: str, T: int, heads: int, dim: int) -> int:
     raise ValueError(f"{name} must be a CUDA tensor [{T}, {heads or 'heads'}, {dim}]")
 
 
-def _raw_stream(stream, index: int) -> int:
-    """cudaStream_t of a stream argument; None: the device's current stream."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(index)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+def _check_devices(cache: KVCache, **tensors):
+    """The tensors lie on the cache's device, and that is the current one: the
+    library launches on the current device (with a stream argument, the
+    stream's)."""
+    for name, t in tensors.items():
+        if t is not None and t.device != cache.device:
+            raise ValueError(f"{name} lies on {t.device}, the cache on {cache.device}")
+    if torch.cuda.current_device() != cache.device.index:
+        raise ValueError(f"the cache lies on {cache.device}, the current device is cuda:{torch.cuda.current_device()}")
 
 
 @_on_stream
@@ -682,8 +695,9 @@ def qkv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor,
                                       positions.shape != (T,) or not positions.is_contiguous()):
             raise ValueError(f"positions must be a contiguous int32 CUDA tensor [{T}]")
         turn = QgRope(rope.data_ptr(), _ptr(positions), *rope.shape, interleaved)
+    _check_devices(cache, k=k, v=v, q=q, q_out=q_out, rope=rope, positions=positions)
     st = lib().qkv_append(cache._ref, batch._ref, turn, q_at, ldq, heads_q, k.data_ptr(), ldk, v.data_ptr(), ldv,
-                          _DTYPES[xt], out_at, ldq_out, _raw_stream(stream, cache.device.index))
+                          _DTYPES[xt], out_at, ldq_out, _stream(stream))
     if st != QG_OK:
         _check(st, "qkv_append")
     return q_out
@@ -721,10 +735,13 @@ def qattn_forward(q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: float 
         raise ValueError(f"lse must be a contiguous float32 CUDA tensor [{T}, {heads_q}]")
     if workspace is None:
         workspace = torch.empty(qattn_workspace_size(cache, batch, heads_q), dtype=torch.uint8, device=cache.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _check_devices(cache, q=q, out=out, lse=lse, workspace=workspace)
     st = lib().qattn_forward(cache._ref, batch._ref, q.data_ptr(), ldq, heads_q, D ** -0.5 if scale is None else scale,
                              out.data_ptr(), ldo, _DTYPES[out.dtype], None if lse is None else lse.data_ptr(),
                              workspace.data_ptr() or None, workspace.numel() * workspace.element_size(),
-                             _raw_stream(stream, cache.device.index))
+                             _stream(stream))
     if st != QG_OK:
         _check(st, "qattn_forward")
     return out
