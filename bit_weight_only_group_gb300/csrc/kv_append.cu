@@ -92,9 +92,10 @@ __device__ __forceinline__ Place find_place(const AppendArgs& a, int t, bool the
     if (!there) return p;
     int t0, t1, len;
     token_range(a.bt, b, t0, t1);
+    // a length outside its bound says nothing of where the token belongs: it is not cached, so that what is stays
     bool ok = own_length(a.bt, b, len) && t >= t0 && t < t1 && t1 - t0 <= a.bt.max_q;
     const int own = len - (t1 - t);   // len - n + i
-    if (own >= 0 && own < len) {
+    if (ok && own >= 0 && own < len) {
         const int e = own >> a.c.page_shift;
         const int page = e < a.bt.table_ld ? __ldg(a.bt.table + (long long)b * a.bt.table_ld + e) : -1;
         if (page >= 0 && page < a.c.num_pages) p.page = page;

@@ -167,6 +167,34 @@ def test_positions_and_places_outside_are_reported(qg):
     assert torch.equal(before, c.k)
 
 
+@pytest.mark.parametrize("heads_first", [True, False])
+def test_lengths_outside_their_bounds_leave_the_cache_alone(qg, heads_first):
+    # the sequence's keys so far are still there after a call that counted its tokens wrongly; other sequences are written
+    assert qg.qgemm_device_status(reset=True) == 0
+    c = Case([2, 1, 1], [40, 20, 33], 0, 4, 2, 128, 16, BF, heads_first, seed=10, garbage=3.0)
+    k, q = torch.randn((4, 2, 128), device="cuda").to(BF), torch.randn((4, 4, 128), device="cuda").to(BF)
+    where = [[(c.table_host[b, own // 16].item(), own % 16) for own in range(c.kv[b] - c.n_q[b], c.kv[b])] for b in range(3)]
+
+    def check(written, **bounds):
+        before_k, before_v = c.k.clone(), c.v.clone()
+        q_out = qg.qkv_append(c.cache(qg), c.batch(qg, **bounds), k, -k, q=q)
+        assert qg.qgemm_device_status(reset=True) == -7
+        for b in written:
+            for i, (page, place) in enumerate(where[b]):
+                before_k[page, place], before_v[page, place] = k[c.cu[b] + i], -k[c.cu[b] + i]
+        for a, b in ((before_k, c.k), (before_v, c.v)):
+            assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+        assert all(torch.equal(q_out[c.cu[b]:c.cu[b + 1]], q[c.cu[b]:c.cu[b + 1]]) for b in written)
+
+    check([1, 2], max_kv=39)          # sequence 0 is longer than its bound
+    check([1], max_kv=32)             # and sequence 2
+    check([1, 2], max_q=1)            # sequence 0 has more new tokens than its bound
+    for bad in (-1, -(1 << 31), 1 << 30, 0x7FFFFFFF):
+        c.kv_len[1] = bad
+        check([0, 2])
+    c.kv_len[1] = 20
+
+
 def test_append_then_attend(qg):
     """The two calls as a decoding step uses them: the appended tokens are what the attention sees."""
     from _paged import check_attention
