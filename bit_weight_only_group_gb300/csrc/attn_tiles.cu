@@ -262,22 +262,23 @@ __device__ __forceinline__ bool next_item(const Args& a, const Deal& d, const La
     }
 }
 
-// Inclusive sums over the block's threads; scratch holds 33 ints.
-__device__ __forceinline__ int block_sums(int v, int* scratch, int& total)
+// Inclusive sums over the block's threads.
+template <typename V>
+__device__ __forceinline__ V block_sums(V v, V (&scratch)[32], V& total)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int i = 1; i < 32; i *= 2) {
-        const int u = __shfl_up_sync(0xffffffffu, v, i);
+        const V u = __shfl_up_sync(0xffffffffu, v, i);
         if (lane >= i) v += u;
     }
     if (lane == 31) scratch[warp] = v;
     __syncthreads();
     if (warp == 0) {
-        int w = lane < (int)blockDim.x / 32 ? scratch[lane] : 0;
+        V w = lane < (int)blockDim.x / 32 ? scratch[lane] : 0;
 #pragma unroll
         for (int i = 1; i < 32; i *= 2) {
-            const int u = __shfl_up_sync(0xffffffffu, w, i);
+            const V u = __shfl_up_sync(0xffffffffu, w, i);
             if (lane >= i) w += u;
         }
         scratch[lane] = w;
@@ -293,27 +294,33 @@ __device__ __forceinline__ int block_sums(int v, int* scratch, int& total)
 // sequences, blocks over the pairs).
 __global__ void __launch_bounds__(1024) k_attn_layout(const __grid_constant__ Args a, const __grid_constant__ Layout lay)
 {
-    __shared__ int scratch[33];
+    __shared__ long long wide[32];
+    __shared__ int scratch[32];
     kv::pdl_wait();
     kv::pdl_release();
     const int per2 = 2 * lay.per;
-    int pairs = 0, total;
+    // Offsets that are not ascending may give every sequence all the tokens: 2^30 sequences of 2^22 pairs.  So the
+    // pairs are summed in 64 bits, and what is past max_pairs, more than ascending offsets can make, is left out:
+    // `first` stays ascending, so each pair kept lies within its sequence's tokens.
+    long long sum = 0;
     for (int b0 = 0; b0 < a.bt.B; b0 += (int)blockDim.x) {
         const int b = b0 + (int)threadIdx.x;
         int t0 = 0, t1 = 0;
         if (b < a.bt.B) kv::token_range(a.bt, b, t0, t1);
-        const int n = (t1 - t0 + per2 - 1) / per2, upto = block_sums(n, scratch, total);
-        if (b < a.bt.B) lay.first[b] = pairs + upto - n;
-        pairs += total;
+        const long long n = (t1 - t0 + per2 - 1) / per2;
+        long long total;
+        const long long upto = block_sums(n, wide, total);
+        if (b < a.bt.B) lay.first[b] = (int)min(sum + upto - n, (long long)lay.max_pairs);
+        sum += total;
     }
-    if (threadIdx.x == 0) lay.first[a.bt.B] = pairs;
-    if (pairs > lay.max_pairs) {   // offsets that are not ascending: more pairs than the tokens can make
-        if (threadIdx.x == 0) kv::report(a.status);
-        pairs = lay.max_pairs;
+    const int pairs = (int)min(sum, (long long)lay.max_pairs);
+    if (threadIdx.x == 0) {
+        lay.first[a.bt.B] = pairs;
+        if (sum > pairs) kv::report(a.status);
     }
     __syncthreads();
     const int np = (a.bt.prefix_len + KB - 1) / KB;
-    int blocks = 0;
+    int blocks = 0, total;
     for (int i0 = 0; i0 < pairs; i0 += (int)blockDim.x) {
         const int i = i0 + (int)threadIdx.x;
         Pair p{0, 0, 0};

@@ -331,6 +331,30 @@ def test_bad_lengths_and_pages_are_reported(qg):
     check_attention(c, *_run(qg, c))
 
 
+def test_offsets_whose_pairs_of_tiles_pass_32_bits(qg):
+    # every other sequence claims all 2^16 tokens, a tile holds one of them: the pairs of tiles add up to 2^31
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    assert qg.qgemm_device_status(reset=True) == 0
+    T, B = 1 << 16, (1 << 17) + 1
+    cache = qg.KVCache.empty(1, 16, 1, 64)
+    cache.k.fill_(1.0)
+    cache.v.fill_(2.0)
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    cu[1::2] = T
+    batch = qg.KVBatch(torch.zeros((B, 1), dtype=torch.int32, device="cuda"), torch.ones(B, dtype=torch.int32, device="cuda"),
+                       max_kv=1, cu_q=cu, max_q=1, tokens=T)
+    q = torch.zeros((T + 2, 128, 64), dtype=BF, device="cuda")
+    out = torch.full_like(q, 7.0)
+    qg.qattn_forward(q[1:-1], cache, batch, out=out[1:-1])
+    assert qg.qgemm_device_status(reset=True) == -7
+    assert (out[0] == 7.0).all() and (out[-1] == 7.0).all()
+    del q, out
+    torch.cuda.empty_cache()
+    c = Case([100, 90], [100, 90], 0, 16, 2, 128, 16, BF, seed=25)
+    check_attention(c, *_run(qg, c))
+
+
 def test_refusals(qg):
     c = Case([1, 1], [40, 30], 300, 8, 2, 128, 16, BF, seed=23)
     cache, batch = c.cache(qg), c.batch(qg)
