@@ -84,8 +84,7 @@ __device__ __forceinline__ Item find_item(const Args& a, int unit, int row_block
     int t0, t1;
     bool ok = true;
     if (KEYS & kOwn) {
-        kv::token_range(a.bt, unit, t0, t1);
-        ok = t1 - t0 <= a.bt.max_q;
+        ok = kv::token_range(a.bt, unit, t0, t1);
     } else {
         t0 = 0;
         t1 = kv::used_tokens(a.bt);

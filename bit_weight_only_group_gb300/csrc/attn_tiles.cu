@@ -203,7 +203,7 @@ struct Cursor {
 
 // The CTA's next item, or false past the end.
 template <int KEYS>
-__device__ __forceinline__ bool next_item(const Args& a, const Deal& d, const Layout& lay, Cursor& cur, bool tell, Item& it)
+__device__ __forceinline__ bool next_item(const Args& a, const Deal& d, const Layout& lay, Cursor& cur, Item& it)
 {
     it.own0 = it.own = 0;
     it.b = 0;
@@ -245,8 +245,7 @@ __device__ __forceinline__ bool next_item(const Args& a, const Deal& d, const La
         kv::token_range(a.bt, p.b, t0, it.t1);
         it.two = it.t1 - it.t0 > lay.per;
         int len;
-        const bool ok = kv::own_length(a.bt, p.b, len) && it.t1 - t0 <= a.bt.max_q;
-        if (!ok && tell) kv::report(a.status);
+        kv::own_length(a.bt, p.b, len);   // the layout kernel has reported what is outside its bounds
         it.own0 = len - (it.t1 - it.t0) + 1;
         it.own = max(0, it.own0 + min(2 * lay.per, it.t1 - it.t0) - 1);
         it.blk0 = at - p.start;
@@ -306,7 +305,7 @@ __global__ void __launch_bounds__(1024) k_attn_layout(const __grid_constant__ Ar
     for (int b0 = 0; b0 < a.bt.B; b0 += (int)blockDim.x) {
         const int b = b0 + (int)threadIdx.x;
         int t0 = 0, t1 = 0;
-        if (b < a.bt.B) kv::token_range(a.bt, b, t0, t1);
+        if (b < a.bt.B && !kv::token_range(a.bt, b, t0, t1)) kv::report(a.status);
         const long long n = (t1 - t0 + per2 - 1) / per2;
         long long total;
         const long long upto = block_sums(n, wide, total);
@@ -334,7 +333,7 @@ __global__ void __launch_bounds__(1024) k_attn_layout(const __grid_constant__ Ar
             }
             int t0, t1, len;
             kv::token_range(a.bt, p.b, t0, t1);
-            kv::own_length(a.bt, p.b, len);
+            if (!kv::own_length(a.bt, p.b, len)) kv::report(a.status);
             p.t0 = t0 + (i - lay.first[p.b]) * per2;
             const int own = len - (t1 - min(p.t0 + per2, t1));   // own tokens the pair's last token sees
             n = max(1, np + (max(0, own) + KB - 1) / KB);        // 1: a pair that sees nothing is still written
@@ -450,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int pos = 0;                                       // loads so far
             int q_loaded = -1;                                 // phase of the last load of Q
             uint32_t item_phase = 0, tail_phase = 0;
-            for (; ok && next_item<KEYS>(a, deal, lay, cur, false, it); item_phase ^= 1u) {
+            for (; ok && next_item<KEYS>(a, deal, lay, cur, it); item_phase ^= 1u) {
                 const int n = it.blk1 - it.blk0;
                 const int n_prefix = (it.prefix + in_page_mask) >> a.c.page_shift;
                 const int* own_table = (KEYS & kOwn) ? a.bt.table + (long long)it.b * a.bt.table_ld : nullptr;
@@ -547,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::tc_fence_after();
                 return r;
             };
-            for (; ok && next_item<KEYS>(a, deal, lay, cur, false, it); item_phase ^= 1u) {
+            for (; ok && next_item<KEYS>(a, deal, lay, cur, it); item_phase ^= 1u) {
                 const int n = it.blk1 - it.blk0;
                 const int step = it.two ? 1 : 2;       // a stream's next block
                 ok = ptx::mbar_wait(q_full, item_phase);
@@ -605,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tok_in_tile = r / a.group;
         uint32_t s_phase = 0, o_phase = 0, join_phase = 0;
         const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
-        while (ok && next_item<KEYS>(a, deal, lay, cur, threadIdx.x == 0, it)) {
+        while (ok && next_item<KEYS>(a, deal, lay, cur, it)) {
             const int n = it.blk1 - it.blk0, step = it.two ? 1 : 2;
             const int tok = it.t0 + (it.two ? s * per : 0) + tok_in_tile;
             const bool in = tok_in_tile < per && tok < it.t1;

@@ -91,9 +91,10 @@ __device__ __forceinline__ Place find_place(const AppendArgs& a, int t, bool the
     const int b = find_sequences(a.bt, t);
     if (!there) return p;
     int t0, t1, len;
-    token_range(a.bt, b, t0, t1);
-    // a length outside its bound says nothing of where the token belongs: it is not cached, so that what is stays
-    bool ok = own_length(a.bt, b, len) && t >= t0 && t < t1 && t1 - t0 <= a.bt.max_q;
+    // a length or an offset outside its bound says nothing of where the token belongs: it is not cached, so that what is
+    // stays
+    bool ok = token_range(a.bt, b, t0, t1) && t >= t0 && t < t1;
+    ok = own_length(a.bt, b, len) && ok;
     const int own = len - (t1 - t);   // len - n + i
     if (ok && own >= 0 && own < len) {
         const int e = own >> a.c.page_shift;

@@ -50,16 +50,19 @@ __device__ __forceinline__ void report(int* status)
     if (status) atomicExch(status, (int)QG_ERR_DEVICE_STATUS);
 }
 
-// Token rows [t0, t1) of sequence b, cut to the array.
-__device__ __forceinline__ void token_range(const Batch& bt, int b, int& t0, int& t1)
+// Token rows [t0, t1) of sequence b, cut to the array; false if they had to
+// be, or if there are more than the bound.
+__device__ __forceinline__ bool token_range(const Batch& bt, int b, int& t0, int& t1)
 {
     if (!bt.cu_q) {
         t0 = b;
         t1 = min(b + 1, bt.T);
-        return;
+        return true;
     }
-    t0 = min(max(__ldg(bt.cu_q + b), 0), bt.T);
-    t1 = min(max(__ldg(bt.cu_q + b + 1), t0), bt.T);
+    const int from = __ldg(bt.cu_q + b), to = __ldg(bt.cu_q + b + 1);
+    t0 = min(max(from, 0), bt.T);
+    t1 = min(max(to, t0), bt.T);
+    return t0 == from && t1 == to && t1 - t0 <= bt.max_q;
 }
 
 // Rows that belong to a sequence: [0, used_tokens).

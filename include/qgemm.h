@@ -511,9 +511,9 @@ typedef struct {
  *               token a sequence (T = B, max_q = 1).
  *  prefix_table int32 [ceil(prefix_len / page_size)] (NULL when prefix_len = 0).
  *  prefix_len   tokens of the shared prefix (a host value; 0: none).
- * A length outside its bound is cut to it where keys are read, and nothing is
- * cached for it; a page number outside [0, num_pages) is not followed.  Both
- * set the device status word to QG_ERR_DEVICE_STATUS (see
+ * A length or offset outside its bound is cut to it where keys are read, and
+ * nothing is cached for it; a page number outside [0, num_pages) is not
+ * followed.  Both set the device status word to QG_ERR_DEVICE_STATUS (see
  * qgemm_device_status), and the outputs of the sequences concerned are then
  * not valid.
  */
@@ -554,8 +554,8 @@ typedef struct {
  * k (rotated) and v are written to their pages, q (rotated) to q_out, each
  * value computed in fp32 and rounded once to the cache's type.  A token whose
  * own place is negative, whose page number is invalid, or whose sequence has a
- * length outside its bound (L_b above max_kv or negative, n_b above max_q) is
- * not cached, and one whose position is outside the rotation table is not
+ * length or offset outside its bound (L_b above max_kv or negative, n_b above
+ * max_q, cu_q outside 0 .. T or descending) is not cached, and one whose position is outside the rotation table is not
  * written at all; both set the status word.  Two tokens must not share a place.
  * Pointers 16-byte aligned, leading dimensions multiples of 16 bytes.
  * Bounds-checked on the device as the batch's text says.

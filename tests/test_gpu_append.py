@@ -195,6 +195,20 @@ def test_lengths_outside_their_bounds_leave_the_cache_alone(qg, heads_first):
     c.kv_len[1] = 20
 
 
+def test_offsets_past_the_rows_are_reported(qg):
+    # the last sequence claims a row that is not there: it is not cached, the others are
+    assert qg.qgemm_device_status(reset=True) == 0
+    c = Case([2, 1, 2], [40, 20, 33], 0, 4, 2, 128, 16, BF, seed=11, garbage=3.0)
+    k = torch.randn((5, 2, 128), device="cuda").to(BF)
+    c.cu_q[3] = 6
+    before = c.k.clone()
+    qg.qkv_append(c.cache(qg), c.batch(qg), k, k)
+    assert qg.qgemm_device_status(reset=True) == -7
+    for t, (b, own) in enumerate([(0, 38), (0, 39), (1, 19)]):
+        before[c.table_host[b, own // 16].item(), own % 16] = k[t]
+    assert torch.equal(before, c.k)
+
+
 def test_append_then_attend(qg):
     """The two calls as a decoding step uses them: the appended tokens are what the attention sees."""
     from _paged import check_attention

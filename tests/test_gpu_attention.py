@@ -331,6 +331,23 @@ def test_bad_lengths_and_pages_are_reported(qg):
     check_attention(c, *_run(qg, c))
 
 
+@pytest.mark.parametrize("n_q,prefix", [([1, 1, 1], 0), ([1] * 5, 700), ([1] * 40, 2500), ([100, 90, 70], 300)])
+def test_offsets_past_the_rows_are_reported(qg, n_q, prefix):
+    # the last sequence claims rows that are not there, in each of the ways a call is run: the others are as they were
+    assert qg.qgemm_device_status(reset=True) == 0
+    c = Case(n_q, [n + 30 for n in n_q], prefix, 64, 8, 128, 64, BF, seed=26)
+    want, _ = _run(qg, c)
+    for past in (c.T + 1, 0x7FFFFFFF):
+        c.cu_q[-1] = past
+        out = qg.qattn_forward(c.q, c.cache(qg), c.batch(qg))
+        assert qg.qgemm_device_status(reset=True) == -7
+        assert torch.equal(out[:c.cu[-2]], want[:c.cu[-2]])
+    # and one without rows, past their end
+    c.cu_q[-2:] = c.T + 5
+    qg.qattn_forward(c.q, c.cache(qg), c.batch(qg))
+    assert qg.qgemm_device_status(reset=True) == -7
+
+
 def test_offsets_whose_pairs_of_tiles_pass_32_bits(qg):
     # every other sequence claims all 2^16 tokens, a tile holds one of them: the pairs of tiles add up to 2^31
     if torch.cuda.mem_get_info()[0] < 40 << 30:
