@@ -384,8 +384,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tail = bars + 96;      // a block of V with rows past the last key has arrived
     auto kv_full = [&](int x) { return bars + 104 + 8 * x; };
     auto kv_empty = [&](int x) { return bars + 104 + 8 * (NS + x); };
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 104 + 16 * NS);
-    static_assert(104 + 16 * NS + 4 <= 256, "barriers");
+    const uint32_t products_done = bars + 104 + 16 * NS;   // when the CTA leaves
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 112 + 16 * NS);
+    static_assert(112 + 16 * NS + 4 <= 256, "barriers");
     float2* ml1 = reinterpret_cast<float2*>(smem + C::OFF_ML);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -393,6 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_init(q_full, 1);
         ptx::mbar_init(q_empty, 1);
         ptx::mbar_init(tail, 1);
+        ptx::mbar_init(products_done, 1);
         for (int s = 0; s < 2; s++) {
             ptx::mbar_init(s_full(s), 1);
             ptx::mbar_init(p_full(s, 0), 4);
@@ -593,6 +595,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 base += 2 * n;
             }
+            // no product reads shared memory or writes tensor memory when the CTA leaves, not even after a wait that gave up
+            commit(products_done);
+            ok = ptx::mbar_wait(products_done, 0) && ok;
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
