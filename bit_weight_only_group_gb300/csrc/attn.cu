@@ -25,12 +25,11 @@ enum Way {
 // How a call is split.  Parts are numbered prefix first.
 struct Plan {
     Way way;
-    Parts n;        // parts of the row kernel's keys; most parts of an item (kTilesShared: of the prefix, kPrompts: own)
-    int parts;      // in all; 1: no joining, results are written at once
+    Parts n;        // parts of the row kernel's keys; kTilesShared: most pieces of the prefix
+    int parts;      // in all; 1: no joining, results are written at once (kPrompts: 0, its pieces have slots)
     int ctas;       // of the tile kernel
     Deal deal;      // kTilesShared
-    int64_t pairs;  // kPrompts: bound of the pairs of tiles of all sequences, and
-    int min_run;    // the least run of a CTA that keeps an item to its most parts
+    int64_t pairs;  // kPrompts: bound of the pairs of tiles of all sequences
 };
 
 // Parts of `tiles` tiles for `units` independent units of work: about `ctas`
@@ -162,13 +161,8 @@ Plan make_plan(const qg_kv_cache& c, const qg_kv_batch& b, int heads_q)
             p.n.prefix_parts = p.deal.most_pieces();
             break;
         case kPrompts: {
-            p.ctas = (int)sms;
             p.pairs = b.tokens / (2 * per) + b.sequences;
-            // an item's parts, from the run that the card gets when all the bounds are met half way
-            const int64_t longest = std::max<int64_t>(1, np + no);
-            const int64_t fair = std::max<int64_t>(2, c.heads_kv * ceil_div(b.tokens, 2 * per) * ((np + longest) / 2) / sms);
-            p.n.own_parts = (int)std::min<int64_t>(32, std::max<int64_t>(2, ceil_div(longest, fair) + 1));
-            p.min_run = (int)std::max<int64_t>(2, ceil_div(longest, p.n.own_parts - 1));
+            p.ctas = (int)std::min<int64_t>(sms, ceil_div(c.heads_kv * p.pairs * std::max<int64_t>(1, np + no), kMinRun));
             break;
         }
     }
@@ -183,12 +177,19 @@ struct Places {
 Places places(const Plan& p, const qg_kv_batch& b, int heads_q, int dim)
 {
     Places w{};
-    if (p.parts <= 1) return w;
-    const size_t rows = (size_t)b.tokens * heads_q;
-    w.ml = align_up(p.parts * rows * dim * 4, 256);
-    w.line = w.ml + align_up(p.parts * rows * sizeof(float2), 256);
+    size_t rows = p.parts * (size_t)b.tokens * heads_q;
+    if (p.way == kPrompts) {
+        // The slots of the CTAs' pieces: 41 MB with heads of 128 on 152 SMs, however long the prompts are.  Short
+        // prompts are asked for two parts of each row, up to 2^18 rows (139 MB), whether the slots fill that or not: a
+        // size that callers may have fixed, and that grows with the prompt no further.
+        rows = std::max((size_t)2 * p.ctas * kSlotRows, std::min<size_t>(2 * (size_t)b.tokens * heads_q, (size_t)1 << 18));
+    } else if (p.parts <= 1) {
+        return w;
+    }
+    w.ml = align_up(rows * dim * 4, 256);
+    w.line = w.ml + align_up(rows * sizeof(float2), 256);
     w.bytes = w.line;
-    if (p.pairs) {
+    if (p.way == kPrompts) {
         w.first = w.line + align_up(sizeof(Line), 256);
         w.pair = w.first + align_up((size_t)(b.sequences + 1) * 4, 256);
         w.cut = w.pair + align_up((size_t)(p.pairs + 1) * sizeof(Pair), 256);
@@ -198,20 +199,19 @@ Places places(const Plan& p, const qg_kv_batch& b, int heads_q, int dim)
 }
 
 // out[r] = sum_p w_p o_p / sum_p w_p l_p with w_p = 2^(m_p - max m), in the
-// order of the parts: dim / 8 lanes a row, 8 of its values a lane.  Part p <
-// pieces is in slot p, the others follow from slot part0 on.  Bound by latency
+// order of the parts: dim / 8 lanes a row, 8 of its values a lane.  slot(p) is
+// the place of part p's row.  Bound by latency
 // (the parts were just written and are in L2): the (m, l) and the values of
 // the first AT_ONCE parts are loaded at once, before anything that decides
 // whether they are wanted.  Few rows take eight parts at once; many take two,
 // in 48 registers, so that more rows run in a round.
-template <int D, int AT_ONCE>
-__device__ __forceinline__ void join_row(const Args& a, int t, int hq, int pieces, int part0, int n, const int* used)
+template <int D, int AT_ONCE, typename Slot>
+__device__ __forceinline__ void join_row(const Args& a, int t, int hq, int n, const int* used, Slot slot)
 {
     constexpr int LANES = D / 8;
     const int lane = threadIdx.x % LANES;
     const uint32_t mask = (LANES == 32 ? 0xffffffffu : (1u << LANES) - 1u) << (threadIdx.x % 32 / LANES * LANES);
     const long long row = (long long)t * a.heads_q + hq;
-    auto slot = [&](int p) { return (long long)(p < pieces ? p : part0 + p - pieces) * a.rows + row; };
     auto load_ml = [&](int p) { return p < n ? __ldcg(a.part_ml + slot(p)) : make_float2(-INFINITY, 0.0f); };
     float4 v[AT_ONCE][2];
     auto load_o = [&](int p0) {   // where a part saw nothing its values are unset, and are not used
@@ -281,7 +281,8 @@ __global__ void __launch_bounds__(256, AT_ONCE == 2 ? 5 : 2) k_attn_join(const _
     const int t = (int)(row / (uint32_t)a.heads_q), hq = (int)row - t * a.heads_q;
     int pieces = 0;
     if (d.blocks) pieces = d.pieces(hq / a.group, t < d.pairs * 2 * d.per ? d.groups : d.sgroups);
-    join_row<D, AT_ONCE>(a, t, hq, pieces, part0, pieces + parts, a.bt.cu_q ? a.bt.cu_q + a.bt.B : nullptr);
+    join_row<D, AT_ONCE>(a, t, hq, pieces + parts, a.bt.cu_q ? a.bt.cu_q + a.bt.B : nullptr,
+                         [&](int p) { return (long long)(p < pieces ? p : part0 + p - pieces) * a.rows + row; });
 }
 
 // The rows of items that the end of a CTA's run cut: kCutCtas CTAs for the 256
@@ -302,12 +303,14 @@ __global__ void __launch_bounds__(256, 5) k_attn_join_line(const __grid_constant
     if (p.start == at || first / line.run != c - 1) return;
     int t0, t1;
     kv::token_range(a.bt, p.b, t0, t1);
-    const int n = last / line.run - first / line.run + 1;
+    const int n = last / line.run - (c - 1) + 1, tile_rows = lay.per * a.group;
     for (int r = blockIdx.x % kCutCtas * (256 / kCutCtas) + threadIdx.x / (D / 8); r < (blockIdx.x % kCutCtas + 1) * (256 / kCutCtas);
          r += kJoinRows<D>) {
         const int t = p.t0 + r / a.group;
-        if (r >= 2 * lay.per * a.group || t >= t1) return;
-        join_row<D, 2>(a, t, head * a.group + r % a.group, n, 0, n, nullptr);
+        if (r >= 2 * tile_rows || t >= t1) return;
+        const int at = r < tile_rows ? r : 128 + r - tile_rows;
+        join_row<D, 2>(a, t, head * a.group + r % a.group, n, nullptr,
+                       [&](int p) { return (long long)lay.slot(c - 1, p) * kSlotRows + at; });
     }
 }
 
@@ -411,8 +414,8 @@ qg_status launch_attn(const qg_kv_cache& cache, const qg_kv_batch& batch, const 
     a.rows = (int64_t)batch.tokens * heads_q;
     const attn::Places w = attn::places(p, batch, heads_q, cache.head_dim);
     char* base = static_cast<char*>(ws);
-    a.part_o = p.parts > 1 ? reinterpret_cast<float*>(base) : nullptr;
-    a.part_ml = p.parts > 1 ? reinterpret_cast<float2*>(base + w.ml) : nullptr;
+    a.part_o = w.bytes ? reinterpret_cast<float*>(base) : nullptr;
+    a.part_ml = w.bytes ? reinterpret_cast<float2*>(base + w.ml) : nullptr;
     a.status = device_status_ptr();
     qg_status st = QG_OK;
     CUtensorMap qmap, kmap, vmap;
@@ -426,7 +429,7 @@ qg_status launch_attn(const qg_kv_cache& cache, const qg_kv_batch& batch, const 
         if (p.way == attn::kPrompts) {
             const attn::Layout lay{reinterpret_cast<attn::Line*>(base + w.line), reinterpret_cast<int*>(base + w.first),
                                    reinterpret_cast<attn::Pair*>(base + w.pair), reinterpret_cast<int*>(base + w.cut),
-                                   attn::tile_tokens(a.group), p.ctas, p.min_run, (int)p.pairs};
+                                   attn::tile_tokens(a.group), p.ctas, (int)p.pairs};
             e = attn::launch_tiles(a, cache.dtype, qmap, kmap, vmap, lay, s);
             if (e == cudaSuccess) e = attn::launch_join_line(a, lay, s);
         } else {

@@ -30,7 +30,8 @@ struct Args {
     long long ldo;
     int out_type;
     float* lse;                  // or null
-    // partial results: o of part p, row r at part_o + (p * rows + r) * dim, (m, l) at part_ml + p * rows + r
+    // partial results: o of part p, row r at part_o + (p * rows + r) * dim, (m, l) at part_ml + p * rows + r;
+    // those of prompts in slots of 256 rows (Layout)
     float* part_o;
     float2* part_ml;
     long long rows;              // T * heads_q
@@ -157,8 +158,10 @@ struct Deal {
 // sequences, each with the blocks its last token sees, are laid end to end for
 // a head, the heads after one another, and each CTA takes an equal run of
 // that line.  An item (a pair, a head) inside one run is written at once; one
-// that runs cross falls into pieces, one part each, joined afterwards.  The
-// lengths are on the device, so a small kernel lays the line out.
+// that runs cross falls into pieces, joined afterwards.  A CTA has at most two
+// pieces, one of an item that starts before its run and one of an item that
+// starts in it and ends after it, so two slots of a pair's 256 rows a CTA hold
+// them all.  The lengths are on the device, so a small kernel lays the line out.
 struct Line {
     int run;                  // blocks of a CTA
     int head;                 // blocks of a head
@@ -176,9 +179,13 @@ struct Layout {
     int* cut;                 // [ctas] pair in which the run of each CTA starts
     int per;                  // tokens of a tile
     int ctas;
-    int min_run;
     int max_pairs;            // entries of `pair` but one
+    // slot of piece p of an item that starts in the run of CTA c
+    __host__ __device__ int slot(int c, int p) const { return p == 0 ? 2 * c + 1 : 2 * (c + p); }
 };
+constexpr int kSlotRows = 256;   // the first tile's 128, the second's
+constexpr int kMinRun = 2;       // blocks: a CTA's start and end cost several
+constexpr int kMostPieces = 32;  // of an item: joining takes them two at a time, one after another
 
 // The kernels' launches.  A keys flag says what a row sees: the shared
 // prefix, its own sequence's tokens, or both in that order.

@@ -183,7 +183,7 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 
 // One item: a pair of tiles (or one) of a unit's rows, a key/value head, a part of the keys.
 struct Item {
-    int head, part;
+    int head, part;     // part: where partial results go (a piece of the prefix; prompts: a slot)
     int t0, t1;         // first token of the pair, end of the unit's tokens
     bool two;           // the second tile has rows
     int own0;           // own places token t sees: own0 + t - t0
@@ -250,7 +250,8 @@ __device__ __forceinline__ bool next_item(const Args& a, const Deal& d, const La
         it.own = max(0, it.own0 + min(2 * lay.per, it.t1 - it.t0) - 1);
         it.blk0 = at - p.start;
         it.blk1 = min(blocks, it.blk0 + end - cur.i);
-        it.part = (int)blockIdx.x - first / line.run;
+        const int from = first / line.run;   // the CTA whose run the item starts in
+        it.part = lay.slot(from, (int)blockIdx.x - from);
         it.whole = it.blk0 == 0 && it.blk1 == blocks;
         cur.i += it.blk1 - it.blk0;
         if (++cur.pair == line.pairs) {
@@ -295,6 +296,8 @@ __global__ void __launch_bounds__(1024) k_attn_layout(const __grid_constant__ Ar
 {
     __shared__ long long wide[32];
     __shared__ int scratch[32];
+    __shared__ int longest;   // blocks of any pair
+    if (threadIdx.x == 0) longest = 0;
     kv::pdl_wait();
     kv::pdl_release();
     const int per2 = 2 * lay.per;
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(1024) k_attn_layout(const __grid_constant__ Ar
     }
     __syncthreads();
     const int np = (a.bt.prefix_len + KB - 1) / KB;
-    int blocks = 0, total;
+    int blocks = 0, total, most = 0;
     for (int i0 = 0; i0 < pairs; i0 += (int)blockDim.x) {
         const int i = i0 + (int)threadIdx.x;
         Pair p{0, 0, 0};
@@ -342,8 +345,13 @@ __global__ void __launch_bounds__(1024) k_attn_layout(const __grid_constant__ Ar
         p.start = blocks + upto - n;
         if (i < pairs) lay.pair[i] = p;
         blocks += total;
+        most = max(most, n);
     }
-    const int run = max(lay.min_run, (a.c.heads * blocks + lay.ctas - 1) / lay.ctas);
+    atomicMax(&longest, most);
+    __syncthreads();
+    // an item of n blocks touches at most ceil((n - 1) / run) + 1 runs
+    const int run = max(max(kMinRun, (longest + kMostPieces - 2) / (kMostPieces - 1)),
+                        (a.c.heads * blocks + lay.ctas - 1) / lay.ctas);
     if (threadIdx.x == 0) {
         lay.pair[pairs] = Pair{blocks, 0, 0};
         *lay.line = Line{run, blocks, pairs};
@@ -725,7 +733,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool final = it.whole;
                 const float inv = inverse(l);
                 if (final) { w0 *= inv; w1 *= inv; }
-                const long long at = (long long)it.part * a.rows + row;
+                const long long at = (KEYS & kOwn) ? (long long)it.part * kSlotRows + (it.two ? 128 * s : 0) + r
+                                                   : (long long)it.part * a.rows + row;
                 if (in) {
                     if (final) store_lse(a, row, m, l);
                     else a.part_ml[at] = make_float2(m, l);

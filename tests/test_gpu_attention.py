@@ -193,6 +193,63 @@ def test_strided_arrays(qg):
     assert (into[:, 16 * 128:] == 0).all()
 
 
+@pytest.mark.parametrize("n_q,kv,heads_q,heads_kv,dim", [
+    ([16], [20000], 8, 1, 128), ([9, 30], [9000, 31], 9, 1, 64), ([40, 33, 70], [4000, 33, 70], 28, 4, 128),
+    ([300], [2500], 16, 2, 64), ([3], [5000], 100, 1, 128)])
+def test_prompts_in_many_pieces(qg, n_q, kv, heads_q, heads_kv, dim):
+    # few items of many keys: cut to pieces over many CTAs.  Nothing past the workspace is written.
+    c = Case(n_q, kv, 0, heads_q, heads_kv, dim, 64, BF, seed=27)
+    cache, batch = c.cache(qg), c.batch(qg)
+    need = qg.qattn_workspace_size(cache, batch, heads_q)
+    ws = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    lse = torch.empty((c.T, heads_q), dtype=torch.float32, device="cuda")
+    out = qg.qattn_forward(c.q, cache, batch, lse=lse, workspace=ws)
+    check_attention(c, out, lse)
+    assert (ws[need:] == 0x5A).all()
+
+
+def _time(f):
+    """Least time of some calls, in microseconds."""
+    for _ in range(3):
+        f()
+    times = []
+    for _ in range(10):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(4):
+            f()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b) * 250)
+    return min(times)
+
+
+def _loose(qg, n_q, kv, prefix, bound):
+    """Times of a call with its bound of own tokens far above the lengths, and at them."""
+    c = Case(n_q, kv, prefix, 64, 8, 128, 64, BF, seed=28)
+    wide = torch.zeros((len(n_q), -(-bound // 64)), dtype=torch.int32, device="cuda")
+    wide[:, :c.table.shape[1]] = c.table
+    tight, c.table = c.table, wide
+    cache, batches = c.cache(qg), [c.batch(qg, max_kv=bound)]
+    c.table = tight
+    batches.append(c.batch(qg))
+    times = []
+    for b in batches:
+        ws = torch.empty(qg.qattn_workspace_size(cache, b, 64), dtype=torch.uint8, device="cuda")
+        out = torch.empty_like(c.q)
+        times.append(_time(lambda: qg.qattn_forward(c.q, cache, b, out=out, workspace=ws)))
+        check_attention(c, out)
+    assert qg.qgemm_device_status() == 0
+    return times
+
+
+def test_prompts_are_dealt_by_their_lengths(qg):
+    # 512 tokens where 131072 might be: the blocks there are go to all CTAs (run by run of the bound they all went to one,
+    # 24 times as long)
+    loose, tight = _loose(qg, [512], [512], 0, 131072)
+    assert loose < 3 * tight, (loose, tight)
+
+
 def test_one_token_each_without_offsets(qg):
     c = Case([1] * 6, [3, 1, 20, 64, 65, 18], 260, 8, 2, 64, 16, FP, seed=13)
     out, lse = _run(qg, c, cu_q=None)

@@ -122,3 +122,17 @@ def test_workspace_size_on_the_host(qg):
     assert need() >= 2 * 4 * row and need() % 256 == 0
     assert need(tokens=2000, max_q=600, max_kv=256) >= 2 * 2000 * row
     assert need(tokens=2000, max_q=600, max_kv=256) < 8 * 2000 * row
+
+
+def test_workspace_of_long_prompts_does_not_grow_with_them(qg):
+    # only the pieces at the ends of the CTAs' runs are kept there
+    def need(tokens):
+        b, n = _batch(qg, sequences=1, tokens=tokens, max_q=tokens, max_kv=tokens, table_ld=-(-tokens // 64), prefix_len=0), ctypes.c_size_t()
+        assert qg.lib().qattn_workspace_size(ctypes.byref(_cache(qg)), ctypes.byref(b), 64, ctypes.byref(n)) == 0
+        return n.value
+
+    row = 128 * 4 + 8
+    layout = lambda tokens: 64 + 16 * (tokens // 32 + 2) + 2048   # a few words a pair of tiles
+    for tokens in (4096, 8192, 65536, 131072):
+        assert need(tokens) <= (1 << 18) * row + layout(tokens)
+    assert need(20) <= 2 * 20 * 64 * row + 16 * 256 * row + layout(20)
