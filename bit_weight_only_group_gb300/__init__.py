@@ -569,6 +569,7 @@ class KVCache:
         if k.device != v.device:
             raise ValueError("k and v must lie on one device")
         self.k, self.v, self.dtype, self.device = k, v, k.dtype, k.device
+        self.index = k.get_device()
         self.num_pages, self.page_size, self.heads_kv, self.head_dim = k.shape
         self._desc = QgKvCache(k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype], *k.shape, *k.stride()[:3])
         self._ref = ctypes.byref(self._desc)
@@ -605,9 +606,9 @@ class KVBatch:
             if table.dtype != torch.int32 or not table.is_cuda or table.dim() != 2 or table.shape[0] != B or \
                     (table.shape[1] > 1 and table.stride(1) != 1):
                 raise ValueError("table must be an int32 CUDA tensor [B, width] with unit inner stride")
-        self.device = kv_len.device
+        self.index = kv_len.get_device()
         for name, t in (("table", table), ("cu_q", cu_q), ("prefix_table", prefix_table)):
-            if t is not None and t.device != self.device:
+            if t is not None and t.get_device() != self.index:
                 raise ValueError(f"{name} must lie on the device of kv_len")
         if cu_q is None and tokens not in (None, B):
             raise ValueError("without cu_q every sequence has one new token")
@@ -628,36 +629,34 @@ class KVBatch:
     def check(self, cache: KVCache):
         """The tables hold an entry for every page the bounds reach, and lie on
         the cache's device."""
-        if self.device != cache.device:
-            raise ValueError(f"the batch lies on {self.device}, the cache on {cache.device}")
+        if self.index != cache.index:
+            raise ValueError(f"the batch lies on cuda:{self.index}, the cache on cuda:{cache.index}")
         if self._width * cache.page_size < self.max_kv:
             raise ValueError(f"table width {self._width} holds fewer than max_kv={self.max_kv} tokens")
         if self._shared * cache.page_size < self.prefix_len:
             raise ValueError(f"prefix_table of {self._shared} pages holds fewer than prefix_len={self.prefix_len} tokens")
 
 
-def _rows(t: torch.Tensor, name: str, T: int, heads: int, dim: int) -> int:
-    """Token stride of a CUDA array [T, heads, dim] whose heads are contiguous (heads 0: any number)."""
-    shape = t.shape
-    if len(shape) == 3 and t.is_cuda:
+def _rows(t: torch.Tensor, name: str, T: int, heads: int, cache: KVCache) -> int:
+    """Token stride of an array [T, heads, head_dim] on the cache's device whose heads are contiguous (heads 0: any
+    number)."""
+    shape, dim = t.shape, cache.head_dim
+    if len(shape) == 3 and t.get_device() == cache.index:
         n, h, d = shape
         if n == T and d == dim and (h == heads or not heads):
             st, sh, sd = t.stride()
             if sd == 1 and (sh == dim or h == 1):
                 return st if T > 1 else h * dim
             raise ValueError(f"the heads of a token of {name} must be contiguous")
-    raise ValueError(f"{name} must be a CUDA tensor [{T}, {heads or 'heads'}, {dim}]")
+    raise ValueError(f"{name} must be a tensor [{T}, {heads or 'heads'}, {dim}] on cuda:{cache.index}")
 
 
-def _check_devices(cache: KVCache, **tensors):
-    """The tensors lie on the cache's device, and that is the current one: the
-    library launches on the current device (with a stream argument, the
-    stream's)."""
-    for name, t in tensors.items():
-        if t is not None and t.device != cache.device:
-            raise ValueError(f"{name} lies on {t.device}, the cache on {cache.device}")
-    if torch.cuda.current_device() != cache.device.index:
-        raise ValueError(f"the cache lies on {cache.device}, the current device is cuda:{torch.cuda.current_device()}")
+def _launch_stream(cache: KVCache) -> int:
+    """The current stream.  The library launches on the current device (with a
+    stream argument, the stream's), which must be the cache's."""
+    if torch.cuda.current_device() != cache.index:
+        raise ValueError(f"the cache lies on cuda:{cache.index}, the current device is cuda:{torch.cuda.current_device()}")
+    return torch.cuda.current_stream(cache.index).cuda_stream
 
 
 @_on_stream
@@ -671,33 +670,32 @@ def qkv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor,
     rotation); positions: int32 [T] in place of the batch's own."""
     T, D, xt = batch.tokens, cache.head_dim, k.dtype
     batch.check(cache)
-    ldk, ldv = _rows(k, "k", T, cache.heads_kv, D), _rows(v, "v", T, cache.heads_kv, D)
+    ldk, ldv = _rows(k, "k", T, cache.heads_kv, cache), _rows(v, "v", T, cache.heads_kv, cache)
     if v.dtype != xt or (q is not None and q.dtype != xt) or xt not in _DTYPES:
         raise ValueError("q, k and v must share one dtype (float32, bfloat16 or float16)")
     heads_q = ldq = ldq_out = 0
     q_at = out_at = None
     if q is not None:
-        ldq = _rows(q, "q", T, 0, D)
+        ldq = _rows(q, "q", T, 0, cache)
         heads_q = q.shape[1]
         if q_out is None:
             q_out = torch.empty((T, heads_q, D), dtype=cache.dtype, device=cache.device)
             ldq_out = heads_q * D
         else:
-            ldq_out = _rows(q_out, "q_out", T, heads_q, D)
+            ldq_out = _rows(q_out, "q_out", T, heads_q, cache)
             if q_out.dtype != cache.dtype:
                 raise ValueError("q_out must have the cache's dtype")
         q_at, out_at = q.data_ptr(), q_out.data_ptr()
     turn = None
     if rope is not None:
-        if rope.dtype != torch.float32 or not rope.is_cuda or rope.dim() != 2 or not rope.is_contiguous():
-            raise ValueError("rope must be a contiguous float32 CUDA tensor [positions, R]")
-        if positions is not None and (positions.dtype != torch.int32 or not positions.is_cuda or
+        if rope.dtype != torch.float32 or rope.get_device() != cache.index or rope.dim() != 2 or not rope.is_contiguous():
+            raise ValueError(f"rope must be a contiguous float32 tensor [positions, R] on cuda:{cache.index}")
+        if positions is not None and (positions.dtype != torch.int32 or positions.get_device() != cache.index or
                                       positions.shape != (T,) or not positions.is_contiguous()):
-            raise ValueError(f"positions must be a contiguous int32 CUDA tensor [{T}]")
+            raise ValueError(f"positions must be a contiguous int32 tensor [{T}] on cuda:{cache.index}")
         turn = QgRope(rope.data_ptr(), _ptr(positions), *rope.shape, interleaved)
-    _check_devices(cache, k=k, v=v, q=q, q_out=q_out, rope=rope, positions=positions)
     st = lib().qkv_append(cache._ref, batch._ref, turn, q_at, ldq, heads_q, k.data_ptr(), ldk, v.data_ptr(), ldv,
-                          _DTYPES[xt], out_at, ldq_out, _stream(stream))
+                          _DTYPES[xt], out_at, ldq_out, _launch_stream(cache))
     if st != QG_OK:
         _check(st, "qkv_append")
     return q_out
@@ -721,27 +719,26 @@ def qattn_forward(q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: float 
     batch.check(cache)
     if q.dtype != cache.dtype:
         raise ValueError("q must have the cache's dtype")
-    ldq = _rows(q, "q", T, 0, D)
+    ldq = _rows(q, "q", T, 0, cache)
     heads_q = q.shape[1]
     if out is None:
         out = torch.empty((T, heads_q, D), dtype=out_dtype or cache.dtype, device=cache.device)
         ldo = heads_q * D
     else:
-        ldo = _rows(out, "out", T, heads_q, D)
+        ldo = _rows(out, "out", T, heads_q, cache)
     if out.dtype not in _DTYPES:
         raise ValueError("out must be float32, bfloat16 or float16")
-    if lse is not None and (lse.dtype != torch.float32 or not lse.is_cuda or lse.shape != (T, heads_q) or
+    if lse is not None and (lse.dtype != torch.float32 or lse.get_device() != cache.index or lse.shape != (T, heads_q) or
                             not lse.is_contiguous()):
-        raise ValueError(f"lse must be a contiguous float32 CUDA tensor [{T}, {heads_q}]")
+        raise ValueError(f"lse must be a contiguous float32 tensor [{T}, {heads_q}] on cuda:{cache.index}")
     if workspace is None:
         workspace = torch.empty(qattn_workspace_size(cache, batch, heads_q), dtype=torch.uint8, device=cache.device)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    _check_devices(cache, q=q, out=out, lse=lse, workspace=workspace)
+    elif workspace.get_device() != cache.index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{cache.index}")
     st = lib().qattn_forward(cache._ref, batch._ref, q.data_ptr(), ldq, heads_q, D ** -0.5 if scale is None else scale,
                              out.data_ptr(), ldo, _DTYPES[out.dtype], None if lse is None else lse.data_ptr(),
                              workspace.data_ptr() or None, workspace.numel() * workspace.element_size(),
-                             _stream(stream))
+                             _launch_stream(cache))
     if st != QG_OK:
         _check(st, "qattn_forward")
     return out

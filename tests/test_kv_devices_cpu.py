@@ -17,6 +17,9 @@ class Fake:
         self.shape, self.dtype, self.device = torch.Size(shape), dtype, torch.device(device)
         self.is_cuda, self._contiguous = self.device.type == "cuda", contiguous
 
+    def get_device(self):
+        return self.device.index if self.is_cuda else -1
+
     def dim(self):
         return len(self.shape)
 
