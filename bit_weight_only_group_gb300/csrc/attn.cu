@@ -146,16 +146,16 @@ Plan make_plan(const qg_kv_cache& c, const qg_kv_batch& b, int heads_q)
     }
     switch (p.way) {
         case kAlone:
-            split(own_units, prefix_tiles + own_tiles, 3 * sms, 4, &p.n.own_parts, &p.n.own_tiles);
+            split(own_units, prefix_tiles + own_tiles, 3 * sms, kLeastTiles, &p.n.own_parts, &p.n.own_tiles);
             break;
         case kRowsShared: {
             const int64_t units = c.heads_kv * ceil_div(rows, 64);
             split(units, prefix_tiles, sms, 2, &p.n.prefix_parts, &p.n.prefix_tiles);
-            split(own_units, own_tiles, 3 * sms, 4, &p.n.own_parts, &p.n.own_tiles);
+            split(own_units, own_tiles, 3 * sms, kLeastTiles, &p.n.own_parts, &p.n.own_tiles);
             break;
         }
         case kTilesShared:
-            split(own_units, own_tiles, 4 * sms, 4, &p.n.own_parts, &p.n.own_tiles);
+            split(own_units, own_tiles, 4 * sms, kLeastTiles, &p.n.own_parts, &p.n.own_tiles);
             p.ctas = choose_ctas(c, b, group, own_units * p.n.own_parts);
             p.deal = make_deal(c, b, group, p.ctas);
             p.n.prefix_parts = p.deal.most_pieces();

@@ -190,12 +190,14 @@ constexpr int kMostPieces = 32;  // of an item: joining takes them two at a time
 // The kernels' launches.  A keys flag says what a row sees: the shared
 // prefix, its own sequence's tokens, or both in that order.
 enum Keys { kPrefix = 1, kOwn = 2 };
-// Parts of the keys and tiles (64 keys) of one, for the row kernel; own: of the
-// own tokens, or of prefix and own tokens together.  Parts of the prefix come
-// first.
+// Parts of the keys and most tiles (64 keys) of one, for the row kernel; own: of
+// the own tokens, or of prefix and own tokens together.  Parts of the prefix
+// come first.  The tiles there are, which only the device knows, are dealt
+// evenly to the parts, at least kLeastTiles to one.
 struct Parts {
     int prefix_parts, prefix_tiles, own_parts, own_tiles;
 };
+constexpr int kLeastTiles = 4;   // fewer do not pay for a CTA's start and a part's joining
 // beside: launched right after the tile kernel of the same call, whose results it does not use, to run at its side.
 cudaError_t launch_rows(const Args& a, int dtype, const CUtensorMap& kmap, const CUtensorMap& vmap, int keys,
                         const Parts& p, bool beside, cudaStream_t s);

@@ -250,6 +250,12 @@ def test_prompts_are_dealt_by_their_lengths(qg):
     assert loose < 3 * tight, (loose, tight)
 
 
+def test_parts_are_dealt_by_the_lengths(qg):
+    # 4096 tokens where 131072 might be: cut to parts of the bound only 2 of 57 had keys, 3.6 times as long
+    loose, tight = _loose(qg, [1], [4096], 0, 131072)
+    assert loose < 2.5 * tight, (loose, tight)
+
+
 def test_one_token_each_without_offsets(qg):
     c = Case([1] * 6, [3, 1, 20, 64, 65, 18], 260, 8, 2, 64, 16, FP, seed=13)
     out, lse = _run(qg, c, cu_q=None)
