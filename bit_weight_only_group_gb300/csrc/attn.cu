@@ -86,17 +86,24 @@ double block_time(const qg_kv_cache& c, int64_t tiles)
 // sequences over 8192 + 1024 keys best at 64 (134 us, 158 on all SMs), 64 over
 // 32768 + 2048 at 96 to 112 (103, 120), 128 over 131072 + 2048 at 136 (429,
 // 446), 32 over 2011 + 700 with a key/value head per query head at 32 (48, 56).
+//
+// Lengths far below max_kv leave the SMs kept for the own tokens idle early, so
+// the prefix gets no fewer CTAs than make it take kSlowest times as long as all
+// of them would.
+constexpr double kSlowest = 2.25;
 int choose_ctas(const qg_kv_cache& c, const qg_kv_batch& b, int64_t group, int64_t own_ctas)
 {
     const double sms = num_sms();
     const double own = own_time(c, b, group) + 0.006 * own_ctas;
     int best = num_sms();
-    double least = 1e30;
+    double least = 1e30, on_all = 0.0;
     for (int x = num_sms(); x >= 8; x -= 4) {
         const Deal d = make_deal(c, b, group, x);
         const double line = (double)d.heads * d.blocks, rounds = (double)ceil_div(d.slots(), x);
         const double each = rounds * std::max(d.pairs ? block_time(c, 2) * line / d.groups : 0.0,
                                               d.single ? block_time(c, 1) * line / d.sgroups : 0.0);
+        if (x == num_sms()) on_all = 10.0 + each;
+        if (10.0 + each > kSlowest * on_all) continue;
         const double busy = std::min(x, d.slots());
         const double tile_end = (10.0 + each) * (1.0 + 0.7 * (sms - busy) / sms);
         const double all_end = own + (10.0 + each) * busy / sms;

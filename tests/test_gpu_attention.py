@@ -256,6 +256,12 @@ def test_parts_are_dealt_by_the_lengths(qg):
     assert loose < 2.5 * tight, (loose, tight)
 
 
+def test_a_loose_bound_leaves_the_prefix_its_share_of_the_card(qg):
+    # 40 own histories of 300 where 32768 might be, over 20000: SMs kept for own tokens that are not there stay idle
+    loose, tight = _loose(qg, [1] * 40, [300] * 40, 20000, 32768)
+    assert loose < 3 * tight, (loose, tight)
+
+
 def test_one_token_each_without_offsets(qg):
     c = Case([1] * 6, [3, 1, 20, 64, 65, 18], 260, 8, 2, 64, 16, FP, seed=13)
     out, lse = _run(qg, c, cu_q=None)
