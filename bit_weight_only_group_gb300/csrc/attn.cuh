@@ -193,11 +193,14 @@ enum Keys { kPrefix = 1, kOwn = 2 };
 // Parts of the keys and most tiles (64 keys) of one, for the row kernel; own: of
 // the own tokens, or of prefix and own tokens together.  Parts of the prefix
 // come first.  The tiles there are, which only the device knows, are dealt
-// evenly to the parts, at least kLeastTiles to one.
+// evenly to the parts, at least kLeastTiles to one; beside the tile kernel at
+// least kLeastBeside, since there the SMs' time counts, and a CTA's start and
+// end take some of it (64 sequences over 32768 + 32 to 2048 own tokens 100 us,
+// 105 with kLeastTiles; 48 of 5 drafted tokens 38, 40.5).
 struct Parts {
     int prefix_parts, prefix_tiles, own_parts, own_tiles;
 };
-constexpr int kLeastTiles = 4;   // fewer do not pay for a CTA's start and a part's joining
+constexpr int kLeastTiles = 4, kLeastBeside = 16;
 // beside: launched right after the tile kernel of the same call, whose results it does not use, to run at its side.
 cudaError_t launch_rows(const Args& a, int dtype, const CUtensorMap& kmap, const CUtensorMap& vmap, int keys,
                         const Parts& p, bool beside, cudaStream_t s);

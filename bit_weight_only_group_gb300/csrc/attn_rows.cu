@@ -76,7 +76,7 @@ struct Item {
 };
 
 template <int KEYS>
-__device__ __forceinline__ Item find_item(const Args& a, int unit, int row_block, int part, int parts, int most_tiles,
+__device__ __forceinline__ Item find_item(const Args& a, int unit, int row_block, int part, int parts, int least_tiles,
                                           int rows_cap, bool tell)
 {
     Item it;
@@ -103,8 +103,7 @@ __device__ __forceinline__ Item find_item(const Args& a, int unit, int row_block
     it.prefix = (KEYS & kPrefix) ? a.bt.prefix_len : 0;
     it.np = (it.prefix + KT - 1) / KT;
     const int tiles = it.rows > 0 ? it.np + (it.own + KT - 1) / KT : 0;
-    // not more than most_tiles, which as many parts were counted for
-    const int per = max(min(kLeastTiles, most_tiles), (tiles + parts - 1) / parts);
+    const int per = max(least_tiles, (tiles + parts - 1) / parts);
     it.tile0 = min(part * per, tiles);
     it.tile1 = min(it.tile0 + per, tiles);
     return it;
@@ -112,7 +111,7 @@ __device__ __forceinline__ Item find_item(const Args& a, int unit, int row_block
 
 // The CTA numbered x of a launch's (unit, row block, part, head) CTAs.
 struct Split {
-    int part0, parts, most_tiles, row_blocks;
+    int part0, parts, least_tiles, row_blocks;
 };
 
 template <typename T, int D, int RW, int KEYS>
@@ -146,7 +145,7 @@ __device__ __forceinline__ void work(const CUtensorMap& kmap, const CUtensorMap&
     if (!beside) kv::pdl_wait();
     kv::pdl_release();
     if (beside && blockIdx.x == gridDim.x - 1) kv::pdl_wait();
-    const Item it = find_item<KEYS>(a, unit, row_block, part, sp.parts, sp.most_tiles, 16 * RW, threadIdx.x == 0);
+    const Item it = find_item<KEYS>(a, unit, row_block, part, sp.parts, sp.least_tiles, 16 * RW, threadIdx.x == 0);
     if (it.rows == 0) return;
     bool ok = true;
     // keys of tile j that any row sees
@@ -425,11 +424,12 @@ struct Launch {
     Split sp;
     int64_t ctas;
 };
-Launch plan(const Args& a, int keys, int rw, int part0, int parts, int most_tiles)
+Launch plan(const Args& a, int keys, int rw, int part0, int parts, int most_tiles, bool beside = false)
 {
     const int64_t units = (keys & kOwn) ? a.bt.B : 1;
     const int64_t blocks = ceil_div((int64_t)a.group * ((keys & kOwn) ? a.bt.max_q : a.bt.T), 16 * rw);
-    return Launch{Split{part0, parts, most_tiles, (int)blocks}, units * blocks * parts * a.c.heads};
+    const int least = std::min(beside ? kLeastBeside : kLeastTiles, most_tiles);
+    return Launch{Split{part0, parts, least, (int)blocks}, units * blocks * parts * a.c.heads};
 }
 
 // No more stages than tiles: more of the shared memory stays with the kernel beside.
@@ -444,7 +444,7 @@ cudaError_t launch_one(const Args& a, const CUtensorMap& kmap, const CUtensorMap
     static std::atomic<unsigned long long> done{0};
     const cudaError_t e = kv::allow_smem(kernel, smem_for<D>(Cfg<D>::MAX_STAGES), done);
     if (e != cudaSuccess) return e;
-    const Launch l = plan(a, KEYS, RW, part0, parts, most_tiles);
+    const Launch l = plan(a, KEYS, RW, part0, parts, most_tiles, beside);
     if (l.ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     const int stages = stages_for<D>(most_tiles);
     return kv::launch_dependent(kernel, dim3((unsigned)l.ctas), kThreads, smem_for<D>(stages), s, kmap, vmap, a, l.sp,
