@@ -93,16 +93,17 @@ double block_time(const qg_kv_cache& c, int64_t tiles)
 constexpr double kSlowest = 2.25;
 int choose_ctas(const qg_kv_cache& c, const qg_kv_batch& b, int64_t group, int64_t own_ctas)
 {
-    const double sms = num_sms();
+    const int all = num_sms();
+    const double sms = all;
     const double own = own_time(c, b, group) + 0.006 * own_ctas;
-    int best = num_sms();
+    int best = all;
     double least = 1e30, on_all = 0.0;
-    for (int x = num_sms(); x >= 8; x -= 4) {
+    for (int x = all; x >= 8; x -= 4) {
         const Deal d = make_deal(c, b, group, x);
         const double line = (double)d.heads * d.blocks, rounds = (double)ceil_div(d.slots(), x);
         const double each = rounds * std::max(d.pairs ? block_time(c, 2) * line / d.groups : 0.0,
                                               d.single ? block_time(c, 1) * line / d.sgroups : 0.0);
-        if (x == num_sms()) on_all = 10.0 + each;
+        if (x == all) on_all = 10.0 + each;
         if (10.0 + each > kSlowest * on_all) continue;
         const double busy = std::min(x, d.slots());
         const double tile_end = (10.0 + each) * (1.0 + 0.7 * (sms - busy) / sms);

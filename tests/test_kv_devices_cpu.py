@@ -49,7 +49,7 @@ def qg(monkeypatch):
                                 qattn_forward=lambda *a: calls.append("attention") or 0)
     monkeypatch.setattr(qg, "lib", lambda: lib)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: types.SimpleNamespace(cuda_stream=0))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0)
     monkeypatch.setattr(qg, "calls", calls, raising=False)
     return qg
 
