@@ -6,7 +6,9 @@
 // key/value head.  Keys come in blocks of 128.  For a tile and a block
 //     S = Q K^T     tcgen05, Q and K from shared memory, S in tensor memory
 //     P = 2^(S scale_log2 - m)   one thread a row: S read from tensor memory,
-//                   P written back over it in the cache's type
+//                   P written back over it in the cache's type (16-bit operands
+//                   of the next product; the sum l is of P before that rounding,
+//                   whose error attn_rows.cu gives)
 //     O += P V      tcgen05, P from tensor memory, V from shared memory
 //                   (its head dimension contiguous), O in tensor memory
 // The tensor core waits for the softmax of a block and the softmax for its S,
@@ -30,6 +32,9 @@
 // dropped: steps of 64 keys with two S buffers a stream, which need not wait
 // for S (470 us: products of N = 64 read Q twice as often); two threads a row
 // (5 % slower); waits that poll without being suspended (6 % slower).
+//
+// Registers: 168 a thread at launch; the prompts' form spills 32 bytes, the
+// shared prefix's none.
 //
 // Warps: 0-3 softmax of stream 0, 4-7 of stream 1 (a warp may reach only the
 // 32 lanes of tensor memory its index modulo 4 names), 8 loads (one lane per

@@ -15,7 +15,11 @@
 // pairs.  8192 tokens of 64 + 2 x 8 heads of 128 (bf16, 340 MB): 58.7 us, 5.8 TB/s;
 // a plain copy of as much takes 55.5.  With a CTA a token and its place found
 // by itself 66 us (1.5 us of dependent loads a token, whatever was in flight).
-// One token 3.7 us, 256 tokens 4.5 us, one launch after another in a graph.
+// One token 4.0 us, 256 tokens 4.8 us, one launch after another in a graph.
+// fp32 values into an fp16 cache are further from the bytes' time: 778 tokens of
+// 32 + 2 x 32 heads (58 MB) 17.9 us, 3.2 TB/s.  A CTA has about five units there
+// (two a token), too few to hide the launch's start and end (the 4.0 us of one
+// token) and the first places; what the rest waits for has not been measured.
 #include "kv_batch.cuh"
 #include "ptx.cuh"
 

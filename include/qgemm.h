@@ -516,6 +516,11 @@ typedef struct {
  * followed.  Both set the device status word to QG_ERR_DEVICE_STATUS (see
  * qgemm_device_status), and the outputs of the sequences concerned are then
  * not valid.
+ *
+ * The bounds decide how an attention call is split, the lengths what each part
+ * does, so bounds above the lengths may cost time: measured, 1 token over 4096
+ * own tokens where 131072 might be 19 us instead of 11, 64 sequences over
+ * 32768 + 2048 where 65536 might be 149 instead of 129.
  */
 typedef struct {
     int32_t sequences, tokens, max_q, max_kv, table_ld, prefix_len;
@@ -580,14 +585,18 @@ QG_API qg_status qkv_append(const qg_kv_cache* cache, const qg_kv_batch* batch, 
  *            16-byte aligned, ldo a multiple of 16 bytes.
  *   lse      fp32 [T, heads_q] or NULL: ln sum_j exp(scale * q . k_j).
  *   ws       qattn_workspace_size bytes, 256-byte aligned; contents need not
- *            be kept or cleared between calls.
+ *            be kept or cleared between calls.  The size follows from the
+ *            bounds and the current device's SMs; for prompts it stays below
+ *            about 140 MB, however long they are.
  * A token that sees nothing (kv_len below n_b, no prefix) gets out = 0 and
  * lse = -inf.  What lies past kv_len or prefix_len in a page is never used,
  * whatever it holds.  A value in reach that is not finite stays in its
  * sequence (and its key/value head), where also new tokens before its own may
  * become NaN.  Logits, the softmax's maximum and sum, and the sums over v are
- * held in fp32; p is rounded to the cache's type for the product with v.  The result does not
- * depend on the order in which blocks run (repeatable bit for bit).
+ * held in fp32; p is rounded to the cache's type for the product with v, also
+ * where ot is QG_T_F32 (measured with fp32 output: off by 5.4e-5 rms of 0.047
+ * rms in bf16, 0.75e-5 of 0.039 in fp16).  The result does not depend on the
+ * order in which blocks run (repeatable bit for bit).
  * Errors: QG_ERR_INVALID_ARG, QG_ERR_UNSUPPORTED, QG_ERR_ALIGNMENT,
  * QG_ERR_WORKSPACE, QG_ERR_CUDA.
  */
