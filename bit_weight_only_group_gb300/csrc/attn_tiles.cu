@@ -352,7 +352,8 @@ __global__ void __launch_bounds__(1024) k_attn_layout(const __grid_constant__ Ar
         blocks += total;
         most = max(most, n);
     }
-    atomicMax(&longest, most);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if ((threadIdx.x & 31) == 0) atomicMax(&longest, most);
     __syncthreads();
     // an item of n blocks touches at most ceil((n - 1) / run) + 1 runs
     const int run = max(max(kMinRun, (longest + kMostPieces - 2) / (kMostPieces - 1)),
