@@ -444,14 +444,18 @@ def qgemm_moe_grouped_multi(x: torch.Tensor, topk_ids: torch.Tensor, experts_per
 
 
 def qgemm_set_dependent_launch(enable: bool) -> None:
-    """Programmatic dependent launch of the dense products (decode and tensor-core kernels), process-wide."""
+    """Programmatic dependent launch of the dense products (decode and tensor-core kernels) and of the paged-cache
+    kernels, process-wide."""
     lib().qgemm_set_dependent_launch.argtypes = [ctypes.c_int32]
     _check(lib().qgemm_set_dependent_launch(1 if enable else 0), "qgemm_set_dependent_launch")
 
 
 def qgemm_device_status(reset: bool = False) -> int:
-    """Status word of the decode kernels on the current device (0 = QG_OK,
-    QG_ERR_TIMEOUT after a bounded wait gave up).  Synchronizes the device."""
+    """Status word of the library's kernels on the current device: 0 (QG_OK),
+    QG_ERR_TIMEOUT (-6) after a bounded wait gave up, QG_ERR_DEVICE_STATUS (-7)
+    after a length, offset, page or position outside its bounds,
+    QG_ERR_WORKSPACE (-4) after a fallback list over capacity.  Synchronizes the
+    device."""
     v = ctypes.c_int32(0)
     _check(lib().qgemm_device_status(ctypes.byref(v), 1 if reset else 0), "qgemm_device_status")
     return v.value
