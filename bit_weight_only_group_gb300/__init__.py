@@ -14,8 +14,10 @@ Entry points (same names as the C ABI):
 * ``qgemm_moe_grouped(x, topk_ids, experts)`` -> y [T, k, N]
 * ``qgemm_moe_grouped_multi(x, topk_ids, [experts_0, experts_1])`` -> [y_0, y_1]
   (products sharing one routing, e.g. an MoE layer's gate and up)
-* ``qkv_append(cache, batch, k, v, q=, rope=)`` -> q turned; k (turned) and v
-  written to the pages of a :class:`KVCache`
+* ``qkv_append(cache, batch, k, v, q=, rope=, q_norm=, k_norm=)`` -> q (normed
+  and) turned; k (normed and turned) and v written to the pages of a
+  :class:`KVCache`, or quantised to those of a :class:`KVCache8` (8 bits)
+* ``qkv_read(cache, batch)`` -> k, v: the values an 8-bit cache holds
 * ``qattn_forward(q, cache, batch)`` -> attention over a shared prefix and each
   sequence's own cached tokens (:class:`KVBatch`)
 
@@ -52,7 +54,8 @@ ABI_FUNCTIONS = ("qpack_query_sizes", "qpack_workspace_size", "qpack_quantize", 
                  "qgemm_device_status", "qgemm_selftest_bounded_wait", "qdiag_workspace_size", "qdiag_layer",
                  "qgemm_w8a8_workspace_size", "qgemm_forward_w8a8",
                  "qrepack_tiles_size", "qrepack_tiles", "qgemm_tiles_workspace_size", "qgemm_forward_tiles",
-                 "qgemm_set_dependent_launch", "qkv_append", "qattn_workspace_size", "qattn_forward",
+                 "qgemm_set_dependent_launch", "qkv_append", "qkv_append_norm", "qkv8_append", "qkv8_read",
+                 "qattn_workspace_size", "qattn_forward", "qattn8_workspace_size", "qattn8_forward",
                  "qgemm_last_error")
 
 
@@ -81,6 +84,15 @@ class QgKvCache(ctypes.Structure):
                 ("head_stride", ctypes.c_int64)]
 
 
+class QgKv8Cache(ctypes.Structure):
+    """Mirror of ``qg_kv8_cache`` in include/qgemm.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("heads_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("scale_page_stride", ctypes.c_int64),
+                ("scale_block_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64)]
+
+
 class QgKvBatch(ctypes.Structure):
     """Mirror of ``qg_kv_batch`` in include/qgemm.h."""
     _fields_ = [("sequences", ctypes.c_int32), ("tokens", ctypes.c_int32), ("max_q", ctypes.c_int32),
@@ -93,6 +105,11 @@ class QgRope(ctypes.Structure):
     """Mirror of ``qg_rope`` in include/qgemm.h."""
     _fields_ = [("table", ctypes.c_void_p), ("at", ctypes.c_void_p), ("positions", ctypes.c_int32),
                 ("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+class QgHeadNorm(ctypes.Structure):
+    """Mirror of ``qg_head_norm`` in include/qgemm.h."""
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 _lib = None
@@ -133,8 +150,16 @@ def lib() -> ctypes.CDLL:
         i64, pc, pb = ctypes.c_int64, ctypes.POINTER(QgKvCache), ctypes.POINTER(QgKvBatch)
         L.qkv_append.argtypes = [pc, pb, ctypes.POINTER(QgRope), vp, i64, i32, vp, i64, vp, i64, ctypes.c_int, vp, i64,
                                  vp]
+        pc8, pn = ctypes.POINTER(QgKv8Cache), ctypes.POINTER(QgHeadNorm)
+        L.qkv_append_norm.argtypes = [pc, pb, pn, ctypes.POINTER(QgRope), vp, i64, i32, vp, i64, vp, i64, ctypes.c_int, vp,
+                                      i64, vp]
+        L.qkv8_append.argtypes = [pc8, pb, pn, ctypes.POINTER(QgRope), vp, i64, i32, vp, i64, vp, i64, ctypes.c_int, vp,
+                                  i64, ctypes.c_int, vp]
+        L.qkv8_read.argtypes = [pc8, pb, vp, i64, vp, i64, ctypes.c_int, vp]
         L.qattn_workspace_size.argtypes = [pc, pb, i32, psz]
         L.qattn_forward.argtypes = [pc, pb, vp, i64, i32, f32, vp, i64, ctypes.c_int, vp, vp, sz, vp]
+        L.qattn8_workspace_size.argtypes = [pc8, pb, i32, psz]
+        L.qattn8_forward.argtypes = [pc8, pb, vp, i64, i32, ctypes.c_int, f32, vp, i64, ctypes.c_int, vp, vp, sz, vp]
         for name in ABI_FUNCTIONS[:-1]:
             getattr(L, name).restype = ctypes.c_int
         L.qgemm_last_error.argtypes = []
@@ -587,6 +612,47 @@ class KVCache:
         return KVCache(k, v)
 
 
+KV8_BLOCK = 16   # places of a page that share a scale
+
+
+class KVCache8:
+    """Pages of keys and values in 8 bits: codes k and v [num_pages, page_size,
+    heads_kv, head_dim] (torch.float8_e4m3fn, CUDA) with one set of strides, in
+    any order with the head's codes contiguous, and for each block of 16 places
+    and head the byte of a power of two, k_scale and v_scale [num_pages,
+    page_size / 16, heads_kv] (uint8) with one set of strides in any order.  A
+    value is code * 2^(byte - 127)."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+            raise ValueError("k and v must be 4-D with the same shape, strides and dtype")
+        if k.dtype != torch.float8_e4m3fn or not k.is_cuda or k.stride(3) != 1:
+            raise ValueError("k and v must be float8_e4m3fn CUDA tensors with unit inner stride")
+        blocks = (k.shape[0], k.shape[1] // KV8_BLOCK, k.shape[2])
+        if tuple(k_scale.shape) != blocks or tuple(v_scale.shape) != blocks or k_scale.stride() != v_scale.stride():
+            raise ValueError(f"k_scale and v_scale must be {list(blocks)} with the same strides")
+        if k_scale.dtype != torch.uint8 or v_scale.dtype != torch.uint8:
+            raise ValueError("k_scale and v_scale must be uint8")
+        self.index = k.get_device()
+        if any(t.get_device() != self.index for t in (v, k_scale, v_scale)):
+            raise ValueError("k, v, k_scale and v_scale must lie on one device")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.dtype, self.device = k.dtype, k.device
+        self.num_pages, self.page_size, self.heads_kv, self.head_dim = k.shape
+        self._desc = QgKv8Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *k.shape,
+                                *k.stride()[:3], *k_scale.stride())
+        self._ref = ctypes.byref(self._desc)
+
+    @staticmethod
+    def empty(num_pages: int, page_size: int, heads_kv: int, head_dim: int, device="cuda") -> "KVCache8":
+        """Pages with heads first: a head's rows of a page are one contiguous run, and so are its scales."""
+        k, v = (torch.empty((num_pages, heads_kv, page_size, head_dim), dtype=torch.float8_e4m3fn,
+                            device=device).transpose(1, 2) for _ in range(2))
+        ks, vs = (torch.empty((num_pages, heads_kv, page_size // KV8_BLOCK), dtype=torch.uint8,
+                              device=device).transpose(1, 2) for _ in range(2))
+        return KVCache8(k, v, ks, vs)
+
+
 class KVBatch:
     """Sequences over one cache (``qg_kv_batch``): own pages table [B, width]
     and own lengths kv_len [B] (new tokens counted), new tokens per sequence
@@ -664,33 +730,61 @@ def _launch_stream(cache: KVCache) -> int:
     return torch._C._cuda_getCurrentRawStream(cache.index)
 
 
+def _norm(q_norm, k_norm, eps: float, cache):
+    """The norms' weights [head_dim], as the library takes them (None: nothing is normed)."""
+    some = q_norm if q_norm is not None else k_norm
+    if some is None:
+        return None
+    for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+        if w is not None and (w.dtype != some.dtype or w.dtype not in _DTYPES or w.get_device() != cache.index or
+                              w.shape != (cache.head_dim,) or not w.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous tensor [{cache.head_dim}] on cuda:{cache.index}, both norms of one "
+                             "dtype (float32, bfloat16 or float16)")
+    return QgHeadNorm(None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(),
+                      _DTYPES[some.dtype], eps)
+
+
 @_on_stream
-def qkv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, q: torch.Tensor | None = None,
+def qkv_append(cache: "KVCache | KVCache8", batch: KVBatch, k: torch.Tensor, v: torch.Tensor, q: torch.Tensor | None = None,
                rope: torch.Tensor | None = None, positions: torch.Tensor | None = None, interleaved: bool = False,
-               q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+               q_out: torch.Tensor | None = None, stream=None, q_norm: torch.Tensor | None = None,
+               k_norm: torch.Tensor | None = None, eps: float = 1e-6, q_dtype: torch.dtype | None = None) -> torch.Tensor | None:
     """Write the batch's new tokens k and v [T, heads_kv, head_dim] (fp32,
     bf16 or fp16) to their pages, k turned by its position; returns q [T,
     heads_q, head_dim] turned, in the cache's type.  rope: fp32 [positions,
     R], row p the R/2 cosines and then the R/2 sines of position p (None: no
-    rotation); positions: int32 [T] in place of the batch's own."""
-    T, D, xt = batch.tokens, cache.head_dim, k.dtype
+    rotation); positions: int32 [T] in place of the batch's own.
+
+    q_norm, k_norm: weights [head_dim] (fp32, bf16 or fp16) of norms applied to
+    each head of q and k before the rotation, x * w / sqrt(mean(x^2) + eps).
+
+    With a :class:`KVCache8`, k and v are quantised to its codes and scales, and
+    q is returned in q_dtype (default: q's own type, bf16 for fp32)."""
+    T, D, xt, eight = batch.tokens, cache.head_dim, k.dtype, isinstance(cache, KVCache8)
     batch.check(cache)
     ldk, ldv = _rows(k, "k", T, cache.heads_kv, cache), _rows(v, "v", T, cache.heads_kv, cache)
     if v.dtype != xt or (q is not None and q.dtype != xt) or xt not in _DTYPES:
         raise ValueError("q, k and v must share one dtype (float32, bfloat16 or float16)")
+    if q_dtype is None:
+        q_dtype = cache.dtype if not eight else q_out.dtype if q_out is not None else \
+            torch.bfloat16 if xt == torch.float32 else xt
+    if q_dtype not in (torch.bfloat16, torch.float16) or (not eight and q_dtype != cache.dtype):
+        raise ValueError("q is written in the cache's dtype" if not eight else "q is written in bfloat16 or float16")
     heads_q = ldq = ldq_out = 0
     q_at = out_at = None
     if q is not None:
         ldq = _rows(q, "q", T, 0, cache)
         heads_q = q.shape[1]
         if q_out is None:
-            q_out = torch.empty((T, heads_q, D), dtype=cache.dtype, device=cache.device)
+            q_out = torch.empty((T, heads_q, D), dtype=q_dtype, device=cache.device)
             ldq_out = heads_q * D
         else:
             ldq_out = _rows(q_out, "q_out", T, heads_q, cache)
-            if q_out.dtype != cache.dtype:
-                raise ValueError("q_out must have the cache's dtype")
+            if q_out.dtype != q_dtype:
+                raise ValueError("q_out must have the cache's dtype" if not eight else "q_out must have q_dtype")
         q_at, out_at = q.data_ptr(), q_out.data_ptr()
+    elif q_norm is not None:
+        raise ValueError("q_norm without q")
     turn = None
     if rope is not None:
         if rope.dtype != torch.float32 or rope.get_device() != cache.index or rope.dim() != 2 or not rope.is_contiguous():
@@ -699,35 +793,72 @@ def qkv_append(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor,
                                       positions.shape != (T,) or not positions.is_contiguous()):
             raise ValueError(f"positions must be a contiguous int32 tensor [{T}] on cuda:{cache.index}")
         turn = QgRope(rope.data_ptr(), _ptr(positions), *rope.shape, interleaved)
-    st = lib().qkv_append(cache._ref, batch._ref, turn, q_at, ldq, heads_q, k.data_ptr(), ldk, v.data_ptr(), ldv,
-                          _DTYPES[xt], out_at, ldq_out, _launch_stream(cache))
+    norm = _norm(q_norm, k_norm, eps, cache)
+    rows = (q_at, ldq, heads_q, k.data_ptr(), ldk, v.data_ptr(), ldv, _DTYPES[xt], out_at, ldq_out)
+    stream = _launch_stream(cache)
+    if eight:
+        st = lib().qkv8_append(cache._ref, batch._ref, norm, turn, *rows, _DTYPES[q_dtype], stream)
+    elif norm is not None:
+        st = lib().qkv_append_norm(cache._ref, batch._ref, norm, turn, *rows, stream)
+    else:
+        st = lib().qkv_append(cache._ref, batch._ref, turn, *rows, stream)
     if st != QG_OK:
-        _check(st, "qkv_append")
+        _check(st, "qkv8_append" if eight else "qkv_append" if norm is None else "qkv_append_norm")
     return q_out
 
 
-def qattn_workspace_size(cache: KVCache, batch: KVBatch, heads_q: int) -> int:
+@_on_stream
+def qkv_read(cache: KVCache8, batch: KVBatch, k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None,
+             dtype: torch.dtype | None = None, stream=None) -> tuple:
+    """k, v [T, heads_kv, head_dim] (dtype: bf16 by default, fp16 or fp32): the
+    values that an 8-bit cache holds for the batch's tokens, the rows that
+    qkv_append would write (with cu_q the sums of kv_len, whole sequences)."""
+    T, H, D = batch.tokens, cache.heads_kv, cache.head_dim
+    batch.check(cache)
+    if not isinstance(cache, KVCache8):
+        raise ValueError("qkv_read reads a KVCache8")
+    if dtype is None:
+        dtype = k_out.dtype if k_out is not None else v_out.dtype if v_out is not None else torch.bfloat16
+    if k_out is None:
+        k_out = torch.empty((T, H, D), dtype=dtype, device=cache.device)
+    if v_out is None:
+        v_out = torch.empty((T, H, D), dtype=dtype, device=cache.device)
+    if k_out.dtype != dtype or v_out.dtype != dtype or dtype not in _DTYPES:
+        raise ValueError("k_out and v_out must share one dtype (float32, bfloat16 or float16)")
+    ldk, ldv = _rows(k_out, "k_out", T, H, cache), _rows(v_out, "v_out", T, H, cache)
+    st = lib().qkv8_read(cache._ref, batch._ref, k_out.data_ptr(), ldk, v_out.data_ptr(), ldv, _DTYPES[dtype],
+                         _launch_stream(cache))
+    if st != QG_OK:
+        _check(st, "qkv8_read")
+    return k_out, v_out
+
+
+def qattn_workspace_size(cache: "KVCache | KVCache8", batch: KVBatch, heads_q: int) -> int:
     b = ctypes.c_size_t()
-    _check(lib().qattn_workspace_size(cache._ref, batch._ref, heads_q, ctypes.byref(b)), "qattn_workspace_size")
+    name = "qattn8_workspace_size" if isinstance(cache, KVCache8) else "qattn_workspace_size"
+    _check(getattr(lib(), name)(cache._ref, batch._ref, heads_q, ctypes.byref(b)), name)
     return b.value
 
 
 @_on_stream
-def qattn_forward(q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: float | None = None,
+def qattn_forward(q: torch.Tensor, cache: "KVCache | KVCache8", batch: KVBatch, scale: float | None = None,
                   out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
                   lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """out [T, heads_q, head_dim] (default: of q's type): attention of the new
-    tokens q (of the cache's type) over the shared prefix and their own cached
-    tokens.  scale: 1 / sqrt(head_dim) by default; lse: fp32 [T, heads_q] to
-    receive the log of each row's sum of exponentials."""
-    T, D = batch.tokens, cache.head_dim
+    tokens q (of the cache's type; bf16 or fp16 with a :class:`KVCache8`) over
+    the shared prefix and their own cached tokens.  scale: 1 / sqrt(head_dim) by
+    default; lse: fp32 [T, heads_q] to receive the log of each row's sum of
+    exponentials."""
+    T, D, eight = batch.tokens, cache.head_dim, isinstance(cache, KVCache8)
     batch.check(cache)
-    if q.dtype != cache.dtype:
+    if eight and q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("q must be bfloat16 or float16")
+    if not eight and q.dtype != cache.dtype:
         raise ValueError("q must have the cache's dtype")
     ldq = _rows(q, "q", T, 0, cache)
     heads_q = q.shape[1]
     if out is None:
-        out = torch.empty((T, heads_q, D), dtype=out_dtype or cache.dtype, device=cache.device)
+        out = torch.empty((T, heads_q, D), dtype=out_dtype or q.dtype, device=cache.device)
         ldo = heads_q * D
     else:
         ldo = _rows(out, "out", T, heads_q, cache)
@@ -740,10 +871,13 @@ def qattn_forward(q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: float 
         workspace = torch.empty(qattn_workspace_size(cache, batch, heads_q), dtype=torch.uint8, device=cache.device)
     elif workspace.get_device() != cache.index or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{cache.index}")
-    st = lib().qattn_forward(cache._ref, batch._ref, q.data_ptr(), ldq, heads_q, D ** -0.5 if scale is None else scale,
-                             out.data_ptr(), ldo, _DTYPES[out.dtype], None if lse is None else lse.data_ptr(),
-                             workspace.data_ptr() or None, workspace.numel() * workspace.element_size(),
-                             _launch_stream(cache))
+    rest = (D ** -0.5 if scale is None else scale, out.data_ptr(), ldo, _DTYPES[out.dtype],
+            None if lse is None else lse.data_ptr(), workspace.data_ptr() or None,
+            workspace.numel() * workspace.element_size(), _launch_stream(cache))
+    if eight:
+        st = lib().qattn8_forward(cache._ref, batch._ref, q.data_ptr(), ldq, heads_q, _DTYPES[q.dtype], *rest)
+    else:
+        st = lib().qattn_forward(cache._ref, batch._ref, q.data_ptr(), ldq, heads_q, *rest)
     if st != QG_OK:
-        _check(st, "qattn_forward")
+        _check(st, "qattn8_forward" if eight else "qattn_forward")
     return out

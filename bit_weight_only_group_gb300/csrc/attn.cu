@@ -14,6 +14,13 @@ namespace {
 constexpr int kTile = 64;     // keys of a tile of the row kernel
 constexpr int kBlock = 128;   // keys of a block of the tile kernel
 
+// What the split of a call goes by in a cache.
+struct Shape {
+    int heads_kv, head_dim;
+    int bytes;      // of a value
+    bool tiles;     // there is a tile kernel for it
+};
+
 // How a call is run.
 enum Way {
     kAlone,         // row kernel: each sequence over prefix and own tokens
@@ -43,7 +50,7 @@ void split(int64_t units, int64_t tiles, int64_t ctas, int least, int* parts, in
 }
 
 // The shared prefix dealt to `ctas` CTAs, none with less than two blocks.
-Deal make_deal(const qg_kv_cache& c, const qg_kv_batch& b, int64_t group, int ctas)
+Deal make_deal(const Shape& c, const qg_kv_batch& b, int64_t group, int ctas)
 {
     Deal d{};
     d.per = tile_tokens(group);
@@ -62,10 +69,10 @@ Deal make_deal(const qg_kv_cache& c, const qg_kv_batch& b, int64_t group, int ct
 // Microseconds the row kernel takes on the whole card for the own tokens,
 // which fill half of max_kv, say: 6.4 TB/s, or, with more than 16 rows a
 // sequence and head, 0.7 an SM for each 32 rows and 64 keys.
-double own_time(const qg_kv_cache& c, const qg_kv_batch& b, int64_t group)
+double own_time(const Shape& c, const qg_kv_batch& b, int64_t group)
 {
     const double pairs = 0.5 * b.sequences * c.heads_kv, rows = (double)group * b.max_q;
-    const double bytes = pairs * b.max_kv * c.head_dim * 4 / 6.4e6;
+    const double bytes = pairs * b.max_kv * c.head_dim * (2 * c.bytes) / 6.4e6;
     const double products = rows > 16 ? pairs * ceil_div((int64_t)rows, 32) * ceil_div(b.max_kv, kTile) * 0.7 / num_sms() : 0.0;
     return 5.0 + std::max(bytes, products);
 }
@@ -73,7 +80,7 @@ double own_time(const qg_kv_cache& c, const qg_kv_batch& b, int64_t group)
 // Microseconds the tile kernel takes on an SM for a block and so many tiles:
 // 1.35 for a pair, 1.2 for a single tile (bound by its loads), two thirds of
 // that with 64-wide heads.
-double block_time(const qg_kv_cache& c, int64_t tiles)
+double block_time(const Shape& c, int64_t tiles)
 {
     return (c.head_dim == 128 ? 1.0 : 0.67) * ((double)(tiles / 2) * 1.35 + (double)(tiles % 2) * 1.2);
 }
@@ -91,7 +98,7 @@ double block_time(const qg_kv_cache& c, int64_t tiles)
 // the prefix gets no fewer CTAs than make it take kSlowest times as long as all
 // of them would.
 constexpr double kSlowest = 2.25;
-int choose_ctas(const qg_kv_cache& c, const qg_kv_batch& b, int64_t group, int64_t own_ctas)
+int choose_ctas(const Shape& c, const qg_kv_batch& b, int64_t group, int64_t own_ctas)
 {
     const int all = num_sms();
     const double sms = all;
@@ -118,13 +125,13 @@ int choose_ctas(const qg_kv_cache& c, const qg_kv_batch& b, int64_t group, int64
 }
 
 // The line of prompts is counted in 32 bits.
-bool line_fits(const qg_kv_cache& c, const qg_kv_batch& b, int64_t per2)
+bool line_fits(const Shape& c, const qg_kv_batch& b, int64_t per2)
 {
     const int64_t pairs = b.tokens / per2 + b.sequences;
     return pairs * (ceil_div(b.prefix_len, kBlock) + ceil_div(b.max_kv, kBlock) + 1) < ((int64_t)1 << 30) / c.heads_kv;
 }
 
-Plan make_plan(const qg_kv_cache& c, const qg_kv_batch& b, int heads_q)
+Plan make_plan(const Shape& c, const qg_kv_batch& b, int heads_q)
 {
     Plan p{};
     const int64_t group = heads_q / c.heads_kv, sms = num_sms();
@@ -132,7 +139,7 @@ Plan make_plan(const qg_kv_cache& c, const qg_kv_batch& b, int heads_q)
     const int64_t np = ceil_div(b.prefix_len, kBlock), no = ceil_div(b.max_kv, kBlock);
     const int64_t prefix_tiles = ceil_div(b.prefix_len, kTile), own_tiles = ceil_div(b.max_kv, kTile);
     const int64_t own_units = (int64_t)b.sequences * c.heads_kv * ceil_div(group * b.max_q, 64);
-    const bool tiles = group <= 128;   // a tile holds whole tokens
+    const bool tiles = c.tiles && group <= 128;   // a tile holds whole tokens
     const bool share = b.sequences > 1 && b.prefix_len >= 256;
     p.way = share ? kTilesShared : kAlone;
     if (share) {
@@ -360,19 +367,20 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder()
     return fn;
 }
 
-qg_status encode(CUtensorMap* map, int dtype, int rank, const void* base, const cuuint64_t* dims,
-                 const cuuint64_t* strides, const cuuint32_t* box)
+qg_status encode(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
+                 const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B)
 {
     const PFN_cuTensorMapEncodeTiled_v12000 fn = encoder();
     if (!fn) return fail(QG_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
     const cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
-    const CUresult r = fn(map, dtype == QG_T_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                          (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const CUresult r = fn(map, type, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(QG_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
     return QG_OK;
 }
+
+CUtensorMapDataType type_of(int dtype) { return dtype == QG_T_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16; }
 }  // namespace
 
 qg_status encode_pages(CUtensorMap* map, const qg_kv_cache& c, const void* base, int box_rows, bool whole)
@@ -385,11 +393,23 @@ qg_status encode_pages(CUtensorMap* map, const qg_kv_cache& c, const void* base,
     if (whole) {
         const cuuint64_t dims[5] = {64, places, halves, heads, pages}, strides[4] = {token, 128, head, page};
         const cuuint32_t box[5] = {64u, (cuuint32_t)box_rows, (cuuint32_t)halves, 1u, 1u};
-        return encode(map, c.dtype, 5, base, dims, strides, box);
+        return encode(map, type_of(c.dtype), 5, base, dims, strides, box);
     }
     const cuuint64_t dims[4] = {64 * halves, places, heads, pages}, strides[3] = {token, head, page};
     const cuuint32_t box[4] = {64u, (cuuint32_t)box_rows, 1u, 1u};
-    return encode(map, c.dtype, 4, base, dims, strides, box);
+    return encode(map, type_of(c.dtype), 4, base, dims, strides, box);
+}
+
+qg_status encode_pages8(CUtensorMap* map, const qg_kv8_cache& c, const void* base, int box_rows)
+{
+    const cuuint64_t any = 16, token = (cuuint64_t)c.token_stride;   // as above
+    const cuuint64_t head = c.heads_kv > 1 ? (cuuint64_t)c.head_stride : any;
+    const cuuint64_t page = c.num_pages > 1 ? (cuuint64_t)c.page_stride : any;
+    const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.heads_kv, (cuuint64_t)c.num_pages};
+    const cuuint64_t strides[3] = {token, head, page};
+    const cuuint32_t box[4] = {(cuuint32_t)c.head_dim, (cuuint32_t)box_rows, 1u, 1u};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box,
+                  c.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 qg_status encode_rows(CUtensorMap* map, int dtype, const void* q, int dim, int heads_q, int64_t ldq, int64_t tokens,
@@ -398,33 +418,59 @@ qg_status encode_rows(CUtensorMap* map, int dtype, const void* q, int dim, int h
     const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads_q, (cuuint64_t)tokens};
     const cuuint64_t strides[2] = {(cuuint64_t)dim * 2, (cuuint64_t)ldq * 2};
     const cuuint32_t box[3] = {64u, (cuuint32_t)group, (cuuint32_t)tile_tokens(group)};
-    return encode(map, dtype, 3, q, dims, strides, box);
+    return encode(map, type_of(dtype), 3, q, dims, strides, box);
 }
 
 }  // namespace attn
 
+namespace {
+
+attn::Shape shape_of(const qg_kv_cache& c) { return attn::Shape{c.heads_kv, c.head_dim, 2, true}; }
+attn::Shape shape_of(const qg_kv8_cache& c) { return attn::Shape{c.heads_kv, c.head_dim, 1, false}; }
+
+attn::Args make_args(const kv::Cache& c, const qg_kv_batch& batch, const void* q, int64_t ldq, int heads_q, float scale,
+                     void* out, int64_t ldo, int ot, float* lse, char* ws, const attn::Places& w)
+{
+    attn::Args a;
+    a.bt = kv::make_batch(batch);
+    a.c = c;
+    a.q = q; a.ldq = ldq;
+    a.heads_q = heads_q; a.group = heads_q / c.heads;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.out = out; a.ldo = ldo; a.out_type = ot; a.lse = lse;
+    a.rows = (int64_t)batch.tokens * heads_q;
+    a.part_o = w.bytes ? reinterpret_cast<float*>(ws) : nullptr;
+    a.part_ml = w.bytes ? reinterpret_cast<float2*>(ws + w.ml) : nullptr;
+    a.status = device_status_ptr();
+    return a;
+}
+
+attn::Layout make_layout(const attn::Plan& p, const attn::Places& w, char* ws, int group)
+{
+    return attn::Layout{reinterpret_cast<attn::Line*>(ws + w.line), reinterpret_cast<int*>(ws + w.first),
+                        reinterpret_cast<attn::Pair*>(ws + w.pair), reinterpret_cast<int*>(ws + w.cut),
+                        attn::tile_tokens(group), p.ctas, (int)p.pairs};
+}
+
+}  // namespace
+
 size_t attn_workspace_bytes(const qg_kv_cache& cache, const qg_kv_batch& batch, int heads_q)
 {
-    return attn::places(attn::make_plan(cache, batch, heads_q), batch, heads_q, cache.head_dim).bytes;
+    return attn::places(attn::make_plan(shape_of(cache), batch, heads_q), batch, heads_q, cache.head_dim).bytes;
+}
+
+size_t attn8_workspace_bytes(const qg_kv8_cache& cache, const qg_kv_batch& batch, int heads_q)
+{
+    return attn::places(attn::make_plan(shape_of(cache), batch, heads_q), batch, heads_q, cache.head_dim).bytes;
 }
 
 qg_status launch_attn(const qg_kv_cache& cache, const qg_kv_batch& batch, const void* q, int64_t ldq, int heads_q,
                       float scale, void* out, int64_t ldo, int ot, float* lse, void* ws, cudaStream_t s)
 {
-    const attn::Plan p = attn::make_plan(cache, batch, heads_q);
-    attn::Args a;
-    a.bt = kv::make_batch(batch);
-    a.c = kv::make_cache(cache);
-    a.q = q; a.ldq = ldq;
-    a.heads_q = heads_q; a.group = heads_q / cache.heads_kv;
-    a.scale_log2 = scale * 1.4426950408889634f;
-    a.out = out; a.ldo = ldo; a.out_type = ot; a.lse = lse;
-    a.rows = (int64_t)batch.tokens * heads_q;
+    const attn::Plan p = attn::make_plan(shape_of(cache), batch, heads_q);
     const attn::Places w = attn::places(p, batch, heads_q, cache.head_dim);
     char* base = static_cast<char*>(ws);
-    a.part_o = w.bytes ? reinterpret_cast<float*>(base) : nullptr;
-    a.part_ml = w.bytes ? reinterpret_cast<float2*>(base + w.ml) : nullptr;
-    a.status = device_status_ptr();
+    attn::Args a = make_args(kv::make_cache(cache), batch, q, ldq, heads_q, scale, out, ldo, ot, lse, base, w);
     qg_status st = QG_OK;
     CUtensorMap qmap, kmap, vmap;
     cudaError_t e = cudaSuccess;
@@ -435,9 +481,7 @@ qg_status launch_attn(const qg_kv_cache& cache, const qg_kv_batch& batch, const 
         if (st == QG_OK) st = attn::encode_pages(&vmap, cache, cache.v, a.box_rows, false);
         if (st != QG_OK) return st;
         if (p.way == attn::kPrompts) {
-            const attn::Layout lay{reinterpret_cast<attn::Line*>(base + w.line), reinterpret_cast<int*>(base + w.first),
-                                   reinterpret_cast<attn::Pair*>(base + w.pair), reinterpret_cast<int*>(base + w.cut),
-                                   attn::tile_tokens(a.group), p.ctas, (int)p.pairs};
+            const attn::Layout lay = make_layout(p, w, base, a.group);
             e = attn::launch_tiles(a, cache.dtype, qmap, kmap, vmap, lay, s);
             if (e == cudaSuccess) e = attn::launch_join_line(a, lay, s);
         } else {
@@ -458,6 +502,28 @@ qg_status launch_attn(const qg_kv_cache& cache, const qg_kv_batch& batch, const 
                                             : attn::launch_join(a, p.deal, 0, p.parts, s);
     }
     if (e != cudaSuccess) return cuda_fail(e, "qattn_forward launch");
+    return QG_OK;
+}
+
+qg_status launch_attn8(const qg_kv8_cache& cache, const qg_kv_batch& batch, const void* q, int64_t ldq, int heads_q, int qt,
+                       float scale, void* out, int64_t ldo, int ot, float* lse, void* ws, cudaStream_t s)
+{
+    const attn::Plan p = attn::make_plan(shape_of(cache), batch, heads_q);
+    const attn::Places w = attn::places(p, batch, heads_q, cache.head_dim);
+    char* base = static_cast<char*>(ws);
+    const kv8::Cache c = kv8::make_cache(cache);
+    const kv::Cache pages{c.num_pages, c.page_shift, c.heads, c.dim, c.page_stride, c.token_stride, c.head_stride};
+    attn::Args8 a{make_args(pages, batch, q, ldq, heads_q, scale, out, ldo, ot, lse, base, w), cache.k_scale, cache.v_scale,
+                  c.scale_page, c.scale_block, c.scale_head, qt};
+    CUtensorMap kmap, vmap;
+    a.a.box_rows = std::min(cache.page_size, attn::kTile);
+    qg_status st = attn::encode_pages8(&kmap, cache, cache.k, a.a.box_rows);
+    if (st == QG_OK) st = attn::encode_pages8(&vmap, cache, cache.v, a.a.box_rows);
+    if (st != QG_OK) return st;
+    cudaError_t e = p.way == attn::kRowsShared ? attn::launch_rows8_shared(a, kmap, vmap, p.n, s)
+                                               : attn::launch_rows8(a, kmap, vmap, attn::kPrefix | attn::kOwn, p.n, false, s);
+    if (e == cudaSuccess && p.parts > 1) e = attn::launch_join(a.a, p.deal, 0, p.parts, s);
+    if (e != cudaSuccess) return cuda_fail(e, "qattn8_forward launch");
     return QG_OK;
 }
 

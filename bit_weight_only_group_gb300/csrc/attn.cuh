@@ -10,6 +10,7 @@
 
 #include <cuda.h>
 
+#include "kv8.cuh"
 #include "kv_batch.cuh"
 #include "ptx.cuh"
 
@@ -39,6 +40,32 @@ struct Args {
     int* status;
 };
 
+// Attention over the 8-bit cache: a.c's strides count bytes, a.q is of type q_type.
+//
+// The products are in fp16, which holds the codes exactly.  A row of q is scaled
+// by a power of two to below 2^15 (its lower bits, down to 2^-39 of the row's
+// largest value, stay), and the K scale goes on the logits in fp32.  The V scale
+// 2^ev goes into the exponent: P' = 2^(s + ev - m) with m the maximum of s + ev,
+// so that P' codes sum to 2^-m sum 2^s v, and l = sum 2^-ev P' (fp32) is 2^-m sum
+// 2^s: parts as above, but that m is not the largest s.  P' is rounded to fp16.
+struct Args8 {
+    Args a;
+    const uint8_t *k_scale, *v_scale;
+    long long scale_page, scale_block, scale_head;
+    int q_type;
+};
+// Exponent of the scale of a K or V block (a byte outside 1 .. 254 is none the appending kernel wrote).
+__device__ __forceinline__ int scale_exp_at(const Args8& p, bool v, int page, int block, int head)
+{
+    const uint8_t* s = (v ? p.v_scale : p.k_scale) + (long long)page * p.scale_page + (long long)block * p.scale_block +
+                       (long long)head * p.scale_head;
+    return min(max((int)__ldg(s), 1), 254) - kv8::kBias;
+}
+// 2^n and 2^-n of such an exponent.
+__device__ __forceinline__ float scale_of(int e) { return kv8::pow2(e); }
+// The power of two 2^x that brings a row with the largest magnitude amax to 2^14 .. 2^15 is 2^(14 - x).
+__device__ __forceinline__ int row_exp(float amax) { return max((int)(__float_as_uint(amax) >> 23) - 127, -100); }
+
 constexpr float kLn2 = 0.69314718055994530942f;
 
 // Values of a finished row.
@@ -49,6 +76,15 @@ __device__ __forceinline__ void store_out2(const Args& a, long long at, float x,
     else
         *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at) =
             a.out_type == QG_T_BF16 ? kv::pack2<__nv_bfloat16>(x, y) : kv::pack2<__half>(x, y);
+}
+__device__ __forceinline__ void store_out4(const Args& a, long long at, float4 v)
+{
+    if (a.out_type == QG_T_F32)
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = v;
+    else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+            a.out_type == QG_T_BF16 ? make_uint2(kv::pack2<__nv_bfloat16>(v.x, v.y), kv::pack2<__nv_bfloat16>(v.z, v.w))
+                                    : make_uint2(kv::pack2<__half>(v.x, v.y), kv::pack2<__half>(v.z, v.w));
 }
 // Eight fp32 values (as bits).
 __device__ __forceinline__ void store_out8(const Args& a, long long at, const uint32_t* v)
@@ -119,6 +155,8 @@ __device__ __forceinline__ int page_of(const Args& a, const int* table, int n, i
 // head, head, page), boxes of box_rows places of a whole head; else (dim,
 // place, head, page), boxes of 64 values x box_rows places.
 qg_status encode_pages(CUtensorMap* map, const qg_kv_cache& c, const void* base, int box_rows, bool whole);
+// Map of 8-bit K or V pages: dimensions (dim, place, head, page), boxes of box_rows places of a whole head.
+qg_status encode_pages8(CUtensorMap* map, const qg_kv8_cache& c, const void* base, int box_rows);
 // Map of the query rows: dimensions (dim, head, token), boxes of 64 values x a group x a tile's tokens.
 qg_status encode_rows(CUtensorMap* map, int dtype, const void* q, int dim, int heads_q, int64_t ldq, int64_t tokens,
                       int group);
@@ -207,6 +245,11 @@ cudaError_t launch_rows(const Args& a, int dtype, const CUtensorMap& kmap, const
 // The shared prefix for all rows and the own tokens in one launch.
 cudaError_t launch_rows_shared(const Args& a, int dtype, const CUtensorMap& kmap, const CUtensorMap& vmap, const Parts& p,
                                cudaStream_t s);
+// The same two over the 8-bit cache.
+cudaError_t launch_rows8(const Args8& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int keys, const Parts& n,
+                         bool beside, cudaStream_t s);
+cudaError_t launch_rows8_shared(const Args8& p, const CUtensorMap& kmap, const CUtensorMap& vmap, const Parts& n,
+                                cudaStream_t s);
 // Tokens of a tile of the tile kernel (its rows: that times the group, at most 128).
 inline int tile_tokens(int64_t group) { return (int)(128 / group); }
 // The shared prefix for all tokens, dealt to at most `ctas` CTAs, parts 0 .. most_pieces() - 1.

@@ -3,7 +3,10 @@
 //
 // For a rotated pair (a, c) with the position's cosine and sine:
 //     a' = a cos - c sin,  c' = c cos + a sin,
-// in fp32, rounded once to the cache's type.
+// in fp32, rounded once to the cache's type.  Where queries and keys are normed
+// (a form of the kernel of its own) x becomes x w / sqrt(mean x^2 + eps) first:
+// the threads of a head sum their squares by shuffles, and the weights lie in
+// shared memory in fp32.
 //
 // Bound by HBM: every value is read and written once and the arithmetic is a
 // few operations a value.  A CTA works through units (a token, or some heads of
@@ -20,7 +23,7 @@
 // 32 + 2 x 32 heads (58 MB) 17.9 us, 3.2 TB/s.  A CTA has about five units there
 // (two a token), too few to hide the launch's start and end (the 4.0 us of one
 // token) and the first places; what the rest waits for has not been measured.
-#include "kv_batch.cuh"
+#include "kv_heads.cuh"
 #include "ptx.cuh"
 
 #include <algorithm>
@@ -41,46 +44,13 @@ struct AppendArgs {
     const float* rope;   // null: no rotation
     const int* at;
     int positions, rot, interleaved;
+    Norm norm;
     int* status;
 };
 
 constexpr int kWorkers = 256, kThreads = kWorkers + 32;   // the last warp finds places; two CTAs an SM
 constexpr int kPlaces = 64;                   // two rounds of a warp's
 constexpr int kStages = 4, kStageBytes = 24 * 1024;   // at most
-
-template <typename T> struct Run8 { uint4 w; };                 // 8 values of 16 bits
-template <> struct Run8<float> { float4 w[2]; };
-
-template <typename T> __device__ __forceinline__ Run8<T> load8(const T* p)
-{
-    return *reinterpret_cast<const Run8<T>*>(p);
-}
-
-template <typename T> __device__ __forceinline__ void to_float(const Run8<T>& r, float (&f)[8])
-{
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int i = 0; i < 2; i++) {
-            f[4 * i] = r.w[i].x; f[4 * i + 1] = r.w[i].y; f[4 * i + 2] = r.w[i].z; f[4 * i + 3] = r.w[i].w;
-        }
-    } else {
-        const uint32_t w[4] = {r.w.x, r.w.y, r.w.z, r.w.w};
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            float2 v;
-            if constexpr (std::is_same<T, __half>::value) v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-            else v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
-            f[2 * i] = v.x;
-            f[2 * i + 1] = v.y;
-        }
-    }
-}
-
-template <typename T> __device__ __forceinline__ void store8(T* p, const float (&f)[8])
-{
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]),
-                                              pack2<T>(f[6], f[7]));
-}
 
 // Where a token goes.
 struct Place {
@@ -118,12 +88,13 @@ __device__ __forceinline__ Place find_place(const AppendArgs& a, int t, bool the
     return p;
 }
 
-template <typename TI, typename TO, int D>
+template <typename TI, typename TO, int D, bool NORM>
 __global__ void __launch_bounds__(kThreads, 2) k_kv_append(const __grid_constant__ AppendArgs a, int chunks, int stages)
 {
     constexpr int per_head = D / 16, chunk_heads = kStageBytes / (D * (int)sizeof(TI));
     extern __shared__ __align__(128) unsigned char ring[];
     __shared__ Place places[kPlaces];
+    __shared__ __align__(16) float weights[NORM ? 2 * D : 4];   // of queries, of keys
     __shared__ __align__(8) uint64_t arrived[kStages];
     const uint32_t bars = ptx::smem_u32(arrived);
     if (threadIdx.x == 0) {
@@ -162,6 +133,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_append(const __grid_constant
     };
     for (int i = 0; i < stages; i++) load(blockIdx.x + i * stride, i);
     if (blockIdx.x >= units) return;   // fewer tokens in use than rows
+    if constexpr (NORM) {
+        if (threadIdx.x < 2 * D) {
+            const bool key = threadIdx.x >= D;
+            weights[threadIdx.x] = norm_weight(a.norm, key, threadIdx.x % D);
+        }
+    }
     find(0);
     __syncthreads();
 
@@ -192,7 +169,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_append(const __grid_constant
         if (n % 32 == 0 && unit + 32 * stride < units) find(n + 32);
         n++;
         if (unit + stride < units) angles(places[n % kPlaces], next_cs, next_sn);
-        const bool ok = ptx::mbar_wait(bars + 8 * stage, phase);
+        bool ok = ptx::mbar_wait(bars + 8 * stage, phase);
+        if constexpr (NORM) ok = __all_sync(0xffffffffu, ok);   // a head's threads shuffle together or not at all
         const TI* x = reinterpret_cast<const TI*>(ring + stage * kStageBytes);
         const long long cached = (long long)p.page * a.c.page_stride + (long long)p.in_page * a.c.token_stride;
         for (int head = lo + first; threadIdx.x < kWorkers && ok && p.at >= 0 && head < hi; head += step) {
@@ -202,25 +180,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_append(const __grid_constant
             float f0[8], f1[8];
             to_float(load8(x + (head - lo) * D + i0), f0);
             to_float(load8(x + (head - lo) * D + i1), f1);
-            if (turn && !value) {
-                if (a.interleaved) {
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const float c = f0[2 * i], d = f0[2 * i + 1], e = f1[2 * i], f = f1[2 * i + 1];
-                        f0[2 * i] = c * cs[i] - d * sn[i];
-                        f0[2 * i + 1] = d * cs[i] + c * sn[i];
-                        f1[2 * i] = e * cs[4 + i] - f * sn[4 + i];
-                        f1[2 * i + 1] = f * cs[4 + i] + e * sn[4 + i];
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        const float c = f0[i], d = f1[i];
-                        f0[i] = c * cs[i] - d * sn[i];
-                        f1[i] = d * cs[i] + c * sn[i];
-                    }
-                }
+            if constexpr (NORM) {
+                const bool key = head >= hq;
+                if (!value && (key ? a.norm.k : a.norm.q)) norm_head<per_head, D>(f0, f1, weights + key * D, i0, i1, a.norm.eps);
             }
+            if (turn && !value) turn16(f0, f1, cs, sn, a.interleaved);
             TO* dst = head < hq ? static_cast<TO*>(a.q_out) + t * a.ldq_out + head * D
                                 : static_cast<TO*>(value ? a.vc : a.kc) + cached +
                                       (long long)(head - hq - (value ? hk : 0)) * a.c.head_stride;
@@ -242,10 +206,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_kv_append(const __grid_constant
     }
 }
 
-template <typename TI, typename TO, int D>
+template <typename TI, typename TO, int D, bool NORM>
 cudaError_t launch(const AppendArgs& a, cudaStream_t s)
 {
-    auto kernel = k_kv_append<TI, TO, D>;
+    auto kernel = k_kv_append<TI, TO, D, NORM>;
     const int heads = a.heads_q + 2 * a.c.heads, chunks = (int)ceil_div(heads, kStageBytes / (D * (int)sizeof(TI)));
     const int64_t units = (int64_t)a.bt.T * chunks, grid = std::min<int64_t>(units, 2 * num_sms());
     const int stages = (int)std::min<int64_t>(kStages, ceil_div(units, grid)), smem = stages * kStageBytes;
@@ -257,27 +221,29 @@ cudaError_t launch(const AppendArgs& a, cudaStream_t s)
     return launch_dependent(kernel, dim3((unsigned)grid), kThreads, smem, s, a, chunks, stages);
 }
 
-template <typename TO, int D>
+template <typename TO, int D, bool NORM>
 cudaError_t by_input(const AppendArgs& a, int xt, cudaStream_t s)
 {
     switch (xt) {
-        case QG_T_F32: return launch<float, TO, D>(a, s);
-        case QG_T_BF16: return launch<__nv_bfloat16, TO, D>(a, s);
-        default: return launch<__half, TO, D>(a, s);
+        case QG_T_F32: return launch<float, TO, D, NORM>(a, s);
+        case QG_T_BF16: return launch<__nv_bfloat16, TO, D, NORM>(a, s);
+        default: return launch<__half, TO, D, NORM>(a, s);
     }
 }
 
 template <typename TO>
 cudaError_t by_dim(const AppendArgs& a, int xt, cudaStream_t s)
 {
-    return a.c.dim == 128 ? by_input<TO, 128>(a, xt, s) : by_input<TO, 64>(a, xt, s);
+    if (a.norm.q || a.norm.k)
+        return a.c.dim == 128 ? by_input<TO, 128, true>(a, xt, s) : by_input<TO, 64, true>(a, xt, s);
+    return a.c.dim == 128 ? by_input<TO, 128, false>(a, xt, s) : by_input<TO, 64, false>(a, xt, s);
 }
 
 }  // namespace
 }  // namespace kv
 
-qg_status launch_kv_append(const qg_kv_cache& cache, const qg_kv_batch& batch, const qg_rope* rope, const void* q,
-                           int64_t ldq, int heads_q, const void* k, int64_t ldk, const void* v, int64_t ldv, int xt,
+qg_status launch_kv_append(const qg_kv_cache& cache, const qg_kv_batch& batch, const qg_head_norm* norm,
+                           const qg_rope* rope, const void* q, int64_t ldq, int heads_q, const void* k, int64_t ldk, const void* v, int64_t ldv, int xt,
                            void* q_out, int64_t ldq_out, cudaStream_t s)
 {
     kv::AppendArgs a;
@@ -293,6 +259,7 @@ qg_status launch_kv_append(const qg_kv_cache& cache, const qg_kv_batch& batch, c
     a.positions = rope ? rope->positions : 0;
     a.rot = rope ? rope->dim : 0;
     a.interleaved = rope ? rope->interleaved != 0 : 0;
+    a.norm = kv::make_norm(norm);
     a.status = device_status_ptr();
     const cudaError_t e = cache.dtype == QG_T_BF16 ? kv::by_dim<__nv_bfloat16>(a, xt, s)
                                                    : kv::by_dim<__half>(a, xt, s);

@@ -140,11 +140,19 @@ qg_status launch_diag(const uint16_t* W, const qg_qweight& w, float threshold, f
                       cudaStream_t s);
 
 // ---------------------------------------------------------------- paged cache and attention
-qg_status launch_kv_append(const qg_kv_cache& cache, const qg_kv_batch& batch, const qg_rope* rope, const void* q,
-                           int64_t ldq, int heads_q, const void* k, int64_t ldk, const void* v, int64_t ldv, int xt,
+qg_status launch_kv_append(const qg_kv_cache& cache, const qg_kv_batch& batch, const qg_head_norm* norm,
+                           const qg_rope* rope, const void* q, int64_t ldq, int heads_q, const void* k, int64_t ldk, const void* v, int64_t ldv, int xt,
                            void* q_out, int64_t ldq_out, cudaStream_t s);
+qg_status launch_kv8_append(const qg_kv8_cache& cache, const qg_kv_batch& batch, const qg_head_norm* norm,
+                            const qg_rope* rope, const void* q, int64_t ldq, int heads_q, const void* k, int64_t ldk,
+                            const void* v, int64_t ldv, int xt, void* q_out, int64_t ldq_out, int qt, cudaStream_t s);
+qg_status launch_kv8_read(const qg_kv8_cache& cache, const qg_kv_batch& batch, void* k, int64_t ldk, void* v,
+                          int64_t ldv, int ot, cudaStream_t s);
 size_t attn_workspace_bytes(const qg_kv_cache& cache, const qg_kv_batch& batch, int heads_q);
 qg_status launch_attn(const qg_kv_cache& cache, const qg_kv_batch& batch, const void* q, int64_t ldq, int heads_q,
                       float scale, void* out, int64_t ldo, int ot, float* lse, void* ws, cudaStream_t s);
+size_t attn8_workspace_bytes(const qg_kv8_cache& cache, const qg_kv_batch& batch, int heads_q);
+qg_status launch_attn8(const qg_kv8_cache& cache, const qg_kv_batch& batch, const void* q, int64_t ldq, int heads_q, int qt,
+                       float scale, void* out, int64_t ldo, int ot, float* lse, void* ws, cudaStream_t s);
 
 }  // namespace qg

@@ -572,6 +572,90 @@ QG_API qg_status qkv_append(const qg_kv_cache* cache, const qg_kv_batch* batch, 
                             qg_dtype xt, void* q_out, int64_t ldq_out, void* stream);
 
 /*
+ * Norms of queries and keys for each head, applied before the rotation in the
+ * pass that appends them:  y = x * w / sqrt(mean_d x_d^2 + eps)  over a head's
+ * head_dim values, in fp32.
+ *  q, k    head_dim weights of type dtype, shared by the heads (DEVICE, 16-byte
+ *          aligned); NULL: the queries, or the keys, are not normed.
+ *  dtype   QG_T_F32, QG_T_BF16 or QG_T_F16.
+ *  eps     >= 0, finite.  (With 0 a head of zeros becomes NaN, as the formula.)
+ */
+typedef struct {
+    const void* q;
+    const void* k;
+    int32_t dtype;
+    float eps;
+} qg_head_norm;
+
+/* qkv_append with the norms applied first (norm NULL: qkv_append itself); each
+ * value is still rounded once.  Other arguments and errors as qkv_append. */
+QG_API qg_status qkv_append_norm(const qg_kv_cache* cache, const qg_kv_batch* batch, const qg_head_norm* norm,
+                                 const qg_rope* rope, const void* q, int64_t ldq, int32_t heads_q, const void* k,
+                                 int64_t ldk, const void* v, int64_t ldv, qg_dtype xt, void* q_out, int64_t ldq_out,
+                                 void* stream);
+
+/*
+ * The paged cache in 8 bits: E4M3 codes (1 sign, 4 exponent bits with bias 7, 3
+ * fraction bits, up to 448, 0x7F a NaN) and one power of two for QG_KV8_BLOCK
+ * places of a page and head.  Code c of token place s of page p, head h, is at
+ *     k + p * page_stride + s * token_stride + h * head_stride   (bytes)
+ * and its scale's byte at
+ *     k_scale + p * scale_page_stride + (s / QG_KV8_BLOCK) * scale_block_stride + h * scale_head_stride;
+ * the value is c * 2^(byte - 127).  v and v_scale likewise.
+ *  num_pages, page_size, heads_kv, head_dim   as qg_kv_cache.
+ *  k, v         16-byte aligned; their strides multiples of 16, at least
+ *               head_dim, and below 2^38.  The scales' strides 1 .. 2^38.
+ * A power of two costs E4M3, whose precision is relative, nothing but range at
+ * its lower end, and makes every value exact in bf16.
+ */
+#define QG_KV8_BLOCK 16
+typedef struct {
+    void* k;
+    void* v;
+    uint8_t* k_scale;
+    uint8_t* v_scale;
+    int32_t num_pages, page_size, heads_kv, head_dim;
+    int64_t page_stride, token_stride, head_stride;
+    int64_t scale_page_stride, scale_block_stride, scale_head_stride;
+} qg_kv8_cache;
+
+/*
+ * Append to a cache in 8 bits: qkv_append_norm's arguments, with the queries
+ * written in type qt (QG_T_BF16 or QG_T_F16).  For each block of QG_KV8_BLOCK
+ * places and head, with amax the largest magnitude of its new values (normed and
+ * turned, fp32):
+ *     e = the least integer with amax <= 448 * 2^e, within -64 .. 63,
+ *     code = the nearest E4M3 value of value * 2^-e (ties to even).
+ * A block whose first place is older than the batch's new tokens keeps the
+ * larger of its own e and theirs; where theirs is larger its earlier codes are
+ * rewritten, code * 2^(e_old - e) rounded again (exact above E4M3's subnormal
+ * range), so a block's values may depend on how its tokens were appended.
+ * Values that are not finite or above 448 * 2^63 become NaN and do not count
+ * for amax; values below 2^-9 * 2^-64 become 0.  The places of a block belong
+ * to one sequence.  What is not cached and what sets the status word: as for
+ * qkv_append; for a sequence outside its bounds the queries are not written.
+ */
+QG_API qg_status qkv8_append(const qg_kv8_cache* cache, const qg_kv_batch* batch, const qg_head_norm* norm,
+                             const qg_rope* rope, const void* q, int64_t ldq, int32_t heads_q, const void* k,
+                             int64_t ldk, const void* v, int64_t ldv, qg_dtype xt, void* q_out, int64_t ldq_out,
+                             qg_dtype qt, void* stream);
+
+/*
+ * Read the batch's tokens back: for each of the rows qkv8_append would write
+ * (the last n_b of sequence b's L_b own places) the values its codes stand for,
+ * rounded to type ot (exact in QG_T_F32 and QG_T_BF16; in QG_T_F16 within its
+ * range).  With n_b = L_b that is all a sequence has; the prefix is read as a
+ * sequence over its own pages.
+ *   k, v     [T, heads_kv, head_dim] of type ot, tokens ldk / ldv elements
+ *            apart; DEVICE, 16-byte aligned, leading dimensions multiples of 16 bytes.
+ * Rows of no sequence, of one outside its bounds (status word), at negative
+ * places or in invalid pages are left as they were.
+ * Errors: QG_ERR_INVALID_ARG, QG_ERR_UNSUPPORTED, QG_ERR_ALIGNMENT, QG_ERR_CUDA.
+ */
+QG_API qg_status qkv8_read(const qg_kv8_cache* cache, const qg_kv_batch* batch, void* k, int64_t ldk, void* v,
+                           int64_t ldv, qg_dtype ot, void* stream);
+
+/*
  * Attention of the batch's new tokens over the shared prefix and their own
  * cached tokens:
  *     out[t, h] = sum_j p_j v_j,  p = softmax_j(scale * q[t, h] . k_j)
@@ -605,6 +689,24 @@ QG_API qg_status qattn_workspace_size(const qg_kv_cache* cache, const qg_kv_batc
 QG_API qg_status qattn_forward(const qg_kv_cache* cache, const qg_kv_batch* batch, const void* q, int64_t ldq,
                                int32_t heads_q, float scale, void* out, int64_t ldo, qg_dtype ot, float* lse, void* ws,
                                size_t ws_bytes, void* stream);
+
+/*
+ * Attention over a cache in 8 bits: qattn_forward with K and V the values their
+ * codes stand for.  q is of type qt (QG_T_BF16 or QG_T_F16); ldq a multiple of
+ * 8 elements; the workspace's size comes from qattn8_workspace_size; other
+ * arguments, masks, rows that see nothing and errors as there.
+ * Logits, the softmax's maximum and sum, and the sums over v are held in fp32.
+ * The products' operands are in fp16: the codes are exact in it, q is scaled by
+ * a power of two a row (what is lost lies below 2^-39 of the row's largest
+ * value), and the probabilities, weighted with their V scales, are rounded to it
+ * (off by at most 2^-11 of themselves, or 2^-25 of the row's largest).  A NaN
+ * code in reach stays in its sequence and key/value head, as above.
+ */
+QG_API qg_status qattn8_workspace_size(const qg_kv8_cache* cache, const qg_kv_batch* batch, int32_t heads_q,
+                                       size_t* bytes);
+QG_API qg_status qattn8_forward(const qg_kv8_cache* cache, const qg_kv_batch* batch, const void* q, int64_t ldq,
+                                int32_t heads_q, qg_dtype qt, float scale, void* out, int64_t ldo, qg_dtype ot,
+                                float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /* Self-check of the failure path of the bounded waits: launches one small
  * kernel on `stream` whose single mbarrier wait (at most poll_limit polls,
