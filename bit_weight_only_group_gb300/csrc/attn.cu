@@ -49,6 +49,21 @@ void split(int64_t units, int64_t tiles, int64_t ctas, int least, int* parts, in
     *parts = (int)std::max<int64_t>(1, ceil_div(tiles, *per));
 }
 
+// The same over the 8-bit cache, for the row kernel alone on the card: parts enough for three CTAs an SM as above, and
+// more, of at least 32 tiles, up to six, so that sequences of uneven lengths end together (32 sequences of 1 to 16384
+// tokens 120 us, 140 without; finer parts cost more in starts and ends of CTAs: 16 of 8192 tokens in 4 parts 59 us, in 8
+// 71).
+void split8(int64_t units, int64_t tiles, int64_t sms, int* parts, int* per)
+{
+    int n, t;
+    split(units, tiles, 3 * sms, kLeastTiles, parts, per);
+    split(units, tiles, 6 * sms, 32, &n, &t);
+    if (n > *parts) {
+        *parts = n;
+        *per = t;
+    }
+}
+
 // The shared prefix dealt to `ctas` CTAs, none with less than two blocks.
 Deal make_deal(const Shape& c, const qg_kv_batch& b, int64_t group, int ctas)
 {
@@ -161,7 +176,8 @@ Plan make_plan(const Shape& c, const qg_kv_batch& b, int heads_q)
     }
     switch (p.way) {
         case kAlone:
-            split(own_units, prefix_tiles + own_tiles, 3 * sms, kLeastTiles, &p.n.own_parts, &p.n.own_tiles);
+            if (c.bytes == 1) split8(own_units, prefix_tiles + own_tiles, sms, &p.n.own_parts, &p.n.own_tiles);
+            else split(own_units, prefix_tiles + own_tiles, 3 * sms, kLeastTiles, &p.n.own_parts, &p.n.own_tiles);
             break;
         case kRowsShared: {
             const int64_t units = c.heads_kv * ceil_div(rows, 64);
@@ -426,7 +442,7 @@ qg_status encode_rows(CUtensorMap* map, int dtype, const void* q, int dim, int h
 namespace {
 
 attn::Shape shape_of(const qg_kv_cache& c) { return attn::Shape{c.heads_kv, c.head_dim, 2, true}; }
-attn::Shape shape_of(const qg_kv8_cache& c) { return attn::Shape{c.heads_kv, c.head_dim, 1, false}; }
+attn::Shape shape_of(const qg_kv8_cache& c) { return attn::Shape{c.heads_kv, c.head_dim, 1, true}; }
 
 attn::Args make_args(const kv::Cache& c, const qg_kv_batch& batch, const void* q, int64_t ldq, int heads_q, float scale,
                      void* out, int64_t ldo, int ot, float* lse, char* ws, const attn::Places& w)
@@ -513,16 +529,30 @@ qg_status launch_attn8(const qg_kv8_cache& cache, const qg_kv_batch& batch, cons
     char* base = static_cast<char*>(ws);
     const kv8::Cache c = kv8::make_cache(cache);
     const kv::Cache pages{c.num_pages, c.page_shift, c.heads, c.dim, c.page_stride, c.token_stride, c.head_stride};
-    attn::Args8 a{make_args(pages, batch, q, ldq, heads_q, scale, out, ldo, ot, lse, base, w), cache.k_scale, cache.v_scale,
+    attn::Args8 a{make_args(pages, batch, q, ldq, heads_q, scale, out, ldo, ot, lse, base, w),
+                  static_cast<const uint8_t*>(cache.k), static_cast<const uint8_t*>(cache.v), cache.k_scale, cache.v_scale,
                   c.scale_page, c.scale_block, c.scale_head, qt};
-    CUtensorMap kmap, vmap;
-    a.a.box_rows = std::min(cache.page_size, attn::kTile);
-    qg_status st = attn::encode_pages8(&kmap, cache, cache.k, a.a.box_rows);
-    if (st == QG_OK) st = attn::encode_pages8(&vmap, cache, cache.v, a.a.box_rows);
-    if (st != QG_OK) return st;
-    cudaError_t e = p.way == attn::kRowsShared ? attn::launch_rows8_shared(a, kmap, vmap, p.n, s)
-                                               : attn::launch_rows8(a, kmap, vmap, attn::kPrefix | attn::kOwn, p.n, false, s);
-    if (e == cudaSuccess && p.parts > 1) e = attn::launch_join(a.a, p.deal, 0, p.parts, s);
+    cudaError_t e = cudaSuccess;
+    if (p.way == attn::kPrompts) {
+        const attn::Layout lay = make_layout(p, w, base, a.a.group);
+        e = attn::launch_layout(a.a, lay, s);
+        if (e == cudaSuccess) e = attn::launch_tiles8(a, lay, s);
+        if (e == cudaSuccess) e = attn::launch_join_line(a.a, lay, s);
+    } else {
+        CUtensorMap kmap, vmap;
+        a.a.box_rows = std::min(cache.page_size, attn::kTile);
+        qg_status st = attn::encode_pages8(&kmap, cache, cache.k, a.a.box_rows);
+        if (st == QG_OK) st = attn::encode_pages8(&vmap, cache, cache.v, a.a.box_rows);
+        if (st != QG_OK) return st;
+        if (p.way == attn::kTilesShared) e = attn::launch_tiles8_shared(a, p.deal, p.ctas, s);
+        if (e == cudaSuccess)
+            e = p.way == attn::kRowsShared    ? attn::launch_rows8_shared(a, kmap, vmap, p.n, s)
+                : p.way == attn::kTilesShared ? attn::launch_rows8(a, kmap, vmap, attn::kOwn, p.n, true, s)
+                                              : attn::launch_rows8(a, kmap, vmap, attn::kPrefix | attn::kOwn, p.n, false, s);
+        if (e == cudaSuccess && p.parts > 1)
+            e = p.way == attn::kTilesShared ? attn::launch_join(a.a, p.deal, p.n.prefix_parts, p.n.own_parts, s)
+                                            : attn::launch_join(a.a, p.deal, 0, p.parts, s);
+    }
     if (e != cudaSuccess) return cuda_fail(e, "qattn8_forward launch");
     return QG_OK;
 }

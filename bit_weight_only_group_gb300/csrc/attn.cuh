@@ -50,6 +50,7 @@ struct Args {
 // 2^s: parts as above, but that m is not the largest s.  P' is rounded to fp16.
 struct Args8 {
     Args a;
+    const uint8_t *k_codes, *v_codes;
     const uint8_t *k_scale, *v_scale;
     long long scale_page, scale_block, scale_head;
     int q_type;
@@ -258,6 +259,11 @@ cudaError_t launch_tiles_shared(const Args& a, int dtype, const CUtensorMap& qma
 // Each sequence's tokens over prefix and own tokens: lays the line out and works through it.
 cudaError_t launch_tiles(const Args& a, int dtype, const CUtensorMap& qmap, const CUtensorMap& kmap,
                          const CUtensorMap& vmap, const Layout& lay, cudaStream_t s);
+// Lays the line of prompts out.
+cudaError_t launch_layout(const Args& a, const Layout& lay, cudaStream_t s);
+// The tile kernel over the 8-bit cache (the line of prompts laid out before).
+cudaError_t launch_tiles8_shared(const Args8& p, const Deal& d, int ctas, cudaStream_t s);
+cudaError_t launch_tiles8(const Args8& p, const Layout& lay, cudaStream_t s);
 // Joins, for each row, the pieces of `d` (none when d.blocks = 0) and `parts` parts from part0 on.
 cudaError_t launch_join(const Args& a, const Deal& d, int part0, int parts, cudaStream_t s);
 // Joins the items of a line that fell into pieces.

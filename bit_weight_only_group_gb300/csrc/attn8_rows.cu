@@ -11,25 +11,27 @@
 //  V: transposed, a thread gets two keys' codes of two neighbouring columns, a
 //     byte permutation puts each column's two keys together, and the columns of
 //     a pair go to two products: a thread ends up with four neighbouring ones.
-// Scales and their use: attn.cuh.  The loading warp looks up the page and the
-// scale byte of every 16 keys two and one stages ahead and leaves 2^e beside the
-// stage.
+// Scales and their use: attn.cuh.  The loading warp looks up pages and scale
+// bytes, a chain of two loads, for 256 keys at a time (a lane for the K or the V
+// of 16), one and two such batches ahead of the copies it issues, and leaves 2^e
+// beside the stage.
 #include "attn_rows.cuh"
 
 namespace qg {
 namespace attn {
 namespace {
 
-constexpr int kGroups = KT / kv8::kBlock;    // scales of a stage, of K and of V
+// Keys of a stage: with one row block the four warps share them, 32 each; with four every warp takes all.
+template <int RW> constexpr int kKeys = RW == 4 ? 64 : 128;
 
-template <int D> struct Cfg8 {
-    // stages in flight: 16 KB each with 128-wide heads (two CTAs an SM), 8 KB with 64-wide (three)
-    static constexpr int MAX_STAGES = 6;
+template <int D, int RW> struct Cfg8 {
+    static constexpr int KT = kKeys<RW>, GROUPS = KT / kv8::kBlock;
+    static constexpr int MAX_STAGES = KT == 128 ? (D == 128 ? 3 : 5) : (D == 128 ? 6 : 8);
     static constexpr int TILE = KT * D;                  // bytes of a K or V tile: [key][dim], swizzled
     static constexpr int STAGE = 2 * TILE;
-    static constexpr int SCALES = 3 * kGroups * 4;       // of a stage: 2^ek scale log2(e), ev, 2^-ev
+    static constexpr int SCALES = 3 * GROUPS;            // floats of a stage: 2^ek scale log2(e), ev, 2^-ev
     static constexpr int OFF_SCALES = 2 * 8 * MAX_STAGES;   // after the barriers
-    static constexpr int OFF_ML = OFF_SCALES + MAX_STAGES * SCALES;
+    static constexpr int OFF_ML = OFF_SCALES + MAX_STAGES * SCALES * 4;
     static constexpr int REST = OFF_ML + kWarps * 16 * 8 + 1024;   // barriers, scales, (m, l), alignment
     static_assert(2 * 16 * D * 4 <= STAGE, "joining buffers fit a stage");
     // offset of a 16-byte chunk of a row: the swizzle of 128-byte, or of 64-byte, boxes
@@ -43,8 +45,8 @@ template <int D, int RW, int KEYS>
 __device__ __forceinline__ void work8(const CUtensorMap& kmap, const CUtensorMap& vmap, const Args8& p8, const Split& sp,
                                       int x, int stages, bool beside)
 {
-    using C = Cfg8<D>;
-    constexpr int KW = kWarps / RW, NK = KT / KW, NG = NK / 16;
+    using C = Cfg8<D, RW>;
+    constexpr int KT = C::KT, GROUPS = C::GROUPS, KW = kWarps / RW, NK = KT / KW, NG = NK / 16;
     const Args& a = p8.a;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -72,21 +74,22 @@ __device__ __forceinline__ void work8(const CUtensorMap& kmap, const CUtensorMap
     if (!beside) kv::pdl_wait();
     kv::pdl_release();
     if (beside && blockIdx.x == gridDim.x - 1) kv::pdl_wait();
-    const Item it = find_item<KEYS>(a, unit, row_block, part, sp.parts, sp.least_tiles, 16 * RW, threadIdx.x == 0);
+    const Item it = find_item<KEYS, KT>(a, unit, row_block, part, sp.parts, sp.least_tiles, 16 * RW, threadIdx.x == 0);
     if (it.rows == 0) return;
     bool ok = true;
     // keys of tile j that any row sees
     auto tile_keys = [&](int j) { return j < it.np ? min(KT, it.prefix - j * KT) : min(KT, it.own - (j - it.np) * KT); };
 
     if (warp == kWarps) {
-        // ------------------------------------------------ loads: a lane each for the K and the V of 16 keys
-        const int group = lane % kGroups, is_v = lane / kGroups;
-        const bool busy = is_v < 2, boxes = busy && group * 16 % a.box_rows == 0;   // the first lane of a page's rows loads them
+        // ------------------------------------------------ loads: a lane each for the K or the V of 16 keys
+        constexpr int LANES = 2 * GROUPS, BATCH = 32 / LANES;   // of a tile; tiles of a batch
+        const int turn = lane / LANES, group = lane % GROUPS, is_v = lane % LANES / GROUPS;
+        const bool boxes = group * 16 % a.box_rows == 0;        // the first lane of a page's rows loads them
         const int* own_table = (KEYS & kOwn) ? a.bt.table + (long long)it.b * a.bt.table_ld : nullptr;
         const int mask = (1 << a.c.page_shift) - 1, n_prefix = (it.prefix + mask) >> a.c.page_shift;
         auto key_of = [&](int j) { return (j < it.np ? j : j - it.np) * KT + group * 16; };
         auto page_at = [&](int j) -> int {   // page of this lane's keys of tile j; -1: none
-            if (!busy || j >= it.tile1 || group * 16 >= tile_keys(j)) return -1;
+            if (j >= it.tile1 || group * 16 >= tile_keys(j)) return -1;
             return j < it.np ? page_of(a, a.bt.prefix_table, n_prefix, key_of(j) >> a.c.page_shift)
                              : page_of(a, own_table, a.bt.table_ld, key_of(j) >> a.c.page_shift);
         };
@@ -95,32 +98,36 @@ __device__ __forceinline__ void work8(const CUtensorMap& kmap, const CUtensorMap
         };
         int s = 0, issued = 0;
         uint32_t ph = 0;
-        int page = page_at(it.tile0), next = page_at(it.tile0 + 1), e = exp_at(page, it.tile0);
-        for (int j = it.tile0; j < it.tile1; j++) {
-            const int next_e = exp_at(next, j + 1), after = page_at(j + 2);
-            ok = __all_sync(0xffffffffu, ptx::mbar_wait(empty(s), ph ^ 1u));
-            if (!ok) break;
-            if (busy) {
-                float* to = scales + s * (3 * kGroups) + group;
-                if (!is_v) {
-                    to[0] = a.scale_log2 * scale_of(e);
-                } else {
-                    to[kGroups] = (float)e;
-                    to[2 * kGroups] = scale_of(-e);
+        int mine = it.tile0 + turn;   // this lane's tile of the batch
+        int page = page_at(mine), next = page_at(mine + BATCH), e = exp_at(page, mine);
+        for (int j0 = it.tile0; ok && j0 < it.tile1; j0 += BATCH, mine += BATCH) {
+            const int next_e = exp_at(next, mine + BATCH), after = page_at(mine + 2 * BATCH);
+            for (int t = 0; t < BATCH && j0 + t < it.tile1; t++) {
+                const int j = j0 + t;
+                ok = __all_sync(0xffffffffu, ptx::mbar_wait(empty(s), ph ^ 1u));
+                if (!ok) break;
+                if (turn == t) {
+                    float* to = scales + s * C::SCALES + group;
+                    if (!is_v) {
+                        to[0] = a.scale_log2 * scale_of(e);
+                    } else {
+                        to[GROUPS] = (float)e;
+                        to[2 * GROUPS] = scale_of(-e);
+                    }
                 }
+                __syncwarp();
+                const int used = (tile_keys(j) + a.box_rows - 1) / a.box_rows;
+                if (lane == 0) ptx::mbar_expect_tx(full(s), (uint32_t)(used * a.box_rows * (2 * D)));
+                __syncwarp();
+                if (turn == t && boxes && group * 16 < used * a.box_rows)
+                    tma_load_4d(sbase + s * C::STAGE + is_v * C::TILE + group * 16 * D, is_v ? &vmap : &kmap, 0,
+                                key_of(j) & mask, head, page, full(s));
+                issued++;
+                if (++s == stages) { s = 0; ph ^= 1u; }
             }
-            __syncwarp();
-            const int used = (tile_keys(j) + a.box_rows - 1) / a.box_rows;
-            if (lane == 0) ptx::mbar_expect_tx(full(s), (uint32_t)(used * a.box_rows * (2 * D)));
-            __syncwarp();
-            if (boxes && group * 16 < used * a.box_rows)
-                tma_load_4d(sbase + s * C::STAGE + is_v * C::TILE + group * 16 * D, is_v ? &vmap : &kmap, 0, key_of(j) & mask,
-                            head, page, full(s));
             page = next;
             next = after;
             e = next_e;
-            issued++;
-            if (++s == stages) { s = 0; ph ^= 1u; }
         }
         // no copy is in flight when the CTA leaves, not even after a wait that gave up
         for (int i = min(stages, issued); i > 0; i--) {
@@ -229,12 +236,12 @@ __device__ __forceinline__ void work8(const CUtensorMap& kmap, const CUtensorMap
                 }
                 // s + ev of a group: the raw logits times f, plus ev (f at least the smallest normal number: a masked
                 // logit times 0 would be a NaN)
-                const float* stage = scales + s * (3 * kGroups) + k0 / 16;
+                const float* stage = scales + s * C::SCALES + k0 / 16;
                 float f0[NG], f1[NG], ev[NG], t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
                 for (int n = 0; n < NG; n++) {
                     const float k = stage[n];
-                    ev[n] = stage[kGroups + n];
+                    ev[n] = stage[GROUPS + n];
                     f0[n] = fmaxf(k * back0, 1.17549435e-38f);
                     f1[n] = fmaxf(k * back1, 1.17549435e-38f);
                     t0 = fmaxf(t0, fmaf(fmaxf(fmaxf(sc[2 * n][0], sc[2 * n][1]), fmaxf(sc[2 * n + 1][0], sc[2 * n + 1][1])), f0[n], ev[n]));
@@ -269,7 +276,7 @@ __device__ __forceinline__ void work8(const CUtensorMap& kmap, const CUtensorMap
                         p[2 * e + 1] = exp2_approx(fmaf(sc[2 * n + e / 2][2 * (e % 2) + 1], e % 2 ? f1[n] : f0[n], ev[n] - (e % 2 ? u1 : u0)));
                         pf[n][e] = kv::pack2<__half>(p[2 * e], p[2 * e + 1]);
                     }
-                    const float iv = stage[2 * kGroups + n];
+                    const float iv = stage[2 * GROUPS + n];
                     l0 = fmaf((p[0] + p[1]) + (p[4] + p[5]), iv, l0);
                     l1 = fmaf((p[2] + p[3]) + (p[6] + p[7]), iv, l1);
                 }
@@ -379,15 +386,19 @@ template <int D, int RWP, int RWO>
 __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3)
     k_attn8_rows_shared(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                         const __grid_constant__ Args8 p, const __grid_constant__ Split prefix,
-                        const __grid_constant__ Split own, int prefix_ctas, int stages)
+                        const __grid_constant__ Split own, int prefix_ctas, int prefix_stages, int own_stages)
 {
-    if ((int)blockIdx.x < prefix_ctas) work8<D, RWP, kPrefix>(kmap, vmap, p, prefix, blockIdx.x, stages, false);
-    else work8<D, RWO, kOwn>(kmap, vmap, p, own, (int)blockIdx.x - prefix_ctas, stages, false);
+    if ((int)blockIdx.x < prefix_ctas) work8<D, RWP, kPrefix>(kmap, vmap, p, prefix, blockIdx.x, prefix_stages, false);
+    else work8<D, RWO, kOwn>(kmap, vmap, p, own, (int)blockIdx.x - prefix_ctas, own_stages, false);
 }
 
-// No more stages than tiles: more of the shared memory stays with the kernel beside.
-template <int D> int stages_for(int tiles) { return std::max(1, std::min(tiles, Cfg8<D>::MAX_STAGES)); }
-template <int D> int smem_for(int stages) { return stages * Cfg8<D>::STAGE + Cfg8<D>::REST; }
+// Shared memory of a CTA for parts of so many 64-key tiles: no more stages than it has use for, so that more stays with
+// the kernel beside.
+template <int D, int RW> int stages_for(int tiles)
+{
+    return std::max(1, std::min((int)ceil_div(tiles, kKeys<RW> / 64), Cfg8<D, RW>::MAX_STAGES));
+}
+template <int D, int RW> int smem_for(int stages) { return stages * Cfg8<D, RW>::STAGE + Cfg8<D, RW>::REST; }
 
 template <int D, int RW, int KEYS>
 cudaError_t launch_one(const Args8& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int part0, int parts,
@@ -395,12 +406,12 @@ cudaError_t launch_one(const Args8& p, const CUtensorMap& kmap, const CUtensorMa
 {
     auto kernel = k_attn8_rows<D, RW, KEYS>;
     static std::atomic<unsigned long long> done{0};
-    const cudaError_t e = kv::allow_smem(kernel, smem_for<D>(Cfg8<D>::MAX_STAGES), done);
+    const cudaError_t e = kv::allow_smem(kernel, smem_for<D, RW>(Cfg8<D, RW>::MAX_STAGES), done);
     if (e != cudaSuccess) return e;
-    const Launch l = plan(p.a, KEYS, RW, part0, parts, most_tiles, beside);
+    const Launch l = plan(p.a, KEYS, RW, part0, parts, most_tiles, beside, kKeys<RW>);
     if (l.ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    const int stages = stages_for<D>(most_tiles);
-    return kv::launch_dependent(kernel, dim3((unsigned)l.ctas), kThreads, smem_for<D>(stages), s, kmap, vmap, p, l.sp,
+    const int stages = stages_for<D, RW>(most_tiles);
+    return kv::launch_dependent(kernel, dim3((unsigned)l.ctas), kThreads, smem_for<D, RW>(stages), s, kmap, vmap, p, l.sp,
                                 stages, beside ? 1 : 0);
 }
 
@@ -409,14 +420,16 @@ cudaError_t launch_both(const Args8& p, const CUtensorMap& kmap, const CUtensorM
 {
     auto kernel = k_attn8_rows_shared<D, RWP, RWO>;
     static std::atomic<unsigned long long> done{0};
-    const cudaError_t e = kv::allow_smem(kernel, smem_for<D>(Cfg8<D>::MAX_STAGES), done);
+    const cudaError_t e = kv::allow_smem(kernel, std::max(smem_for<D, RWP>(Cfg8<D, RWP>::MAX_STAGES),
+                                                          smem_for<D, RWO>(Cfg8<D, RWO>::MAX_STAGES)), done);
     if (e != cudaSuccess) return e;
-    const Launch l = plan(p.a, kPrefix, RWP, 0, n.prefix_parts, n.prefix_tiles);
-    const Launch m = plan(p.a, kOwn, RWO, n.prefix_parts, n.own_parts, n.own_tiles);
+    const Launch l = plan(p.a, kPrefix, RWP, 0, n.prefix_parts, n.prefix_tiles, false, kKeys<RWP>);
+    const Launch m = plan(p.a, kOwn, RWO, n.prefix_parts, n.own_parts, n.own_tiles, false, kKeys<RWO>);
     if (l.ctas + m.ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    const int stages = stages_for<D>(std::max(n.prefix_tiles, n.own_tiles));
-    return kv::launch_dependent(kernel, dim3((unsigned)(l.ctas + m.ctas)), kThreads, smem_for<D>(stages), s, kmap, vmap, p,
-                                l.sp, m.sp, (int)l.ctas, stages);
+    const int ps = stages_for<D, RWP>(n.prefix_tiles), os = stages_for<D, RWO>(n.own_tiles);
+    const int smem = std::max(smem_for<D, RWP>(ps), smem_for<D, RWO>(os));
+    return kv::launch_dependent(kernel, dim3((unsigned)(l.ctas + m.ctas)), kThreads, smem, s, kmap, vmap, p, l.sp, m.sp,
+                                (int)l.ctas, ps, os);
 }
 
 template <int D>

@@ -77,7 +77,7 @@ __device__ __forceinline__ void work(const CUtensorMap& kmap, const CUtensorMap&
     if (!beside) kv::pdl_wait();
     kv::pdl_release();
     if (beside && blockIdx.x == gridDim.x - 1) kv::pdl_wait();
-    const Item it = find_item<KEYS>(a, unit, row_block, part, sp.parts, sp.least_tiles, 16 * RW, threadIdx.x == 0);
+    const Item it = find_item<KEYS, KT>(a, unit, row_block, part, sp.parts, sp.least_tiles, 16 * RW, threadIdx.x == 0);
     if (it.rows == 0) return;
     bool ok = true;
     // keys of tile j that any row sees

@@ -11,7 +11,7 @@ namespace qg {
 namespace attn {
 namespace {
 
-constexpr int KT = 64;                       // keys of a stage
+constexpr int KT = 64;                       // keys of a stage of the 16-bit kernel
 constexpr int kWarps = 4;                    // consumer warps; warp 4 issues the loads
 constexpr int kThreads = (kWarps + 1) * 32;
 
@@ -53,7 +53,7 @@ struct Item {
     int tile0, tile1;   // this part's tiles
 };
 
-template <int KEYS>
+template <int KEYS, int TILE>   // TILE: keys of a tile
 __device__ __forceinline__ Item find_item(const Args& a, int unit, int row_block, int part, int parts, int least_tiles,
                                           int rows_cap, bool tell)
 {
@@ -79,8 +79,8 @@ __device__ __forceinline__ Item find_item(const Args& a, int unit, int row_block
     }
     if (!ok && tell) kv::report(a.status);
     it.prefix = (KEYS & kPrefix) ? a.bt.prefix_len : 0;
-    it.np = (it.prefix + KT - 1) / KT;
-    const int tiles = it.rows > 0 ? it.np + (it.own + KT - 1) / KT : 0;
+    it.np = (it.prefix + TILE - 1) / TILE;
+    const int tiles = it.rows > 0 ? it.np + (it.own + TILE - 1) / TILE : 0;
     const int per = max(least_tiles, (tiles + parts - 1) / parts);
     it.tile0 = min(part * per, tiles);
     it.tile1 = min(it.tile0 + per, tiles);
@@ -99,11 +99,12 @@ struct Launch {
     Split sp;
     int64_t ctas;
 };
-Launch plan(const Args& a, int keys, int rw, int part0, int parts, int most_tiles, bool beside = false)
+// most_tiles: of 64 keys, of a part; tile: keys of the kernel's tiles.
+Launch plan(const Args& a, int keys, int rw, int part0, int parts, int most_tiles, bool beside = false, int tile = KT)
 {
     const int64_t units = (keys & kOwn) ? a.bt.B : 1;
     const int64_t blocks = ceil_div((int64_t)a.group * ((keys & kOwn) ? a.bt.max_q : a.bt.T), 16 * rw);
-    const int least = std::min(beside ? kLeastBeside : kLeastTiles, most_tiles);
+    const int least = (int)ceil_div(std::min(beside ? kLeastBeside : kLeastTiles, most_tiles), tile / 64);
     return Launch{Split{part0, parts, least, (int)blocks}, units * blocks * parts * a.c.heads};
 }
 
