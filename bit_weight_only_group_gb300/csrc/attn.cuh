@@ -55,15 +55,28 @@ struct Args8 {
     long long scale_page, scale_block, scale_head;
     int q_type;
 };
-// Exponent of the scale of a K or V block (a byte outside 1 .. 254 is none the appending kernel wrote).
-__device__ __forceinline__ int scale_exp_at(const Args8& p, bool v, int page, int block, int head)
+// Scales are looked up in two steps, the page of 16 keys and the byte there, each some rounds ahead of its use.  What was
+// loaded is first looked at where it is used: a comparison right after the load would wait for it.
+constexpr int kNoPage = -0x7FFFFFFF;   // no keys to look up
+// Entry e of a table of n entries.
+__device__ __forceinline__ int page_entry(const int* table, int n, int e) { return e < n ? __ldg(table + e) : -1; }
+// The page such an entry names; num_pages where it is not to be followed, -1 where there was none to look up.
+__device__ __forceinline__ int checked_page(const Args& a, int entry)
+{
+    if (entry >= 0 && entry < a.c.num_pages) return entry;
+    if (entry == kNoPage) return -1;
+    kv::report(a.status);
+    return a.c.num_pages;
+}
+// Byte of the scale of a K or V block in a checked page (2^0 where there is none).
+__device__ __forceinline__ int scale_byte(const Args8& p, bool v, int page, int block, int head)
 {
     const uint8_t* s = (v ? p.v_scale : p.k_scale) + (long long)page * p.scale_page + (long long)block * p.scale_block +
                        (long long)head * p.scale_head;
-    return min(max((int)__ldg(s), 1), 254) - kv8::kBias;
+    return page >= 0 && page < p.a.c.num_pages ? (int)__ldg(s) : kv8::kBias;
 }
-// 2^n and 2^-n of such an exponent.
-__device__ __forceinline__ float scale_of(int e) { return kv8::pow2(e); }
+// Its exponent (a byte outside 1 .. 254 is none the appending kernel wrote).
+__device__ __forceinline__ int scale_exp(int byte) { return min(max(byte, 1), 254) - kv8::kBias; }
 // The power of two 2^x that brings a row with the largest magnitude amax to 2^14 .. 2^15 is 2^(14 - x).
 __device__ __forceinline__ int row_exp(float amax) { return max((int)(__float_as_uint(amax) >> 23) - 127, -100); }
 

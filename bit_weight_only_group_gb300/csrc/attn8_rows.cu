@@ -88,20 +88,20 @@ __device__ __forceinline__ void work8(const CUtensorMap& kmap, const CUtensorMap
         const int* own_table = (KEYS & kOwn) ? a.bt.table + (long long)it.b * a.bt.table_ld : nullptr;
         const int mask = (1 << a.c.page_shift) - 1, n_prefix = (it.prefix + mask) >> a.c.page_shift;
         auto key_of = [&](int j) { return (j < it.np ? j : j - it.np) * KT + group * 16; };
-        auto page_at = [&](int j) -> int {   // page of this lane's keys of tile j; -1: none
-            if (j >= it.tile1 || group * 16 >= tile_keys(j)) return -1;
-            return j < it.np ? page_of(a, a.bt.prefix_table, n_prefix, key_of(j) >> a.c.page_shift)
-                             : page_of(a, own_table, a.bt.table_ld, key_of(j) >> a.c.page_shift);
+        auto entry_at = [&](int j) -> int {   // of the table, for this lane's keys of tile j
+            if (j >= it.tile1 || group * 16 >= tile_keys(j)) return kNoPage;
+            return j < it.np ? page_entry(a.bt.prefix_table, n_prefix, key_of(j) >> a.c.page_shift)
+                             : page_entry(own_table, a.bt.table_ld, key_of(j) >> a.c.page_shift);
         };
-        auto exp_at = [&](int page, int j) -> int {
-            return page >= 0 && page < a.c.num_pages ? scale_exp_at(p8, is_v != 0, page, (key_of(j) & mask) / 16, head) : 0;
-        };
+        auto byte_at = [&](int page, int j) { return scale_byte(p8, is_v != 0, page, (key_of(j) & mask) / 16, head); };
         int s = 0, issued = 0;
         uint32_t ph = 0;
         int mine = it.tile0 + turn;   // this lane's tile of the batch
-        int page = page_at(mine), next = page_at(mine + BATCH), e = exp_at(page, mine);
+        int page = checked_page(a, entry_at(mine)), next = entry_at(mine + BATCH), byte = byte_at(page, mine);
         for (int j0 = it.tile0; ok && j0 < it.tile1; j0 += BATCH, mine += BATCH) {
-            const int next_e = exp_at(next, mine + BATCH), after = page_at(mine + 2 * BATCH);
+            const int next_page = checked_page(a, next), next_byte = byte_at(next_page, mine + BATCH);
+            const int e = scale_exp(byte);
+            next = entry_at(mine + 2 * BATCH);
             for (int t = 0; t < BATCH && j0 + t < it.tile1; t++) {
                 const int j = j0 + t;
                 ok = __all_sync(0xffffffffu, ptx::mbar_wait(empty(s), ph ^ 1u));
@@ -109,10 +109,10 @@ __device__ __forceinline__ void work8(const CUtensorMap& kmap, const CUtensorMap
                 if (turn == t) {
                     float* to = scales + s * C::SCALES + group;
                     if (!is_v) {
-                        to[0] = a.scale_log2 * scale_of(e);
+                        to[0] = a.scale_log2 * kv8::pow2(e);
                     } else {
                         to[GROUPS] = (float)e;
-                        to[2 * GROUPS] = scale_of(-e);
+                        to[2 * GROUPS] = kv8::pow2(-e);
                     }
                 }
                 __syncwarp();
@@ -125,9 +125,8 @@ __device__ __forceinline__ void work8(const CUtensorMap& kmap, const CUtensorMap
                 issued++;
                 if (++s == stages) { s = 0; ph ^= 1u; }
             }
-            page = next;
-            next = after;
-            e = next_e;
+            page = next_page;
+            byte = next_byte;
         }
         // no copy is in flight when the CTA leaves, not even after a wait that gave up
         for (int i = min(stages, issued); i > 0; i--) {

@@ -3,13 +3,14 @@
 // blocks of 128 keys, two streams, P back through tensor memory, the work dealt
 // the same way) with codes in place of 16-bit values.
 //
-// The tensor core takes fp16.  Three warps load codes from their pages straight
+// The tensor core takes fp16.  Four warps load codes from their pages straight
 // into registers, half the bytes of 16-bit values, turn them into fp16, two an
 // instruction, and store them where TMA would have put the 16-bit block; a block
-// and its conversion serve both tiles (256 rows).  A task is 16 keys of a K or V
-// block, one page and one run of rows; the warps take tasks in turn and each has
-// several in flight.  The softmax's warps scale the rows of q by powers of two
-// and store them as fp16 at the start of an item, when they would wait for S.
+// and its conversion serve both tiles (256 rows).  A warp has two runs of 16 keys
+// of each K or V block, each in one page, and fetches the next block's into the
+// registers of a run as soon as that is stored.  The softmax's warps scale the
+// rows of q by powers of two and store them as fp16 at the start of an item, when
+// they would wait for S.
 // The scales do not touch the operands: the softmax multiplies the logits of 16
 // keys by the K scale (in the fused product that its argument takes anyway) and
 // adds the V scale's exponent to that argument (attn.cuh), so an element costs
@@ -19,7 +20,8 @@
 // bits): the same tensor-core time as fp16, while P's split costs the softmax
 // four conversions a pair, which run at 16 to 32 a clock (measured: 21 to E4M3).
 //
-// Warps: 0-3 softmax of stream 0, 4-7 of stream 1, 8-10 codes, 11 the products.
+// Warps: 0-3 softmax of stream 0, 4-7 of stream 1, 8-11 codes, 12 the products
+// (13-15 only fill the fourth warpgroup).
 #include <algorithm>
 
 #include "attn_tiles.cuh"
@@ -28,11 +30,11 @@ namespace qg {
 namespace attn {
 namespace {
 
-constexpr int kWarpConvert = 8, kConverters = 3, kWarpMma = 11;
-constexpr int kThreads = 384;
-// Registers of a thread: 168 at launch (65536 over 384), then shared out by warpgroup.
-constexpr int kRegsLaunch = 168, kRegsSoftmax = 192, kRegsOther = 120;
-static_assert(2 * kRegsSoftmax + kRegsOther == 3 * kRegsLaunch, "registers shared out are those of the launch");
+constexpr int kWarpConvert = 8, kWarpMma = 12;
+constexpr int kThreads = 512;
+// Registers of a thread: 128 at launch (65536 over 512), then shared out by warpgroup.
+constexpr int kRegsLaunch = 128, kRegsSoftmax = 192, kRegsConvert = 80, kRegsMma = 48;
+static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsMma == 4 * kRegsLaunch, "registers shared out are those of the launch");
 
 template <int D> struct Cfg {
     static constexpr int HALVES = D / 64;
@@ -45,10 +47,9 @@ template <int D> struct Cfg {
     static constexpr int OFF_BACK = OFF_ML + 128 * 8;      // what stream 0 scaled its rows of Q by, for stream 1
     static constexpr int SMEM = OFF_BACK + 128;
     static_assert(SMEM <= 227 * 1024, "shared memory");
-    // a task of the converting warps: 16 keys, LANES lanes a key with 16 codes each, CHUNKS times ROWS keys; tasks in flight
-    static constexpr int LANES = D / 16, ROWS = 32 / LANES, CHUNKS = 16 / ROWS, DEPTH = D == 128 ? 4 : 6;
+    // 16 keys of a converting warp: LANES lanes a key with 16 codes each, CHUNKS times ROWS keys; blocks in flight
+    static constexpr int LANES = D / 16, ROWS = 32 / LANES, CHUNKS = 16 / ROWS, DEPTH = D == 128 ? 1 : 2;
 };
-constexpr int kTasks = KB / 16;   // of a block
 
 template <int D, int KEYS>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -87,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_init(join_full, 4);
         ptx::mbar_init(join_empty, 4);
         ptx::mbar_init(back_full, 4);
-        for (int x = 0; x < NS; x++) { ptx::mbar_init(kv_full(x), kTasks); ptx::mbar_init(kv_empty(x), 1); }
+        for (int x = 0; x < NS; x++) { ptx::mbar_init(kv_full(x), 4); ptx::mbar_init(kv_empty(x), 1); }
         ptx::fence_mbar_init();
     }
     if (warp == kWarpMma) {
@@ -120,86 +121,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int per = (KEYS & kOwn) ? lay.per : deal.per;   // tokens of a tile
     const int in_page_mask = (1 << a.c.page_shift) - 1;
 
-    // Keys of a block of the item that any row sees, the first key's place, and the page of 16 of them (-1: none are seen).
+    // Keys of a block of the item that any row sees, the first key's place, and the table's entry for 16 of them.
     auto keys_of = [&](int blk) { return blk < it.np ? min(KB, it.prefix - blk * KB) : max(0, min(KB, it.own - (blk - it.np) * KB)); };
     auto key_of = [&](int blk, int group) { return (blk < it.np ? blk : blk - it.np) * KB + 16 * group; };
-    auto page_at = [&](int blk, int group) -> int {
-        if (blk >= it.blk1 || 16 * group >= keys_of(blk)) return -1;
+    auto entry_at = [&](int blk, int group) -> int {
+        if (blk >= it.blk1 || 16 * group >= keys_of(blk)) return kNoPage;
         const int e = key_of(blk, group) >> a.c.page_shift;
-        if (!(KEYS & kOwn) || blk < it.np) return page_of(a, a.bt.prefix_table, (it.prefix + in_page_mask) >> a.c.page_shift, e);
-        return page_of(a, a.bt.table + (long long)it.b * a.bt.table_ld, a.bt.table_ld, e);
+        if (!(KEYS & kOwn) || blk < it.np) return page_entry(a.bt.prefix_table, (it.prefix + in_page_mask) >> a.c.page_shift, e);
+        return page_entry(a.bt.table + (long long)it.b * a.bt.table_ld, a.bt.table_ld, e);
     };
 
-    if (warp >= kWarpConvert) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-        if (warp < kWarpMma) {
-            // ------------------------------------------------ codes to fp16
-            const int row0 = lane / C::LANES, chunk = lane % C::LANES;   // keys row0 + c ROWS of a task, codes 16 chunk ..
-            int base = 0;                                                // ring position of the item's first load
-            while (ok && next_item<KEYS>(a, deal, lay, cur, it)) {
-                const int n = it.blk1 - it.blk0, loads = 2 * n, tasks = loads * kTasks;
-                // load number i, in the order K0, K1 V0, K2 V1, .. : whether it is V, and its block
-                auto is_v = [&](int i) { return i != 0 && (!(i & 1) || i == loads - 1); };
-                auto block = [&](int i) { return it.blk0 + (i == loads - 1 ? n - 1 : i == 0 ? 0 : i & 1 ? (i + 1) / 2 : i / 2 - 1); };
-                auto find = [&](int t) { return t < tasks ? page_at(block(t / kTasks), t % kTasks) : -1; };
-                auto fetch = [&](int t, int page, uint4 (&w)[C::CHUNKS]) {
-                    // keys past the last, and pages not to be followed, are zeros
-#pragma unroll
-                    for (int c = 0; c < C::CHUNKS; c++) w[c] = make_uint4(0u, 0u, 0u, 0u);
-                    if (page < 0 || page >= a.c.num_pages) return;
-                    const int i = t / kTasks, g = t % kTasks, blk = block(i), left = keys_of(blk) - 16 * g;
-                    const uint8_t* from = (is_v(i) ? p8.v_codes : p8.k_codes) + (long long)page * a.c.page_stride +
-                                          (long long)((key_of(blk, g) & in_page_mask) + row0) * a.c.token_stride +
-                                          (long long)it.head * a.c.head_stride + 16 * chunk;
-#pragma unroll
-                    for (int c = 0; c < C::CHUNKS; c++)
-                        if (row0 + c * C::ROWS < left)
-                            w[c] = __ldg(reinterpret_cast<const uint4*>(from + (long long)(c * C::ROWS) * a.c.token_stride));
-                };
-                auto convert = [&](int t, const uint4 (&w)[C::CHUNKS]) -> bool {
-                    const int pos = base + t / kTasks, x = pos % NS;
-                    if (!__all_sync(0xffffffffu, ptx::mbar_wait(kv_empty(x), ((pos / NS) & 1) ^ 1u))) return false;
-                    // the lanes of a row's second half store their later 16 bytes first: eight lanes then meet all banks
-                    const int flip = chunk / 4;
-                    unsigned char* slot = smem + C::OFF_KV + x * C::TILE + flip * C::HALF + (t % kTasks) * (16 * 128);
-#pragma unroll
-                    for (int c = 0; c < C::CHUNKS; c++) {
-                        const int row = row0 + c * C::ROWS;
-                        const uint4 lo = make_uint4(kv8::decode_lo(w[c].x), kv8::decode_hi(w[c].x), kv8::decode_lo(w[c].y), kv8::decode_hi(w[c].y));
-                        const uint4 hi = make_uint4(kv8::decode_lo(w[c].z), kv8::decode_hi(w[c].z), kv8::decode_lo(w[c].w), kv8::decode_hi(w[c].w));
-                        const int c0 = (2 * (chunk % 4) + flip) ^ (row & 7);
-                        *reinterpret_cast<uint4*>(slot + row * 128 + 16 * c0) = flip ? hi : lo;
-                        *reinterpret_cast<uint4*>(slot + row * 128 + 16 * (c0 ^ 1)) = flip ? lo : hi;
-                    }
-                    ptx::fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(kv_full(x));
-                    return true;
-                };
-                // a buffer's task, the page of the one after it
-                uint4 w[C::DEPTH][C::CHUNKS];
-                int page[C::DEPTH], t = warp - kWarpConvert;
-                constexpr int ROUND = C::DEPTH * kConverters;
-#pragma unroll
-                for (int d = 0; d < C::DEPTH; d++) page[d] = find(t + d * kConverters);
-#pragma unroll
-                for (int d = 0; d < C::DEPTH; d++) {
-                    fetch(t + d * kConverters, page[d], w[d]);
-                    page[d] = find(t + d * kConverters + ROUND);
-                }
-                for (; ok && t < tasks; t += ROUND) {
-#pragma unroll
-                    for (int d = 0; d < C::DEPTH; d++) {
-                        const int mine = t + d * kConverters;
-                        if (!ok || mine >= tasks) break;
-                        ok = convert(mine, w[d]);
-                        fetch(mine + ROUND, page[d], w[d]);
-                        page[d] = find(mine + 2 * ROUND);
-                    }
-                }
-                base += loads;
-            }
-        } else if (elect_lane()) {
+    if (warp >= kWarpMma) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
+        if (warp == kWarpMma && elect_lane()) {
             // ------------------------------------------------ matrix products, by one lane
             constexpr uint32_t id_qk = idesc<__half>(KB, false), id_pv = idesc<__half>(D, true);
             uint32_t item_phase = 0, p_phase[2] = {0, 0};
@@ -281,6 +215,90 @@ __global__ void __launch_bounds__(kThreads, 1)
             commit(products_done);
             ok = ptx::mbar_wait(products_done, 0) && ok;
         }
+    } else if (warp >= kWarpConvert) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
+        // ------------------------------------------------ codes to fp16: keys 16 w .. and 16 (w + 4) .. of a block
+        const int w = warp - kWarpConvert, row0 = lane / C::LANES, chunk = lane % C::LANES;   // keys row0 + c ROWS, codes 16 chunk ..
+        // where in a slot: the lanes of a row's second half store their later 16 bytes first, so that eight lanes meet all banks
+        const int flip = chunk / 4;
+        uint32_t to[2];   // of rows row0 + c ROWS for even, odd c
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+            const int row = row0 + c * C::ROWS;
+            to[c] = (uint32_t)(flip * C::HALF + (16 * w + row) * 128 + 16 * ((2 * (chunk % 4) + flip) ^ (row & 7)));
+        }
+        const int group = w + 4 * (lane & 1);   // the keys whose page this lane looks up
+        const long long hop = (long long)C::ROWS * a.c.token_stride;
+        int slot = 0;
+        uint32_t round = 1;   // parity of the wait for a free slot
+        while (ok && next_item<KEYS>(a, deal, lay, cur, it)) {
+            const int n = it.blk1 - it.blk0, loads = 2 * n;
+            const long long mine = (long long)it.head * a.c.head_stride + (long long)row0 * a.c.token_stride + 16 * chunk;
+            // where this lane's 16 keys of a block begin among the codes: of the last block K was loaded for, and the one before;
+            // -1: nothing there to load.  The next one's entry of the table is on its way.
+            long long now = -1, before = -1;
+            int entry = entry_at(it.blk0, group);
+            uint4 raw[C::DEPTH][2][C::CHUNKS];
+            // load number i, in the order K0, K1 V0, K2 V1, ..
+            struct Load { const uint8_t* from; long long at; int left; };
+            auto next_load = [&](int i) -> Load {
+                const bool v = i != 0 && (!(i & 1) || i == loads - 1);
+                const int blk = it.blk0 + (i == loads - 1 ? n - 1 : i == 0 ? 0 : i & 1 ? (i + 1) / 2 : i / 2 - 1);
+                if (!v) {
+                    const int page = checked_page(a, entry);
+                    before = now;
+                    now = page >= 0 && page < a.c.num_pages
+                              ? (long long)page * a.c.page_stride + (long long)(key_of(blk, group) & in_page_mask) * a.c.token_stride : -1;
+                    entry = entry_at(blk + 1, group);
+                }
+                return Load{v ? p8.v_codes : p8.k_codes, !v || i == loads - 1 ? now : before, keys_of(blk) - 16 * w - row0};
+            };
+            auto fetch = [&](const Load& l, auto half, uint4 (&r)[C::CHUNKS]) {
+                const long long at = __shfl_sync(0xffffffffu, l.at, half.value);
+                const uint8_t* p = l.from + at + mine;
+#pragma unroll
+                for (int c = 0; c < C::CHUNKS; c++) {
+                    // keys past the last, and pages not to be followed, are zeros
+                    r[c] = make_uint4(0u, 0u, 0u, 0u);
+                    if (at >= 0 && 64 * half.value + c * C::ROWS < l.left) r[c] = __ldg(reinterpret_cast<const uint4*>(p + c * hop));
+                }
+            };
+            auto store = [&](unsigned char* into, auto half, const uint4 (&r)[C::CHUNKS]) {
+#pragma unroll
+                for (int c = 0; c < C::CHUNKS; c++) {
+                    const uint4 lo = make_uint4(kv8::decode_lo(r[c].x), kv8::decode_hi(r[c].x), kv8::decode_lo(r[c].y), kv8::decode_hi(r[c].y));
+                    const uint4 hi = make_uint4(kv8::decode_lo(r[c].z), kv8::decode_hi(r[c].z), kv8::decode_lo(r[c].w), kv8::decode_hi(r[c].w));
+                    const uint32_t at = to[c & 1] + (64 * half.value + (c & ~1) * C::ROWS) * 128;
+                    *reinterpret_cast<uint4*>(into + at) = flip ? hi : lo;
+                    *reinterpret_cast<uint4*>(into + (at ^ 16)) = flip ? lo : hi;
+                }
+            };
+#pragma unroll
+            for (int d = 0; d < C::DEPTH; d++) {
+                const Load l = d < loads ? next_load(d) : Load{p8.k_codes, -1, 0};
+                fetch(l, Const<0>{}, raw[d][0]);
+                fetch(l, Const<1>{}, raw[d][1]);
+            }
+            for (int i0 = 0; ok && i0 < loads; i0 += C::DEPTH) {
+#pragma unroll
+                for (int d = 0; d < C::DEPTH; d++) {
+                    const int i = i0 + d;
+                    if (!ok || i >= loads) break;
+                    const Load l = i + C::DEPTH < loads ? next_load(i + C::DEPTH) : Load{p8.k_codes, -1, 0};
+                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(kv_empty(slot), round));
+                    if (!ok) break;
+                    unsigned char* into = smem + C::OFF_KV + slot * C::TILE;
+                    store(into, Const<0>{}, raw[d][0]);
+                    fetch(l, Const<0>{}, raw[d][0]);
+                    store(into, Const<1>{}, raw[d][1]);
+                    ptx::fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(kv_full(slot));
+                    fetch(l, Const<1>{}, raw[d][1]);
+                    if (++slot == NS) { slot = 0; round ^= 1u; }
+                }
+            }
+        }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         // ------------------------------------------------ softmax, a row a thread
@@ -292,10 +310,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t s_phase = 0, o_phase = 0, join_phase = 0, item_phase = 0;
         // lanes 0-7 hold the K scales of a block's 16s of keys, 8-15 the V scales' exponents, 16-23 those scales' reciprocals
         const int group = lane % 8;
-        auto scale_at = [&](int page, int blk) -> float {
-            const int e = page >= 0 && page < a.c.num_pages
-                              ? scale_exp_at(p8, lane >= 8, page, (key_of(blk, group) & in_page_mask) / 16, it.head) : 0;
-            return lane < 8 ? scale_of(e) : lane < 16 ? (float)e : scale_of(-e);
+        auto byte_at = [&](int entry, int blk) {
+            return scale_byte(p8, lane >= 8, checked_page(a, entry), (key_of(blk, group) & in_page_mask) / 16, it.head);
+        };
+        auto scale_of = [&](int byte) {
+            const int e = scale_exp(byte);
+            return lane < 8 ? kv8::pow2(e) : lane < 16 ? (float)e : kv8::pow2(-e);
         };
         for (; ok && next_item<KEYS>(a, deal, lay, cur, it); item_phase ^= 1u) {
             const int n = it.blk1 - it.blk0, step = it.two ? 1 : 2;
@@ -303,9 +323,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool in = tok_in_tile < per && tok < it.t1;
             float m = -INFINITY, l = 0.0f;
             const int first = it.two ? 0 : s;
-            // pages two blocks ahead, scales one
-            int page = page_at(it.blk0 + first, group), page_next = page_at(it.blk0 + first + step, group);
-            float scale = scale_at(page, it.blk0 + first);
+            // the table's entries two blocks ahead, scales one
+            int entry = entry_at(it.blk0 + first, group), entry_next = entry_at(it.blk0 + first + step, group);
+            int byte = byte_at(entry, it.blk0 + first);
+            float scale = 0.0f;
             // ------------------------------------------------ the warp's 32 rows of Q; row r's is scaled by 2^-back
             int back = 0;
             if (it.two || s == 0) {
@@ -367,8 +388,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = first; j < n; j += step) {
                 const int blk = it.blk0 + j;
                 const int vis = blk < it.np ? it.prefix - blk * KB : it.own0 + (tok - it.t0) - (blk - it.np) * KB;
-                const float scale_next = scale_at(page_next, blk + step);
-                page_next = page_at(blk + 2 * step, group);
+                scale = scale_of(byte);
+                byte = byte_at(entry_next, blk + step);
+                entry_next = entry_at(blk + 2 * step, group);
                 ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full(s), s_phase));
                 s_phase ^= 1u;
                 if (!ok) break;
@@ -443,7 +465,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(p_full(s, h));
                 }
-                scale = scale_next;
             }
             if (!ok) break;
             // ------------------------------------------------ the item's rows
