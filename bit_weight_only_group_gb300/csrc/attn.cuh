@@ -55,25 +55,31 @@ struct Args8 {
     long long scale_page, scale_block, scale_head;
     int q_type;
 };
-// Scales are looked up in two steps, the page of 16 keys and the byte there, each some rounds ahead of its use.  What was
-// loaded is first looked at where it is used: a comparison right after the load would wait for it.
-constexpr int kNoPage = -0x7FFFFFFF;   // no keys to look up
-// Entry e of a table of n entries.
-__device__ __forceinline__ int page_entry(const int* table, int n, int e) { return e < n ? __ldg(table + e) : -1; }
-// The page such an entry names; num_pages where it is not to be followed, -1 where there was none to look up.
-__device__ __forceinline__ int checked_page(const Args& a, int entry)
+// Scales are looked up in two steps, the page of 16 keys and the byte there, each some rounds ahead of its use.  Both are
+// loaded whether there is something to look up or not (from a place that is there), and first looked at where they are
+// used: a choice or a comparison after the load would wait for it.
+struct Entry {
+    int page;      // as the table has it
+    bool there;    // there are keys to look up
+};
+// Entry e of a table (lengths are cut to bounds that the host has checked against the tables).
+__device__ __forceinline__ Entry table_entry(const Args& a, const int* table, int e, bool there)
 {
-    if (entry >= 0 && entry < a.c.num_pages) return entry;
-    if (entry == kNoPage) return -1;
+    return Entry{__ldg(there ? table + e : a.bt.kv_len), there};
+}
+// The page an entry names; num_pages where it is not to be followed, -1 where there was none to look up.
+__device__ __forceinline__ int checked_page(const Args& a, const Entry& e)
+{
+    if (!e.there) return -1;
+    if (e.page >= 0 && e.page < a.c.num_pages) return e.page;
     kv::report(a.status);
     return a.c.num_pages;
 }
-// Byte of the scale of a K or V block in a checked page (2^0 where there is none).
+// Byte of the scale of a K or V block in a checked page; any block's where there is none (its keys count for nothing).
 __device__ __forceinline__ int scale_byte(const Args8& p, bool v, int page, int block, int head)
 {
-    const uint8_t* s = (v ? p.v_scale : p.k_scale) + (long long)page * p.scale_page + (long long)block * p.scale_block +
-                       (long long)head * p.scale_head;
-    return page >= 0 && page < p.a.c.num_pages ? (int)__ldg(s) : kv8::kBias;
+    const long long at = (long long)page * p.scale_page + (long long)block * p.scale_block + (long long)head * p.scale_head;
+    return (int)__ldg((v ? p.v_scale : p.k_scale) + (page >= 0 && page < p.a.c.num_pages ? at : 0));
 }
 // Its exponent (a byte outside 1 .. 254 is none the appending kernel wrote).
 __device__ __forceinline__ int scale_exp(int byte) { return min(max(byte, 1), 254) - kv8::kBias; }

@@ -86,18 +86,18 @@ __device__ __forceinline__ void work8(const CUtensorMap& kmap, const CUtensorMap
         const int turn = lane / LANES, group = lane % GROUPS, is_v = lane % LANES / GROUPS;
         const bool boxes = group * 16 % a.box_rows == 0;        // the first lane of a page's rows loads them
         const int* own_table = (KEYS & kOwn) ? a.bt.table + (long long)it.b * a.bt.table_ld : nullptr;
-        const int mask = (1 << a.c.page_shift) - 1, n_prefix = (it.prefix + mask) >> a.c.page_shift;
+        const int mask = (1 << a.c.page_shift) - 1;
         auto key_of = [&](int j) { return (j < it.np ? j : j - it.np) * KT + group * 16; };
-        auto entry_at = [&](int j) -> int {   // of the table, for this lane's keys of tile j
-            if (j >= it.tile1 || group * 16 >= tile_keys(j)) return kNoPage;
-            return j < it.np ? page_entry(a.bt.prefix_table, n_prefix, key_of(j) >> a.c.page_shift)
-                             : page_entry(own_table, a.bt.table_ld, key_of(j) >> a.c.page_shift);
+        auto entry_at = [&](int j) {   // of the table, for this lane's keys of tile j
+            const bool there = j < it.tile1 && group * 16 < tile_keys(j);
+            return table_entry(a, j < it.np ? a.bt.prefix_table : own_table, key_of(j) >> a.c.page_shift, there);
         };
         auto byte_at = [&](int page, int j) { return scale_byte(p8, is_v != 0, page, (key_of(j) & mask) / 16, head); };
         int s = 0, issued = 0;
         uint32_t ph = 0;
         int mine = it.tile0 + turn;   // this lane's tile of the batch
-        int page = checked_page(a, entry_at(mine)), next = entry_at(mine + BATCH), byte = byte_at(page, mine);
+        int page = checked_page(a, entry_at(mine)), byte = byte_at(page, mine);
+        Entry next = entry_at(mine + BATCH);
         for (int j0 = it.tile0; ok && j0 < it.tile1; j0 += BATCH, mine += BATCH) {
             const int next_page = checked_page(a, next), next_byte = byte_at(next_page, mine + BATCH);
             const int e = scale_exp(byte);

@@ -3,14 +3,16 @@
 // blocks of 128 keys, two streams, P back through tensor memory, the work dealt
 // the same way) with codes in place of 16-bit values.
 //
-// The tensor core takes fp16.  Four warps load codes from their pages straight
-// into registers, half the bytes of 16-bit values, turn them into fp16, two an
-// instruction, and store them where TMA would have put the 16-bit block; a block
-// and its conversion serve both tiles (256 rows).  A warp has two runs of 16 keys
-// of each K or V block, each in one page, and fetches the next block's into the
-// registers of a run as soon as that is stored.  The softmax's warps scale the
-// rows of q by powers of two and store them as fp16 at the start of an item, when
-// they would wait for S.
+// The tensor core takes fp16.  Four warps copy codes from their pages to places
+// of their own in shared memory (asynchronously, two blocks ahead: a thread reads
+// only what it copied), turn them into fp16, two an instruction, and store them
+// where TMA would have put the 16-bit block; a block and its conversion serve
+// both tiles (256 rows).  A warp has two runs of 16 keys of each K or V block,
+// each in one page.  (Loaded into registers, where one block at a time has room,
+// a block took its latency and its conversion one after the other: 128 rows over
+// 128 Ki keys 540 us.)  The softmax's warps scale the rows of q by powers of two
+// and store them as fp16 before they write an item's results, so that S of the
+// next is there when they have.
 // The scales do not touch the operands: the softmax multiplies the logits of 16
 // keys by the K scale (in the fused product that its argument takes anyway) and
 // adds the V scale's exponent to that argument (attn.cuh), so an element costs
@@ -20,8 +22,9 @@
 // bits): the same tensor-core time as fp16, while P's split costs the softmax
 // four conversions a pair, which run at 16 to 32 a clock (measured: 21 to E4M3).
 //
-// Warps: 0-3 softmax of stream 0, 4-7 of stream 1, 8-11 codes, 12 the products
-// (13-15 only fill the fourth warpgroup).
+// Warps: 0-3 softmax of stream 0, 4-7 of stream 1, 8-11 codes, 12 the products, 13
+// looks the scales up and leaves them in shared memory (14 and 15 only fill the
+// fourth warpgroup).
 #include <algorithm>
 
 #include "attn_tiles.cuh"
@@ -30,26 +33,38 @@ namespace qg {
 namespace attn {
 namespace {
 
-constexpr int kWarpConvert = 8, kWarpMma = 12;
+constexpr int kWarpConvert = 8, kWarpMma = 12, kWarpScales = 13;
 constexpr int kThreads = 512;
 // Registers of a thread: 128 at launch (65536 over 512), then shared out by warpgroup.
 constexpr int kRegsLaunch = 128, kRegsSoftmax = 192, kRegsConvert = 80, kRegsMma = 48;
 static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsMma == 4 * kRegsLaunch, "registers shared out are those of the launch");
 
+// Scales of a block: the K scales of its 16s of keys, the V scales' exponents, and those scales' reciprocals.
+constexpr int kScales = 24, kScaleSlots = 4;
+
 template <int D> struct Cfg {
     static constexpr int HALVES = D / 64;
     static constexpr int HALF = 128 * 128;                 // bytes of 128 rows of 64 values
     static constexpr int TILE = HALVES * HALF;             // a Q tile, a K or a V block, in fp16
-    static constexpr int SLOTS = D == 128 ? 5 : 8;         // ring of K and V blocks
+    static constexpr int SLOTS = D == 128 ? 4 : 8;         // ring of K and V blocks
     static constexpr int OFF_KV = 2 * TILE;
-    static constexpr int OFF_BAR = OFF_KV + SLOTS * TILE;
-    static constexpr int OFF_ML = OFF_BAR + 256;           // (m, l) of stream 1's rows (joining)
+    static constexpr int RAW = KB * D, RAWS = D == 128 ? 2 : 4;   // a block's codes, and blocks in flight
+    static constexpr int OFF_RAW = OFF_KV + SLOTS * TILE;
+    static constexpr int OFF_BAR = OFF_RAW + RAWS * RAW;
+    static constexpr int OFF_ML = OFF_BAR + 512;           // (m, l) of stream 1's rows (joining)
     static constexpr int OFF_BACK = OFF_ML + 128 * 8;      // what stream 0 scaled its rows of Q by, for stream 1
-    static constexpr int SMEM = OFF_BACK + 128;
+    static constexpr int OFF_SCALES = OFF_BACK + 2 * 128;  // of each stream's next blocks
+    static constexpr int SMEM = OFF_SCALES + 2 * kScaleSlots * kScales * 4;
     static_assert(SMEM <= 227 * 1024, "shared memory");
-    // 16 keys of a converting warp: LANES lanes a key with 16 codes each, CHUNKS times ROWS keys; blocks in flight
-    static constexpr int LANES = D / 16, ROWS = 32 / LANES, CHUNKS = 16 / ROWS, DEPTH = D == 128 ? 1 : 2;
+    // 16 keys of a converting warp: LANES lanes a key with 16 codes each, CHUNKS times ROWS keys
+    static constexpr int LANES = D / 16, ROWS = 32 / LANES, CHUNKS = 16 / ROWS;
 };
+
+// 16 bytes from global to shared memory, or zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
 
 template <int D, int KEYS>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -68,9 +83,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto kv_full = [&](int x) { return bars + 96 + 8 * x; };
     auto kv_empty = [&](int x) { return bars + 96 + 8 * (NS + x); };
     const uint32_t products_done = bars + 96 + 16 * NS;   // when the CTA leaves
-    const uint32_t back_full = bars + 104 + 16 * NS;      // a single tile's scalings are in shared memory
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 112 + 16 * NS);
-    static_assert(112 + 16 * NS + 4 <= 256, "barriers");
+    auto back_full = [&](int x) { return bars + 104 + 16 * NS + 8 * x; };   // a single tile's scalings are in shared memory
+    auto scale_full = [&](int s, int x) { return bars + 120 + 16 * NS + 8 * (kScaleSlots * s + x); };
+    auto scale_empty = [&](int s, int x) { return bars + 120 + 16 * NS + 8 * (kScaleSlots * (2 + s) + x); };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 120 + 16 * NS + 32 * kScaleSlots);
+    static_assert(120 + 16 * NS + 32 * kScaleSlots + 4 <= 512, "barriers");
+    float* scales = reinterpret_cast<float*>(smem + C::OFF_SCALES);
     float2* ml1 = reinterpret_cast<float2*>(smem + C::OFF_ML);
     signed char* back0 = reinterpret_cast<signed char*>(smem + C::OFF_BACK);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -84,10 +102,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(p_full(s, 0), 4);
             ptx::mbar_init(p_full(s, 1), 4);
             ptx::mbar_init(o_full(s), 1);
+            ptx::mbar_init(back_full(s), 4);
+            for (int x = 0; x < kScaleSlots; x++) { ptx::mbar_init(scale_full(s, x), 1); ptx::mbar_init(scale_empty(s, x), 4); }
         }
         ptx::mbar_init(join_full, 4);
         ptx::mbar_init(join_empty, 4);
-        ptx::mbar_init(back_full, 4);
         for (int x = 0; x < NS; x++) { ptx::mbar_init(kv_full(x), 4); ptx::mbar_init(kv_empty(x), 1); }
         ptx::fence_mbar_init();
     }
@@ -121,14 +140,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int per = (KEYS & kOwn) ? lay.per : deal.per;   // tokens of a tile
     const int in_page_mask = (1 << a.c.page_shift) - 1;
 
-    // Keys of a block of the item that any row sees, the first key's place, and the table's entry for 16 of them.
-    auto keys_of = [&](int blk) { return blk < it.np ? min(KB, it.prefix - blk * KB) : max(0, min(KB, it.own - (blk - it.np) * KB)); };
-    auto key_of = [&](int blk, int group) { return (blk < it.np ? blk : blk - it.np) * KB + 16 * group; };
-    auto entry_at = [&](int blk, int group) -> int {
-        if (blk >= it.blk1 || 16 * group >= keys_of(blk)) return kNoPage;
-        const int e = key_of(blk, group) >> a.c.page_shift;
-        if (!(KEYS & kOwn) || blk < it.np) return page_entry(a.bt.prefix_table, (it.prefix + in_page_mask) >> a.c.page_shift, e);
-        return page_entry(a.bt.table + (long long)it.b * a.bt.table_ld, a.bt.table_ld, e);
+    // Keys of a block of an item that any row sees, the first key's place, and the table's entry for 16 of them.
+    auto keys_of = [&](const Item& it, int blk) { return blk < it.np ? min(KB, it.prefix - blk * KB) : max(0, min(KB, it.own - (blk - it.np) * KB)); };
+    auto key_of = [&](const Item& it, int blk, int group) { return (blk < it.np ? blk : blk - it.np) * KB + 16 * group; };
+    auto entry_at = [&](const Item& it, int blk, int group) {
+        const bool there = blk < it.blk1 && 16 * group < keys_of(it, blk);
+        const int* table = !(KEYS & kOwn) || blk < it.np ? a.bt.prefix_table : a.bt.table + (long long)it.b * a.bt.table_ld;
+        return table_entry(a, table, key_of(it, blk, group) >> a.c.page_shift, there);
     };
 
     if (warp >= kWarpMma) {
@@ -215,21 +233,52 @@ __global__ void __launch_bounds__(kThreads, 1)
             commit(products_done);
             ok = ptx::mbar_wait(products_done, 0) && ok;
         }
+        if (warp == kWarpScales) {
+            // ------------------------------------------------ scales: lanes 0-7 K, 8-15 the exponents of V, 16-23 reciprocals
+            const int group = lane % 8;
+            int slot[2] = {0, 0};
+            uint32_t round[2] = {1, 1};
+            while (ok && next_item<KEYS>(a, deal, lay, cur, it)) {
+                const int n = it.blk1 - it.blk0;
+                auto byte_at = [&](const Entry& e, int blk) {
+                    return scale_byte(p8, lane >= 8, checked_page(a, e), (key_of(it, blk, group) & in_page_mask) / 16, it.head);
+                };
+                // the table's entries two blocks ahead, scales one
+                Entry next = entry_at(it, it.blk0 + 1, group);
+                int byte = byte_at(entry_at(it, it.blk0, group), it.blk0);
+                for (int j = 0; ok && j < n; j++) {
+                    const int e = scale_exp(byte);
+                    byte = byte_at(next, it.blk0 + j + 1);
+                    next = entry_at(it, it.blk0 + j + 2, group);
+                    const float f = lane < 8 ? kv8::pow2(e) : lane < 16 ? (float)e : kv8::pow2(-e);
+                    for (int s = it.two ? 0 : j & 1; ok && s < (it.two ? 2 : (j & 1) + 1); s++) {
+                        const int x = slot[s & 1];
+                        ok = __all_sync(0xffffffffu, ptx::mbar_wait(scale_empty(s, x), round[s & 1]));
+                        if (!ok) break;
+                        if (lane < kScales) scales[(s * kScaleSlots + x) * kScales + lane] = f;
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(scale_full(s, x));
+                        if (++slot[s & 1] == kScaleSlots) { slot[s & 1] = 0; round[s & 1] ^= 1u; }
+                    }
+                }
+            }
+        }
     } else if (warp >= kWarpConvert) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
         // ------------------------------------------------ codes to fp16: keys 16 w .. and 16 (w + 4) .. of a block
-        const int w = warp - kWarpConvert, row0 = lane / C::LANES, chunk = lane % C::LANES;   // keys row0 + c ROWS, codes 16 chunk ..
-        // where in a slot: the lanes of a row's second half store their later 16 bytes first, so that eight lanes meet all banks
-        const int flip = chunk / 4;
+        // keys row0 + c ROWS, codes 16 chunk ..: eight lanes take two rows' half of 64 values, so that their stores meet all banks
+        const int w = warp - kWarpConvert, chunk = lane % 4 + (D == 128 ? lane / 8 % 2 * 4 : 0);
+        const int row0 = D == 128 ? lane / 4 % 2 + lane / 16 * 2 : lane / 4;
         uint32_t to[2];   // of rows row0 + c ROWS for even, odd c
 #pragma unroll
         for (int c = 0; c < 2; c++) {
             const int row = row0 + c * C::ROWS;
-            to[c] = (uint32_t)(flip * C::HALF + (16 * w + row) * 128 + 16 * ((2 * (chunk % 4) + flip) ^ (row & 7)));
+            to[c] = (uint32_t)(chunk / 4 * C::HALF + (16 * w + row) * 128 + 16 * (2 * (chunk % 4) ^ (row & 7)));
         }
         const int group = w + 4 * (lane & 1);   // the keys whose page this lane looks up
         const long long hop = (long long)C::ROWS * a.c.token_stride;
-        int slot = 0;
+        const uint32_t raw = sbase + C::OFF_RAW + 16 * (threadIdx.x - 32 * kWarpConvert);   // this thread's places
+        int slot = 0, raw_slot = 0;
         uint32_t round = 1;   // parity of the wait for a free slot
         while (ok && next_item<KEYS>(a, deal, lay, cur, it)) {
             const int n = it.blk1 - it.blk0, loads = 2 * n;
@@ -237,10 +286,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // where this lane's 16 keys of a block begin among the codes: of the last block K was loaded for, and the one before;
             // -1: nothing there to load.  The next one's entry of the table is on its way.
             long long now = -1, before = -1;
-            int entry = entry_at(it.blk0, group);
-            uint4 raw[C::DEPTH][2][C::CHUNKS];
+            Entry entry = entry_at(it, it.blk0, group);
             // load number i, in the order K0, K1 V0, K2 V1, ..
-            struct Load { const uint8_t* from; long long at; int left; };
+            struct Load { const uint8_t* from; long long at; int left; };   // left: keys of the block
             auto next_load = [&](int i) -> Load {
                 const bool v = i != 0 && (!(i & 1) || i == loads - 1);
                 const int blk = it.blk0 + (i == loads - 1 ? n - 1 : i == 0 ? 0 : i & 1 ? (i + 1) / 2 : i / 2 - 1);
@@ -248,56 +296,61 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int page = checked_page(a, entry);
                     before = now;
                     now = page >= 0 && page < a.c.num_pages
-                              ? (long long)page * a.c.page_stride + (long long)(key_of(blk, group) & in_page_mask) * a.c.token_stride : -1;
-                    entry = entry_at(blk + 1, group);
+                              ? (long long)page * a.c.page_stride + (long long)(key_of(it, blk, group) & in_page_mask) * a.c.token_stride : -1;
+                    entry = entry_at(it, blk + 1, group);
                 }
-                return Load{v ? p8.v_codes : p8.k_codes, !v || i == loads - 1 ? now : before, keys_of(blk) - 16 * w - row0};
+                return Load{v ? p8.v_codes : p8.k_codes, !v || i == loads - 1 ? now : before, keys_of(it, blk)};
             };
-            auto fetch = [&](const Load& l, auto half, uint4 (&r)[C::CHUNKS]) {
-                const long long at = __shfl_sync(0xffffffffu, l.at, half.value);
-                const uint8_t* p = l.from + at + mine;
+            // a load's codes to this thread's places of a raw block: keys past the last, and pages not to be followed, are zeros
+            auto fetch = [&](int i) {
+                if (i < loads) {
+                    const Load l = next_load(i);
 #pragma unroll
-                for (int c = 0; c < C::CHUNKS; c++) {
-                    // keys past the last, and pages not to be followed, are zeros
-                    r[c] = make_uint4(0u, 0u, 0u, 0u);
-                    if (at >= 0 && 64 * half.value + c * C::ROWS < l.left) r[c] = __ldg(reinterpret_cast<const uint4*>(p + c * hop));
+                    for (int h = 0; h < 2; h++) {
+                        const long long at = __shfl_sync(0xffffffffu, l.at, h);
+                        const uint8_t* p = at >= 0 ? l.from + at + mine : l.from;
+#pragma unroll
+                        for (int c = 0; c < C::CHUNKS; c++) {
+                            const bool there = at >= 0 && 16 * w + row0 + 64 * h + c * C::ROWS < l.left;
+                            copy16(raw + raw_slot * C::RAW + (h * C::CHUNKS + c) * (128 * 16), there ? p + c * hop : l.from, there);
+                        }
+                    }
                 }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                if (++raw_slot == C::RAWS) raw_slot = 0;
             };
-            auto store = [&](unsigned char* into, auto half, const uint4 (&r)[C::CHUNKS]) {
+            raw_slot = 0;
+#pragma unroll 1
+            for (int d = 0; d < C::RAWS; d++) fetch(d);
+#pragma unroll 1
+            for (int i = 0; i < loads; i++) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(C::RAWS - 1) : "memory");
+                uint4 r[2 * C::CHUNKS];
 #pragma unroll
-                for (int c = 0; c < C::CHUNKS; c++) {
-                    const uint4 lo = make_uint4(kv8::decode_lo(r[c].x), kv8::decode_hi(r[c].x), kv8::decode_lo(r[c].y), kv8::decode_hi(r[c].y));
-                    const uint4 hi = make_uint4(kv8::decode_lo(r[c].z), kv8::decode_hi(r[c].z), kv8::decode_lo(r[c].w), kv8::decode_hi(r[c].w));
-                    const uint32_t at = to[c & 1] + (64 * half.value + (c & ~1) * C::ROWS) * 128;
-                    *reinterpret_cast<uint4*>(into + at) = flip ? hi : lo;
-                    *reinterpret_cast<uint4*>(into + (at ^ 16)) = flip ? lo : hi;
-                }
-            };
+                for (int c = 0; c < 2 * C::CHUNKS; c++)
+                    r[c] = *reinterpret_cast<const uint4*>(smem + C::OFF_RAW + raw_slot * C::RAW + c * (128 * 16) + 16 * (threadIdx.x - 32 * kWarpConvert));
+                fetch(i + C::RAWS);   // over what has just been read
+                ok = __all_sync(0xffffffffu, ptx::mbar_wait(kv_empty(slot), round));
+                if (!ok) break;
+                unsigned char* into = smem + C::OFF_KV + slot * C::TILE;
 #pragma unroll
-            for (int d = 0; d < C::DEPTH; d++) {
-                const Load l = d < loads ? next_load(d) : Load{p8.k_codes, -1, 0};
-                fetch(l, Const<0>{}, raw[d][0]);
-                fetch(l, Const<1>{}, raw[d][1]);
+                for (int h = 0; h < 2; h++)
+#pragma unroll
+                    for (int c = 0; c < C::CHUNKS; c++) {
+                        const uint4 x = r[h * C::CHUNKS + c];
+                        const uint32_t at = to[c & 1] + (64 * h + (c & ~1) * C::ROWS) * 128;
+                        *reinterpret_cast<uint4*>(into + at) =
+                            make_uint4(kv8::decode_lo(x.x), kv8::decode_hi(x.x), kv8::decode_lo(x.y), kv8::decode_hi(x.y));
+                        *reinterpret_cast<uint4*>(into + (at ^ 16)) =
+                            make_uint4(kv8::decode_lo(x.z), kv8::decode_hi(x.z), kv8::decode_lo(x.w), kv8::decode_hi(x.w));
+                    }
+                ptx::fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(kv_full(slot));
+                if (++slot == NS) { slot = 0; round ^= 1u; }
             }
-            for (int i0 = 0; ok && i0 < loads; i0 += C::DEPTH) {
-#pragma unroll
-                for (int d = 0; d < C::DEPTH; d++) {
-                    const int i = i0 + d;
-                    if (!ok || i >= loads) break;
-                    const Load l = i + C::DEPTH < loads ? next_load(i + C::DEPTH) : Load{p8.k_codes, -1, 0};
-                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(kv_empty(slot), round));
-                    if (!ok) break;
-                    unsigned char* into = smem + C::OFF_KV + slot * C::TILE;
-                    store(into, Const<0>{}, raw[d][0]);
-                    fetch(l, Const<0>{}, raw[d][0]);
-                    store(into, Const<1>{}, raw[d][1]);
-                    ptx::fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(kv_full(slot));
-                    fetch(l, Const<1>{}, raw[d][1]);
-                    if (++slot == NS) { slot = 0; round ^= 1u; }
-                }
-            }
+            // no copy is in flight when the CTA leaves, or where the next item's go
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -308,26 +361,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = 32 * (warp % 4) + lane;
         const int tok_in_tile = r / a.group;
         uint32_t s_phase = 0, o_phase = 0, join_phase = 0, item_phase = 0;
-        // lanes 0-7 hold the K scales of a block's 16s of keys, 8-15 the V scales' exponents, 16-23 those scales' reciprocals
-        const int group = lane % 8;
-        auto byte_at = [&](int entry, int blk) {
-            return scale_byte(p8, lane >= 8, checked_page(a, entry), (key_of(blk, group) & in_page_mask) / 16, it.head);
-        };
-        auto scale_of = [&](int byte) {
-            const int e = scale_exp(byte);
-            return lane < 8 ? kv8::pow2(e) : lane < 16 ? (float)e : kv8::pow2(-e);
-        };
-        for (; ok && next_item<KEYS>(a, deal, lay, cur, it); item_phase ^= 1u) {
-            const int n = it.blk1 - it.blk0, step = it.two ? 1 : 2;
-            const int tok = it.t0 + (it.two ? s * per : 0) + tok_in_tile;
-            const bool in = tok_in_tile < per && tok < it.t1;
-            float m = -INFINITY, l = 0.0f;
-            const int first = it.two ? 0 : s;
-            // the table's entries two blocks ahead, scales one
-            int entry = entry_at(it.blk0 + first, group), entry_next = entry_at(it.blk0 + first + step, group);
-            int byte = byte_at(entry, it.blk0 + first);
-            float scale = 0.0f;
-            // ------------------------------------------------ the warp's 32 rows of Q; row r's is scaled by 2^-back
+        int slot = 0;          // of the scales
+        uint32_t round = 0;
+        int singles = 0;   // items of a single tile
+        // The warp's 32 rows of an item's Q to shared memory, each scaled by 2^-back: the exponent of this lane's row.  Done
+        // before the last item's results are written, so that S of the new item is there when they are.
+        auto prepare = [&](const Item& it) -> int {
             int back = 0;
             if (it.two || s == 0) {
                 constexpr int QL = D / 8, QROWS = 32 / QL, QN = 32 / QROWS;   // lanes of a row, rows at a time, times
@@ -344,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // the last item's Q is no longer read
                 ok = __all_sync(0xffffffffu, ptx::mbar_wait(q_empty, item_phase ^ 1u));
-                if (!ok) break;
+                if (!ok) return 0;
 #pragma unroll
                 for (int i = 0; i < QN; i++) {
                     const int row = 32 * (warp % 4) + i * QROWS + qr;
@@ -370,27 +409,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ptx::fence_proxy_async();
             }
-            if (!it.two && s == 0) back0[r] = (signed char)back;
+            item_phase ^= 1u;
+            // both streams work on a single tile's rows: stream 0 leaves the exponents in one of two buffers, each written again
+            // only after the streams have met at the end of its item
+            signed char* shared = back0 + 128 * (singles & 1);
+            if (!it.two && s == 0) shared[r] = (signed char)back;
             __syncwarp();
             if (lane == 0) {
                 ptx::mbar_arrive(q_full);
-                if (!it.two && s == 0) ptx::mbar_arrive(back_full);
+                if (!it.two && s == 0) ptx::mbar_arrive(back_full(singles & 1));
             }
-            if (!it.two && s == 1) {   // both streams work on the first tile's rows; stream 0 writes the next after they have met
-                ok = __all_sync(0xffffffffu, ptx::mbar_wait(back_full, join_phase));
-                if (!ok) break;
-                back = back0[r];
+            if (!it.two && s == 1) {
+                ok = __all_sync(0xffffffffu, ptx::mbar_wait(back_full(singles & 1), (singles >> 1) & 1));
+                back = shared[r];
             }
+            if (!it.two) singles++;
+            return back;
+        };
+        bool more = next_item<KEYS>(a, deal, lay, cur, it);
+        int back = more ? prepare(it) : 0;
+        while (ok && more) {
+            const int n = it.blk1 - it.blk0, step = it.two ? 1 : 2;
+            const int tok = it.t0 + (it.two ? s * per : 0) + tok_in_tile;
+            const bool in = tok_in_tile < per && tok < it.t1;
+            float m = -INFINITY, l = 0.0f;
+            const int first = it.two ? 0 : s;
             const float row_scale = a.scale_log2 * kv8::pow2(back);
             // what the logits of 16 keys are multiplied by: at least the smallest normal number, since a masked logit times 0
             // would be a NaN
-            auto factor = [&](int g) { return fmaxf(row_scale * __shfl_sync(0xffffffffu, scale, g), 1.17549435e-38f); };
+            auto factor = [&](float scale) { return fmaxf(row_scale * scale, 1.17549435e-38f); };
             for (int j = first; j < n; j += step) {
                 const int blk = it.blk0 + j;
                 const int vis = blk < it.np ? it.prefix - blk * KB : it.own0 + (tok - it.t0) - (blk - it.np) * KB;
-                scale = scale_of(byte);
-                byte = byte_at(entry_next, blk + step);
-                entry_next = entry_at(blk + 2 * step, group);
+                const float* sc = scales + (s * kScaleSlots + slot) * kScales;
+                ok = __all_sync(0xffffffffu, ptx::mbar_wait(scale_full(s, slot), round));
+                if (!ok) break;
                 ok = __all_sync(0xffffffffu, ptx::mbar_wait(s_full(s), s_phase));
                 s_phase ^= 1u;
                 if (!ok) break;
@@ -416,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         u = fmaxf(fmaxf(u, __uint_as_float(y[e])), __uint_as_float(y[e + 1]));
                         v = fmaxf(fmaxf(v, __uint_as_float(y[e + 2])), __uint_as_float(y[e + 3]));
                     }
-                    t = fmaxf(t, fmaf(fmaxf(u, v), factor(g), __shfl_sync(0xffffffffu, scale, 8 + g)));
+                    t = fmaxf(t, fmaf(fmaxf(u, v), factor(sc[g]), sc[8 + g]));
                 }
                 const bool raise = t > m + kRaise || (m == -INFINITY && t > -INFINITY);
                 if (__any_sync(0xffffffffu, raise)) {
@@ -445,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int q = 0; q < 2; q++) {
                             const int g = 2 * c + q;
-                            const float f = factor(g), add = __shfl_sync(0xffffffffu, scale, 8 + g) - u;
+                            const float f = factor(sc[g]), add = sc[8 + g] - u;
                             const float2 f2 = make_float2(f, f), c2 = make_float2(add, add);
                             float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
@@ -456,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 p[e] = kv::pack2<__half>(z.x, z.y);
                             }
                             sum[0] = add2(sum[0], sum[1]);
-                            l = fmaf(sum[0].x + sum[0].y, __shfl_sync(0xffffffffu, scale, 16 + g), l);
+                            l = fmaf(sum[0].x + sum[0].y, sc[16 + g], l);
                         }
                         tmem_st16(t_s + 16 * c, p);
                     }
@@ -465,7 +518,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(p_full(s, h));
                 }
+                if (lane == 0) ptx::mbar_arrive(scale_empty(s, slot));
+                if (++slot == kScaleSlots) { slot = 0; round ^= 1u; }
             }
+            if (!ok) break;
+            Item next;
+            more = next_item<KEYS>(a, deal, lay, cur, next);
+            if (more) back = prepare(next);
             if (!ok) break;
             // ------------------------------------------------ the item's rows
             const bool ran = n > first;
@@ -550,6 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 join_phase ^= 1u;
             }
+            it = next;
         }
     }
     if (!ok && a.status) atomicExch(a.status, (int)QG_ERR_TIMEOUT);
