@@ -139,11 +139,16 @@ int choose_ctas(const Shape& c, const qg_kv_batch& b, int64_t group, int64_t own
     return best;
 }
 
+// Blocks that an item of the 8-bit tile kernel counts for beyond its own when the line of prompts is dealt: its lookups,
+// Q and results are not hidden behind another's.
+constexpr int kExtra8 = 5;
+
 // The line of prompts is counted in 32 bits.
 bool line_fits(const Shape& c, const qg_kv_batch& b, int64_t per2)
 {
     const int64_t pairs = b.tokens / per2 + b.sequences;
-    return pairs * (ceil_div(b.prefix_len, kBlock) + ceil_div(b.max_kv, kBlock) + 1) < ((int64_t)1 << 30) / c.heads_kv;
+    return pairs * (ceil_div(b.prefix_len, kBlock) + ceil_div(b.max_kv, kBlock) + 1 + (c.bytes == 1 ? kExtra8 : 0)) <
+           ((int64_t)1 << 30) / c.heads_kv;
 }
 
 Plan make_plan(const Shape& c, const qg_kv_batch& b, int heads_q)
@@ -461,11 +466,11 @@ attn::Args make_args(const kv::Cache& c, const qg_kv_batch& batch, const void* q
     return a;
 }
 
-attn::Layout make_layout(const attn::Plan& p, const attn::Places& w, char* ws, int group)
+attn::Layout make_layout(const attn::Plan& p, const attn::Places& w, char* ws, int group, int extra)
 {
     return attn::Layout{reinterpret_cast<attn::Line*>(ws + w.line), reinterpret_cast<int*>(ws + w.first),
                         reinterpret_cast<attn::Pair*>(ws + w.pair), reinterpret_cast<int*>(ws + w.cut),
-                        attn::tile_tokens(group), p.ctas, (int)p.pairs};
+                        attn::tile_tokens(group), p.ctas, (int)p.pairs, extra};
 }
 
 }  // namespace
@@ -497,7 +502,7 @@ qg_status launch_attn(const qg_kv_cache& cache, const qg_kv_batch& batch, const 
         if (st == QG_OK) st = attn::encode_pages(&vmap, cache, cache.v, a.box_rows, false);
         if (st != QG_OK) return st;
         if (p.way == attn::kPrompts) {
-            const attn::Layout lay = make_layout(p, w, base, a.group);
+            const attn::Layout lay = make_layout(p, w, base, a.group, 0);
             e = attn::launch_tiles(a, cache.dtype, qmap, kmap, vmap, lay, s);
             if (e == cudaSuccess) e = attn::launch_join_line(a, lay, s);
         } else {
@@ -534,7 +539,7 @@ qg_status launch_attn8(const qg_kv8_cache& cache, const qg_kv_batch& batch, cons
                   c.scale_page, c.scale_block, c.scale_head, qt};
     cudaError_t e = cudaSuccess;
     if (p.way == attn::kPrompts) {
-        const attn::Layout lay = make_layout(p, w, base, a.a.group);
+        const attn::Layout lay = make_layout(p, w, base, a.a.group, attn::kExtra8);
         e = attn::launch_layout(a.a, lay, s);
         if (e == cudaSuccess) e = attn::launch_tiles8(a, lay, s);
         if (e == cudaSuccess) e = attn::launch_join_line(a.a, lay, s);

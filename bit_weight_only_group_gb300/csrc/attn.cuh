@@ -238,6 +238,7 @@ struct Layout {
     int per;                  // tokens of a tile
     int ctas;
     int max_pairs;            // entries of `pair` but one
+    int extra;                // blocks that an item's start and end count for, before its first
     // slot of piece p of an item that starts in the run of CTA c
     __host__ __device__ int slot(int c, int p) const { return p == 0 ? 2 * c + 1 : 2 * (c + p); }
 };

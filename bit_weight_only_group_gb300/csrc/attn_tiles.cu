@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(1024) k_attn_layout(const __grid_constant__ Ar
             if (!kv::own_length(a.bt, p.b, len)) kv::report(a.status);
             p.t0 = t0 + (i - lay.first[p.b]) * per2;
             const int own = len - (t1 - min(p.t0 + per2, t1));   // own tokens the pair's last token sees
-            n = max(1, np + (max(0, own) + KB - 1) / KB);        // 1: a pair that sees nothing is still written
+            n = lay.extra + max(1, np + (max(0, own) + KB - 1) / KB);   // 1: a pair that sees nothing is still written
         }
         const int upto = block_sums(n, scratch, total);
         p.start = blocks + upto - n;

@@ -178,7 +178,7 @@ __device__ __forceinline__ bool next_item(const Args& a, const Deal& d, const La
         it.head = cur.head;
         const int at = cur.i - it.head * line.head, lo = cur.pair;
         const Pair p = lay.pair[lo];
-        const int blocks = lay.pair[lo + 1].start - p.start, first = it.head * line.head + p.start;
+        const int blocks = lay.pair[lo + 1].start - p.start, first = it.head * line.head + p.start;   // with the extra ones
         int t0;
         it.b = p.b;
         it.t0 = p.t0;
@@ -188,12 +188,13 @@ __device__ __forceinline__ bool next_item(const Args& a, const Deal& d, const La
         kv::own_length(a.bt, p.b, len);   // the layout kernel has reported what is outside its bounds
         it.own0 = len - (it.t1 - it.t0) + 1;
         it.own = max(0, it.own0 + min(2 * lay.per, it.t1 - it.t0) - 1);
-        it.blk0 = at - p.start;
-        it.blk1 = min(blocks, it.blk0 + end - cur.i);
+        const int u0 = at - p.start, u1 = min(blocks, u0 + end - cur.i);
+        it.blk0 = max(0, u0 - lay.extra);
+        it.blk1 = max(0, u1 - lay.extra);   // blk0 where the run ends among the extra ones: the piece is written as having seen nothing
         const int from = first / line.run;   // the CTA whose run the item starts in
         it.part = lay.slot(from, (int)blockIdx.x - from);
-        it.whole = it.blk0 == 0 && it.blk1 == blocks;
-        cur.i += it.blk1 - it.blk0;
+        it.whole = u0 == 0 && u1 == blocks;
+        cur.i += u1 - u0;
         if (++cur.pair == line.pairs) {
             cur.pair = 0;
             cur.head++;
