@@ -94,10 +94,15 @@ double own_time(const Shape& c, const qg_kv_batch& b, int64_t group)
 
 // Microseconds the tile kernel takes on an SM for a block and so many tiles:
 // 1.35 for a pair, 1.2 for a single tile (bound by its loads), two thirds of
-// that with 64-wide heads.
+// that with 64-wide heads.  The 8-bit kernel's conversions make it 1.6 times as
+// long in these terms (2.0 us a block measured alone, 128 rows over 128 Ki keys;
+// 256 sequences over 8192 + 1024 keys 184 us with the 16-bit figure, 162 with
+// this one), and no shorter with 64-wide heads, whose blocks take it as many
+// steps (48 of 5 drafted tokens 51 us at two thirds, 45 at 112 to 152 CTAs).
 double block_time(const Shape& c, int64_t tiles)
 {
-    return (c.head_dim == 128 ? 1.0 : 0.67) * ((double)(tiles / 2) * 1.35 + (double)(tiles % 2) * 1.2);
+    const double each = c.bytes == 1 ? (c.head_dim == 128 ? 1.6 : 2.0) : c.head_dim == 128 ? 1.0 : 0.67;
+    return each * ((double)(tiles / 2) * 1.35 + (double)(tiles % 2) * 1.2);
 }
 
 // CTAs (one an SM) for the shared prefix, so that the own tokens' kernel, which
@@ -140,8 +145,9 @@ int choose_ctas(const Shape& c, const qg_kv_batch& b, int64_t group, int64_t own
 }
 
 // Blocks that an item of the 8-bit tile kernel counts for beyond its own when the line of prompts is dealt: its lookups,
-// Q and results are not hidden behind another's.
-constexpr int kExtra8 = 5;
+// Q and results are not hidden behind another's, and the CTAs that start with the short items of a prompt's head would end
+// last (a prompt of 8192 tokens: 1336 us with none, 997 with 5, 993 with 8, 1019 with 12; of 2048 221, 144, 139, 149).
+constexpr int kExtra8 = 8;
 
 // The line of prompts is counted in 32 bits.
 bool line_fits(const Shape& c, const qg_kv_batch& b, int64_t per2)
