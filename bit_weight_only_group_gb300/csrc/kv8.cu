@@ -55,7 +55,7 @@ __device__ __forceinline__ long long scale_at(const Cache& c, const Unit& x, int
 
 // SINGLE: at most one new token a sequence; a warp's rows are then heads, else places of the block.
 template <typename TI, int D, bool SINGLE>
-__global__ void __launch_bounds__(kThreads, 2) k_kv8_append(const __grid_constant__ AppendArgs a)
+__global__ void __launch_bounds__(kThreads, D == 64 ? 3 : 2) k_kv8_append(const __grid_constant__ AppendArgs a)
 {
     constexpr int LANES = D / 16, ROWS = 32 / LANES, ITER = SINGLE ? 1 : kBlock / ROWS;
     constexpr int HEADS = SINGLE ? ROWS : 1;                 // heads of a warp at a time
