@@ -91,10 +91,25 @@ __device__ __forceinline__ float norm_weight(const Norm& n, bool key, int i)
     return __half2float(static_cast<const __half*>(p)[i]);
 }
 
-// x w / sqrt(mean x^2 + eps) over a head of D values, 16 a lane (runs i0 and i1) over LANES neighbouring lanes; lanes of
-// other heads need not take part.
+// The weights of both norms in shared memory as the lanes of a head read them, 16 bytes at a time without a conflict:
+// [queries, keys][quarter of a lane's 16 weights][lane][4], the lane's two runs of 8 where the rotation wants them (rot 0:
+// there is none).  (In the order of the head eight lanes met four banks: 8192 tokens 73.4 us, 69 to 71 so.)  By at least 32 LANES
+// threads.
+template <int LANES>
+__device__ __forceinline__ void stage_weights(float4* w, const Norm& n, int rot, bool interleaved)
+{
+    const int t = threadIdx.x;
+    if (t >= 32 * LANES) return;
+    const int j = t / 4 % LANES, c = t / (4 * LANES) % 4;
+    const bool apart = j < rot / 16 && !interleaved;
+    const int run = c < 2 ? (apart ? 8 * j : 16 * j) : (apart ? rot / 2 + 8 * j : 16 * j + 8);
+    reinterpret_cast<float*>(w)[t] = norm_weight(n, t >= 16 * LANES, run + 4 * (c & 1) + t % 4);
+}
+
+// x w / sqrt(mean x^2 + eps) over a head of D values, 16 a lane over LANES neighbouring lanes; lanes of other heads need
+// not take part.  w: the lane's staged weights, LANES apart.
 template <int LANES, int D>
-__device__ __forceinline__ void norm_head(float (&f0)[8], float (&f1)[8], const float* w, int i0, int i1, float eps)
+__device__ __forceinline__ void norm_head(float (&f0)[8], float (&f1)[8], const float4* w, float eps)
 {
     const uint32_t mask = ((1u << LANES) - 1u) << (threadIdx.x % 32 / LANES * LANES);
     float s0 = 0.0f, s1 = 0.0f;
@@ -109,7 +124,7 @@ __device__ __forceinline__ void norm_head(float (&f0)[8], float (&f1)[8], const 
     const float r = rsqrtf(fmaf(s0, 1.0f / D, eps));
 #pragma unroll
     for (int i = 0; i < 8; i += 4) {
-        const float4 a = *reinterpret_cast<const float4*>(w + i0 + i), b = *reinterpret_cast<const float4*>(w + i1 + i);
+        const float4 a = w[i / 4 * LANES], b = w[(2 + i / 4) * LANES];
         f0[i] *= r * a.x; f0[i + 1] *= r * a.y; f0[i + 2] *= r * a.z; f0[i + 3] *= r * a.w;
         f1[i] *= r * b.x; f1[i + 1] *= r * b.y; f1[i + 2] *= r * b.z; f1[i + 3] *= r * b.w;
     }
