@@ -18,7 +18,6 @@ constexpr int kBlock = 128;   // keys of a block of the tile kernel
 struct Shape {
     int heads_kv, head_dim;
     int bytes;      // of a value
-    bool tiles;     // there is a tile kernel for it
 };
 
 // How a call is run.
@@ -96,7 +95,7 @@ double own_time(const Shape& c, const qg_kv_batch& b, int64_t group)
 // 1.35 for a pair, 1.2 for a single tile (bound by its loads), two thirds of
 // that with 64-wide heads.  The 8-bit kernel's conversions make it 1.6 times as
 // long in these terms (2.0 us a block measured alone, 128 rows over 128 Ki keys;
-// 256 sequences over 8192 + 1024 keys 184 us with the 16-bit figure, 162 with
+// 256 sequences over 8192 + 1024 keys 178 us with the 16-bit figure, 162 with
 // this one), and no shorter with 64-wide heads, whose blocks take it as many
 // steps (48 of 5 drafted tokens 51 us at two thirds, 45 at 112 to 152 CTAs).
 double block_time(const Shape& c, int64_t tiles)
@@ -165,7 +164,7 @@ Plan make_plan(const Shape& c, const qg_kv_batch& b, int heads_q)
     const int64_t np = ceil_div(b.prefix_len, kBlock), no = ceil_div(b.max_kv, kBlock);
     const int64_t prefix_tiles = ceil_div(b.prefix_len, kTile), own_tiles = ceil_div(b.max_kv, kTile);
     const int64_t own_units = (int64_t)b.sequences * c.heads_kv * ceil_div(group * b.max_q, 64);
-    const bool tiles = c.tiles && group <= 128;   // a tile holds whole tokens
+    const bool tiles = group <= 128;   // a tile holds whole tokens
     const bool share = b.sequences > 1 && b.prefix_len >= 256;
     p.way = share ? kTilesShared : kAlone;
     if (share) {
@@ -452,8 +451,8 @@ qg_status encode_rows(CUtensorMap* map, int dtype, const void* q, int dim, int h
 
 namespace {
 
-attn::Shape shape_of(const qg_kv_cache& c) { return attn::Shape{c.heads_kv, c.head_dim, 2, true}; }
-attn::Shape shape_of(const qg_kv8_cache& c) { return attn::Shape{c.heads_kv, c.head_dim, 1, true}; }
+attn::Shape shape_of(const qg_kv_cache& c) { return attn::Shape{c.heads_kv, c.head_dim, 2}; }
+attn::Shape shape_of(const qg_kv8_cache& c) { return attn::Shape{c.heads_kv, c.head_dim, 1}; }
 
 attn::Args make_args(const kv::Cache& c, const qg_kv_batch& batch, const void* q, int64_t ldq, int heads_q, float scale,
                      void* out, int64_t ldo, int ot, float* lse, char* ws, const attn::Places& w)

@@ -15,8 +15,8 @@
 // read twice.  The unit's cosines and sines are staged in shared memory, once
 // for all heads.  With one new token a sequence the rows of a warp are heads.
 // Appending and reading back: one token into 40 8.2 us, 256 into sequences of up
-// to 512 (16 heads of 128 read back, 404 MB in all) 84.9 us, 4.9 TB/s; prompts of
-// 4000 tokens of 32 + 2 x 8 heads of 64 28.6 us (72 MB), two launches whose CTAs
+// to 512 (16 heads of 128 read back, 416 MB in all) 84.9 us, 4.9 TB/s; prompts of
+// 4200 tokens of 32 + 2 x 8 heads of 64 28.6 us (72 MB), two launches whose CTAs
 // wait for offsets, lengths, table and data one after another.
 #include <algorithm>
 
